@@ -292,12 +292,146 @@ int dmuon_newton_schulz_noalloc(const float* input, float* output,
                                 const float* coeffs, float eps,
                                 int sync_status, void* stream);
 
+/* Element types of the operators below. */
+#define DMUON_F32  0
+#define DMUON_BF16 1
+#define DMUON_F16  2
+
+/*
+ * MXFP4 matrices: the 4-bit operands of a projection whose weights the Muon
+ * step trains (OCP microscaling: along a row, blocks of 32 E2M1 elements
+ * {0, 1/2, 1, 3/2, 2, 3, 4, 6} with a sign, one E8M0 scale 2^e a block, stored
+ * as e + 127; byte 255 = NaN).  A matrix of rows x k is two device buffers,
+ * 16-byte aligned, of the sizes dmuon_mxfp4_bytes gives:
+ *   data    row-major, pitch 16 * ceil(k / 32) bytes; element 2i in the low
+ *           half of byte i, 2i + 1 in the high half; elements past k zero
+ *   scales  tiles of 128 rows x 4 blocks (512 bytes), row-major: row r, block
+ *           j of a tile at (r % 32) * 16 + (r / 32) * 4 + j; bytes past the
+ *           matrix zero
+ * Sides up to 2^30.  The products contract over k, along which both operands
+ * are quantised: a weight W [out, in] is quantised by rows for the forward
+ * product X W^T and by columns for the input gradient dY W; X and dY by
+ * columns for the weight gradient dY^T X.
+ */
+int dmuon_mxfp4_bytes(int64_t rows, int64_t k, size_t* data_bytes,
+                      size_t* scale_bytes);
+
+/* How a block's exponent follows its largest magnitude amax (clamped to
+ * [-127, 127]; a zero block takes -127). */
+#define DMUON_MXFP4_SCALE_FLOOR 0  /* floor(log2 amax) - 2 (OCP): values in
+                                    * (6, 8) * 2^e saturate to 6 * 2^e        */
+#define DMUON_MXFP4_SCALE_CEIL  1  /* least e with amax <= 6 * 2^e: nothing
+                                    * saturates, as stochastic rounding wants */
+
+/*
+ * Quantise src (device, rows x cols of `dtype`, row-major with leading
+ * dimension ld >= cols elements, aligned to its element) by rows into
+ * (row_data, row_scales), a rows x cols MXFP4 matrix, and / or by columns into
+ * (col_data, col_scales), a cols x rows one (the transpose, quantised along
+ * src's columns); a pair of NULLs leaves a direction out.  Both directions
+ * read src once.
+ *   noise  NULL: to the nearest value, ties to the even code.  Else device
+ *          bytes, rows x cols with leading dimension noise_ld, uniformly
+ *          random: stochastic rounding, up exactly when 256 times the
+ *          fraction of the way to the next value exceeds byte + 1/2.  Both
+ *          directions use an element's own byte.
+ * A block that holds Inf or NaN gets the NaN scale (and codes 0): it reads
+ * back as NaN and makes the products of its row NaN.  The buffers are written
+ * whole, padding included.  rows == 0 or cols == 0 returns DMUON_OK.
+ * Asynchronous on `stream`, as the calls below.
+ */
+int dmuon_mxfp4_quantize(dmuon_handle_t h, const void* src, int dtype,
+                         int64_t rows, int64_t cols, int64_t ld,
+                         int scale_mode, const uint8_t* noise,
+                         int64_t noise_ld, void* row_data, void* row_scales,
+                         void* col_data, void* col_scales, void* stream);
+
+/* The values of a rows x k MXFP4 matrix into dst (device, `dtype`, leading
+ * dimension ld >= k elements): exact in fp32 and bf16, rounded to nearest in
+ * fp16 where 2^e is outside its range. */
+int dmuon_mxfp4_dequantize(dmuon_handle_t h, const void* data,
+                           const void* scales, int64_t rows, int64_t k,
+                           void* dst, int dtype, int64_t ld, void* stream);
+
+/*
+ * D = alpha * A B^T + beta * D with A m x k and B n x k in MXFP4 and D device,
+ * m x n of `dtype`, leading dimension ldd >= n elements.  fp32 accumulation,
+ * one rounding at the store; beta == 0 does not read D.  DMUON_F32 with
+ * beta = 1 accumulates a weight gradient that dmuon_step takes as G.  Any
+ * m, n >= 0 (0 returns DMUON_OK), k >= 1.  The same inputs give the same bits.
+ * A wait that runs out inside the kernel is reported by dmuon_get_status as
+ * DMUON_ERR_TIMEOUT.
+ */
+int dmuon_mxfp4_gemm(dmuon_handle_t h, const void* a_data,
+                     const void* a_scales, const void* b_data,
+                     const void* b_scales, int64_t m, int64_t n, int64_t k,
+                     void* d, int dtype, int64_t ldd, float alpha, float beta,
+                     void* stream);
+
+/*
+ * The norms after a block and before the next one, with the block's gate and
+ * the residual scale.  Per row, with x the residual stream, f the block's
+ * output and g the gate of the row's group (row / rows_per_gate):
+ *   y = res_scale * x + g * rms(f) * post_w,   h = rms(y) * pre_w
+ *   rms(v) = v / sqrt(mean(v^2) + eps)
+ * y (the next residual stream) and h (the next block's input) are rounded once
+ * to `dtype`, h from y before its rounding.  x, f, y, h are rows x cols of
+ * `dtype`, each with its leading dimension (elements, >= cols) and aligned to
+ * its element; weights, gate and res_scale are fp32, contiguous.
+ */
+typedef struct {
+    int64_t rows, cols;
+    int     dtype;           /* of x, f, y, h and their gradients          */
+    float   eps;
+    const void* x;  int64_t ldx;
+    const void* f;  int64_t ldf;
+    const float* post_w;     /* cols                                       */
+    const float* pre_w;      /* cols                                       */
+    const float* gate;       /* ceil(rows / rows_per_gate) x cols, or NULL
+                              * (1)                                        */
+    int64_t rows_per_gate;   /* >= 1: rows for one gate for all, 1 for a
+                              * gate of every row                          */
+    const float* res_scale;  /* cols, or NULL (1)                          */
+    void* y;        int64_t ldy;
+    void* h;        int64_t ldh;
+    float* rstd;             /* 2 x rows: 1 / sqrt(mean(.^2) + eps) of f,
+                              * then of y; what the backward needs         */
+} dmuon_block_norm_t;
+
+int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p,
+                             void* stream);
+
+/*
+ * Its backward: from dh (gradient of h) and dy (gradient of y from its other
+ * uses, NULL = 0) the gradients of x and f and, in fp32, those of post_w,
+ * pre_w, gate and res_scale (written, not added).  Takes p's x (only for
+ * d_res_scale), f, y and rstd as the forward left them; p->h and p->eps are
+ * not used.  Column sums run in a fixed order: the same inputs give the same
+ * bits.  rows == 0 writes zero weight gradients.  The first call of a larger
+ * size allocates workspace (synchronous; DMUON_ERR_ARG while `stream` is being
+ * captured).
+ */
+typedef struct {
+    const void* dy; int64_t lddy;
+    const void* dh; int64_t lddh;
+    void* dx;       int64_t lddx;
+    void* df;       int64_t lddf;
+    float* d_post_w;
+    float* d_pre_w;
+    float* d_gate;           /* as gate, or NULL (not wanted)              */
+    float* d_res_scale;      /* cols, or NULL (not wanted)                 */
+} dmuon_block_norm_grad_t;
+
+int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p,
+                              const dmuon_block_norm_grad_t* q, void* stream);
+
 /*
  * Wait for the handle's stream work to finish and report what the kernels
  * recorded since the previous call of this function: per-matrix flags of
  * the last planned list (bit 0: non-finite input) are copied to
  * flags[0..min(n_flags, n_mats)) when flags != NULL, then cleared.
- * Returns DMUON_ERR_TIMEOUT if a kernel's bounded wait ran out,
+ * Returns DMUON_ERR_TIMEOUT if a kernel's bounded wait ran out (a wait of
+ * dmuon_mxfp4_gemm too),
  * DMUON_ERR_NONFINITE if any flag is set, DMUON_OK otherwise.
  */
 int dmuon_get_status(dmuon_handle_t h, int* flags, int n_flags);
@@ -419,7 +553,12 @@ int64_t dmuon_launch_count(dmuon_handle_t h);
 #define DMUON_KIND_GS_PROD  10  /* Gram backend: m x m window products     */
 #define DMUON_KIND_NS_FUSED 11  /* direct backend: every product of every
                                  * iteration of a chunk in one launch       */
-#define DMUON_NUM_KINDS     12
+#define DMUON_KIND_MX_QUANTIZE   12
+#define DMUON_KIND_MX_DEQUANTIZE 13
+#define DMUON_KIND_MX_GEMM       14
+#define DMUON_KIND_NORM_FWD      15
+#define DMUON_KIND_NORM_BWD      16  /* both launches                      */
+#define DMUON_NUM_KINDS     17
 int dmuon_profile_enable(dmuon_handle_t h, int on);
 int dmuon_profile_read(dmuon_handle_t h, double* ms, int64_t* count,
                        int n_kinds);

@@ -20,6 +20,8 @@ __all__ = [
     "dmuon_adamw_step", "dmuon_adamw_step_ptrs", "dmuon_clip_grad_norm", "dmuon_clip_grad_norm_ptrs",
     "dmuon_workspace_bytes", "dmuon_polar_express_coefficients", "dmuon_gram_check_coefficients",
     "dmuon_plan_preview",
+    "dmuon_mxfp4_bytes", "dmuon_mxfp4_empty", "dmuon_mxfp4_quantize", "dmuon_mxfp4_dequantize", "dmuon_mxfp4_gemm",
+    "dmuon_block_norm_forward", "dmuon_block_norm_backward",
     "dmuon_launch_count", "dmuon_last_error", "dmuon_profile_enable", "dmuon_profile_read",
     "dmuon_plan_summary", "dmuon_error_string", "dmuon_version", "Handle",
     "KIND_NAMES", "STATUS",
@@ -35,7 +37,7 @@ STATUS = {
     -7: "DMUON_ERR_UNSUPPORTED",
 }
 KIND_NAMES = ("momentum", "finalize", "gram", "gram2", "apply", "update0", "adamw", "clip", "small",
-              "gs_gram", "gs_prod", "ns_fused")
+              "gs_gram", "gs_prod", "ns_fused", "mx_quantize", "mx_dequantize", "mx_gemm", "norm_fwd", "norm_bwd")
 
 
 class DmuonError(RuntimeError):
@@ -58,7 +60,25 @@ class Opts(ctypes.Structure):
                 ("restarts", ctypes.POINTER(ctypes.c_int)), ("n_restarts", ctypes.c_int)]
 
 
+class BlockNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("f", ctypes.c_void_p), ("ldf", ctypes.c_int64),
+                ("post_w", ctypes.c_void_p), ("pre_w", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("rows_per_gate", ctypes.c_int64), ("res_scale", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("rstd", ctypes.c_void_p)]
+
+
+class BlockNormGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("df", ctypes.c_void_p), ("lddf", ctypes.c_int64),
+                ("d_post_w", ctypes.c_void_p), ("d_pre_w", ctypes.c_void_p), ("d_gate", ctypes.c_void_p),
+                ("d_res_scale", ctypes.c_void_p)]
+
+
 BACKENDS = {"direct": 0, "gram": 1}
+SCALE_MODES = {"floor": 0, "ceil": 1}
+_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1, "torch.float16": 2}
 
 
 def lib_path():
@@ -147,6 +167,19 @@ def load(path=None):
     L.dmuon_gram_check_coefficients.argtypes = [i32, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int),
                                                 i32, ctypes.c_char_p, ctypes.c_size_t]
     L.dmuon_gram_check_coefficients.restype = i32
+    sz = ctypes.POINTER(ctypes.c_size_t)
+    L.dmuon_mxfp4_bytes.argtypes = [i64, i64, sz, sz]
+    L.dmuon_mxfp4_bytes.restype = i32
+    L.dmuon_mxfp4_quantize.argtypes = [vp, vp, i32, i64, i64, i64, i32, vp, i64, vp, vp, vp, vp, vp]
+    L.dmuon_mxfp4_quantize.restype = i32
+    L.dmuon_mxfp4_dequantize.argtypes = [vp, vp, vp, i64, i64, vp, i32, i64, vp]
+    L.dmuon_mxfp4_dequantize.restype = i32
+    L.dmuon_mxfp4_gemm.argtypes = [vp, vp, vp, vp, vp, i64, i64, i64, vp, i32, i64, f32, f32, vp]
+    L.dmuon_mxfp4_gemm.restype = i32
+    L.dmuon_block_norm_forward.argtypes = [vp, ctypes.POINTER(BlockNorm), vp]
+    L.dmuon_block_norm_forward.restype = i32
+    L.dmuon_block_norm_backward.argtypes = [vp, ctypes.POINTER(BlockNorm), ctypes.POINTER(BlockNormGrad), vp]
+    L.dmuon_block_norm_backward.restype = i32
     _lib = L
     return L
 
@@ -420,6 +453,157 @@ def dmuon_clip_grad_norm(h, grads, max_norm, buckets=None, n_buckets=None, stats
     return norms, coefs
 
 
+# ------------------------------------------- 4-bit projections and their norms
+
+def _matrix(t, name, dtype=None, shape=None):
+    """(pointer, leading dimension, type code) of a 2-D CUDA tensor whose rows
+    are contiguous; ``dtype`` and ``shape``, where given, have to match."""
+    code = _DTYPES.get(str(t.dtype))
+    if code is None or not t.is_cuda or t.dim() != 2 or (dtype is not None and code != dtype):
+        raise ValueError("%s: a 2-D CUDA tensor of float32, bfloat16 or float16%s is wanted"
+                         % (name, "" if dtype is None else " (the type of the others)"))
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError("%s: shape %s, %s wanted" % (name, (rows, cols), shape))
+    ld, inner = t.stride()
+    if cols > 1 and inner != 1 or rows > 1 and ld < cols:
+        raise ValueError("%s: rows must be contiguous and not overlap" % name)
+    return t.data_ptr(), (ld if rows > 1 else max(ld, cols)), code
+
+
+def _floats(t, name, shape):
+    """Pointer of a contiguous fp32 CUDA tensor of ``shape``; None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda or str(t.dtype) != "torch.float32" or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError("%s: a contiguous float32 CUDA tensor of shape %s is wanted" % (name, shape))
+    return t.data_ptr()
+
+
+def _mxfp4(q, name, rows, k):
+    """(data pointer, scales pointer) of an MXFP4 matrix (data, scales)."""
+    data, scales = q
+    nb = -(-k // 32)
+    for t, want in ((data, rows * nb * 16), (scales, -(-rows // 128) * -(-nb // 4) * 512)):
+        if not t.is_cuda or str(t.dtype) != "torch.uint8" or not t.is_contiguous() or t.numel() != want:
+            raise ValueError("%s: contiguous uint8 CUDA tensors of the sizes dmuon_mxfp4_empty(%d, %d) gives are wanted"
+                             % (name, rows, k))
+    return data.data_ptr(), scales.data_ptr()
+
+
+def dmuon_mxfp4_bytes(rows, k):
+    """(data bytes, scale bytes) of a rows x k MXFP4 matrix (host only)."""
+    d, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().dmuon_mxfp4_bytes(int(rows), int(k), ctypes.byref(d), ctypes.byref(s)), "dmuon_mxfp4_bytes")
+    return d.value, s.value
+
+
+def dmuon_mxfp4_empty(rows, k, device="cuda"):
+    """Uninitialised buffers (data, scales) of a rows x k MXFP4 matrix."""
+    import torch
+    d, s = dmuon_mxfp4_bytes(rows, k)
+    return (torch.empty((rows, d // max(1, rows)), dtype=torch.uint8, device=device),
+            torch.empty(s, dtype=torch.uint8, device=device))
+
+
+def dmuon_mxfp4_quantize(h, src, by_rows=None, by_cols=None, noise=None, scale="floor", stream=None):
+    """Quantise the matrix ``src`` [r, c] along its rows into ``by_rows`` (an
+    r x c MXFP4 matrix) and / or along its columns into ``by_cols`` (c x r).
+    ``noise``: uint8 [r, c] of random bytes for stochastic rounding."""
+    ptr, ld, code = _matrix(src, "src")
+    r, c = src.shape
+    nptr, nld = None, 0
+    if noise is not None:
+        if not noise.is_cuda or str(noise.dtype) != "torch.uint8" or noise.shape != src.shape:
+            raise ValueError("noise: a uint8 CUDA tensor of src's shape is wanted")
+        nld, inner = noise.stride()
+        if c > 1 and inner != 1 or r > 1 and nld < c:
+            raise ValueError("noise: rows must be contiguous and not overlap")
+        nptr, nld = noise.data_ptr(), nld if r > 1 else max(nld, c)
+    rd, rs = (None, None) if by_rows is None else _mxfp4(by_rows, "by_rows", r, c)
+    cd, cs = (None, None) if by_cols is None else _mxfp4(by_cols, "by_cols", c, r)
+    if r == 0 or c == 0:
+        return
+    _check(load().dmuon_mxfp4_quantize(h, ptr, code, r, c, ld, SCALE_MODES[scale], nptr, nld, rd, rs, cd, cs,
+                                       _stream_handle(stream)), "dmuon_mxfp4_quantize", h)
+
+
+def dmuon_mxfp4_dequantize(h, q, out, stream=None):
+    """The values of the MXFP4 matrix ``q`` into ``out`` [rows, k]."""
+    ptr, ld, code = _matrix(out, "out")
+    r, k = out.shape
+    d, s = _mxfp4(q, "q", r, k)
+    if r == 0 or k == 0:
+        return
+    _check(load().dmuon_mxfp4_dequantize(h, d, s, r, k, ptr, code, ld, _stream_handle(stream)),
+           "dmuon_mxfp4_dequantize", h)
+
+
+def dmuon_mxfp4_gemm(h, a, b, out, k, alpha=1.0, beta=0.0, stream=None):
+    """out = alpha * a b^T + beta * out of MXFP4 matrices a [m, k] and
+    b [n, k]; out is [m, n] in float32, bfloat16 or float16."""
+    ptr, ld, code = _matrix(out, "out")
+    m, n = out.shape
+    ad, as_ = _mxfp4(a, "a", m, k)
+    bd, bs = _mxfp4(b, "b", n, k)
+    if m == 0 or n == 0:
+        return
+    _check(load().dmuon_mxfp4_gemm(h, ad, as_, bd, bs, m, n, k, ptr, code, ld, alpha, beta, _stream_handle(stream)),
+           "dmuon_mxfp4_gemm", h)
+
+
+def _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale):
+    """The fields that forward and backward share; x may be None."""
+    p = BlockNorm()
+    p.f, p.ldf, code = _matrix(f, "f")
+    rows, cols = shape = tuple(f.shape)
+    p.rows, p.cols, p.dtype = rows, cols, code
+    if x is not None:
+        p.x, p.ldx, _ = _matrix(x, "x", code, shape)
+    p.y, p.ldy, _ = _matrix(y, "y", code, shape)
+    p.post_w, p.pre_w = _floats(post_w, "post_w", (cols,)), _floats(pre_w, "pre_w", (cols,))
+    per = max(1, rows) if rows_per_gate is None else int(rows_per_gate)
+    if per < 1:
+        raise ValueError("rows_per_gate must be at least 1")
+    p.gate, p.rows_per_gate = _floats(gate, "gate", (-(-rows // per), cols)), per
+    p.res_scale = _floats(res_scale, "res_scale", (cols,))
+    p.rstd = _floats(rstd, "rstd", (2, rows))
+    return p, code, shape
+
+
+def dmuon_block_norm_forward(h, x, f, post_w, pre_w, y, out, rstd, gate=None, rows_per_gate=None, res_scale=None,
+                             eps=1e-6, stream=None):
+    """y = res_scale * x + gate * rms(f) * post_w and out = rms(y) * pre_w over
+    the rows of x and f [rows, cols]; rstd [2, rows] is what the backward needs.
+    ``gate`` [ceil(rows / rows_per_gate), cols] (rows_per_gate None: one row for all)."""
+    p, code, shape = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale)
+    p.h, p.ldh, _ = _matrix(out, "out", code, shape)
+    p.eps = eps
+    _check(load().dmuon_block_norm_forward(h, ctypes.byref(p), _stream_handle(stream)), "dmuon_block_norm_forward", h)
+
+
+def dmuon_block_norm_backward(h, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d_post_w, d_pre_w, gate=None,
+                              d_gate=None, rows_per_gate=None, res_scale=None, d_res_scale=None, stream=None):
+    """Gradients of dmuon_block_norm_forward from dh (of its out) and dy (of y,
+    None = 0).  x may be None unless d_res_scale is wanted."""
+    p, code, shape = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale)
+    q = BlockNormGrad()
+    if dy is not None:
+        q.dy, q.lddy, _ = _matrix(dy, "dy", code, shape)
+    q.dh, q.lddh, _ = _matrix(dh, "dh", code, shape)
+    q.dx, q.lddx, _ = _matrix(dx, "dx", code, shape)
+    q.df, q.lddf, _ = _matrix(df, "df", code, shape)
+    cols = shape[1]
+    q.d_post_w, q.d_pre_w = _floats(d_post_w, "d_post_w", (cols,)), _floats(d_pre_w, "d_pre_w", (cols,))
+    if d_gate is not None:
+        if gate is None:
+            raise ValueError("d_gate without a gate")
+        q.d_gate = _floats(d_gate, "d_gate", tuple(gate.shape))
+    q.d_res_scale = _floats(d_res_scale, "d_res_scale", (cols,))
+    _check(load().dmuon_block_norm_backward(h, ctypes.byref(p), ctypes.byref(q), _stream_handle(stream)),
+           "dmuon_block_norm_backward", h)
+
+
 def dmuon_get_status(h, n_flags=0):
     """Synchronise and return (status_code, per-matrix flags list)."""
     flags = (ctypes.c_int * max(1, n_flags))()
@@ -536,3 +720,18 @@ class Handle:
 
     def status(self, n_flags=0):
         return dmuon_get_status(self.h, n_flags)
+
+    def mxfp4_quantize(self, src, by_rows=None, by_cols=None, noise=None, scale="floor", stream=None):
+        return dmuon_mxfp4_quantize(self.h, src, by_rows, by_cols, noise, scale, stream)
+
+    def mxfp4_dequantize(self, q, out, stream=None):
+        return dmuon_mxfp4_dequantize(self.h, q, out, stream)
+
+    def mxfp4_gemm(self, a, b, out, k, alpha=1.0, beta=0.0, stream=None):
+        return dmuon_mxfp4_gemm(self.h, a, b, out, k, alpha, beta, stream)
+
+    def block_norm_forward(self, x, f, post_w, pre_w, y, out, rstd, **kw):
+        return dmuon_block_norm_forward(self.h, x, f, post_w, pre_w, y, out, rstd, **kw)
+
+    def block_norm_backward(self, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d_post_w, d_pre_w, **kw):
+        return dmuon_block_norm_backward(self.h, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d_post_w, d_pre_w, **kw)

@@ -24,17 +24,16 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
-#include <mutex>
 #include <string>
 #include <vector>
-
-#include <cudaTypedefs.h>
 
 #include "../../include/dmuon.h"
 #include "aux.cuh"
 #include "coeffs.cuh"
 #include "common.cuh"
+#include "ctx.cuh"
 #include "gram.cuh"
+#include "mxfp4.cuh"
 #include "plan.cuh"
 #include "small.cuh"
 
@@ -44,27 +43,9 @@ namespace {
 
 const char* kVersion = "dmuon-gb300 0.1.0 (sm_103a, tcgen05/TMA)";
 
-// Cached caller pointer sets per plan (see run()).
-constexpr int kPtrSlots = 64;
-
 // Shapes the fused small-matrix kernel takes (oriented m <= 128, n <= 512).
 inline bool is_small(const dmuon_shape_t& s) {
   return std::min(s.rows, s.cols) <= kSmallMaxM && std::max(s.rows, s.cols) <= kSmallMaxN;
-}
-
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-bool get_encoder() {
-  std::call_once(g_encode_once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode != nullptr;
 }
 
 // fp16 row-major rows x cols with leading dimension ld (elements): 64x64
@@ -74,101 +55,12 @@ bool encode_map(CUtensorMap* map, void* base, int64_t rows, int64_t cols, int64_
   cuuint64_t strides[1] = {(cuuint64_t)(ld * 2)};
   cuuint32_t box[2] = {(cuuint32_t)kBox, (cuuint32_t)kBox};
   cuuint32_t estr[2] = {1, 1};
-  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, estr,
+  return tensor_map_encoder()(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, base, dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
-
-struct ProfRec {
-  cudaEvent_t a, b;
-  int kind;
-};
-
-// One chunk of the matrix list: a contiguous run [i0, i0 + n) planned and
-// launched as a unit.  All chunks share one workspace and run one after the
-// other on the stream.
-struct Chunk {
-  int i0 = 0, n = 0;
-  Layout L;                       // sub-list layout (workspace offsets, work lists)
-  MatDesc* d_mats = nullptr;
-  CUtensorMap* d_maps = nullptr;
-  int64_t* d_prefix = nullptr;
-  float* d_partials = nullptr;
-  float* d_tmax = nullptr;        // per momentum tile: max |U|
-  float* d_svec = nullptr;        // per matrix: s/p
-  float* d_bvec = nullptr;        // per matrix: beta', the scale of the iterate after the first product
-  float* d_pscale = nullptr;      // per matrix: the prescale p of X[0] (kept across steps)
-  int* d_redo = nullptr;          // per matrix: X[0] to be rewritten with a new p
-  int* d_counters = nullptr;      // per matrix: finished tiles of a fused launch (zeroed before it)
-  int4* d_items[3] = {nullptr, nullptr, nullptr};
-  int* d_starts[3] = {nullptr, nullptr, nullptr};
-  GramDesc* d_gd = nullptr;       // gram plans: per-matrix Gram-space buffers
-  CUtensorMap* d_gmaps = nullptr; // gram plans: kGramBufs maps per matrix
-};
-
-struct dmuon_ctx {
-  int device = 0;
-  int num_sms = 0;
-  // plan
-  std::vector<dmuon_shape_t> shapes;   // caller order
-  std::vector<int> order;              // plan position -> caller index
-  int n_large = 0;                     // plan positions [0, n_large) are chunked
-  std::vector<SmallDesc> small_descs;  // plan positions [n_large, n)
-  SmallDesc* d_small = nullptr;
-  bool small_path = true;              // requested
-  bool small_ok = false;               // small kernel configured on this device
-  bool plan_small = false;             // small kernel used by the current plan
-  bool plan_gram = false;              // chunks laid out for the Gram-space backend
-  bool gram_ok = false;                // Gram-space kernels configured on this device
-  std::vector<Chunk> chunks;
-  size_t ws_bytes = 0, small_bytes = 0;
-  void* ws = nullptr;
-  void* small = nullptr;
-  MatPtrs* d_ptrs = nullptr;
-  int* d_flags = nullptr;
-  int* d_err = nullptr;
-  // pointer-set cache: kPtrSlots device slots of n MatPtrs each
-  std::vector<MatPtrs> slot_ptrs[kPtrSlots];
-  uint64_t slot_use[kPtrSlots] = {};
-  bool slot_pending[kPtrSlots] = {};
-  cudaEvent_t slot_ev[kPtrSlots] = {};
-  uint64_t use_clock = 0;
-  MatPtrs* h_stage = nullptr;  // pinned staging, kPtrSlots x n
-  cudaStream_t last_stream = nullptr;
-  int64_t launches = 0;
-  bool profiling = false;
-  std::vector<ProfRec> prof;
-  std::vector<cudaEvent_t> ev_pool;
-  std::string last_error;
-  unsigned long long wait_timeout_ns = 0;  // 0: kernels' default (4 s)
-  int max_clusters = 0;                     // resident 2-CTA clusters (0: pairs unavailable)
-  int tile_mode = 0;                        // requested: 0 auto, 1 single CTA, 2 CTA pairs, 3 single CTA 128x128
-  int64_t chunk_elems = 0;                  // requested chunk size (0: default)
-  bool plan_pair = false;                   // tile kind of the current plan
-  int plan_bn = kBN;                        // its single-CTA tile width (256, or 128)
-  int64_t plan_chunk_elems = 0;             // chunk size of the current plan
-  // Overlap of chunk c+1's momentum pass with chunk c's tensor-core phases:
-  // a side stream, two alternating chunk workspaces and fork/join events.
-  bool overlap = false;                     // requested (off: measured neutral at the power cap)
-  bool balanced = true;                     // requested: work items dealt longest-first to the least loaded
-  int f16_iters = 3;                        // direct backend: leading iterations with fp16 operands
-  int fused = 2;                            // direct backend, one launch per chunk for all products:
-                                            // 0 never, 1 always, 2 for chunks of few work items
-  bool plan_balanced = true;                // in the current plan
-  bool plan_overlap = false;                // in the current plan (needs >= 2 chunks)
-  size_t ws_chunk = 0;                      // bytes of one chunk workspace
-  cudaStream_t side = nullptr;
-  cudaEvent_t ev_fork = nullptr, ev_join = nullptr, ev_norm[2] = {}, ev_gemm[2] = {};
-  // AdamW / clipping: descriptor buffer (device), pinned staging, results
-  void* aux_dev = nullptr;
-  size_t aux_dev_cap = 0;
-  uint8_t* aux_host = nullptr;
-  size_t aux_host_cap = 0;
-  cudaEvent_t aux_ev = nullptr;
-  bool aux_pending = false;
-};
 
 namespace {
 
@@ -186,19 +78,6 @@ constexpr int64_t kDefaultChunkElems = int64_t(1) << 29;
 // the fused kernel's processors drifting apart across phases and reading 41 %
 // more from DRAM.
 constexpr int64_t kFuseItemsPerProc = 8;
-
-int cuda_err(cudaError_t e) { return e == cudaSuccess ? DMUON_OK : (e == cudaErrorMemoryAllocation ? DMUON_ERR_OOM : DMUON_ERR_CUDA); }
-
-// Record what failed (readable through dmuon_last_error) and return `code`.
-int fail(dmuon_ctx* h, int code, const char* what, cudaError_t e = cudaSuccess) {
-  char buf[384];
-  if (e != cudaSuccess)
-    std::snprintf(buf, sizeof buf, "%s: %s (%d)", what, cudaGetErrorString(e), (int)e);
-  else
-    std::snprintf(buf, sizeof buf, "%s", what);
-  h->last_error = buf;
-  return code;
-}
 
 void free_plan(dmuon_ctx* h) {
   if (h->ws || h->small) cudaDeviceSynchronize();
@@ -368,7 +247,7 @@ void plan_sizes(const dmuon_shape_t* shapes, int n, bool pair, int64_t limit, bo
 int build_plan(dmuon_ctx* h, const dmuon_shape_t* shapes, int n, bool gram) {
   if (same_shapes(h, shapes, n, gram)) return DMUON_OK;
   free_plan(h);
-  if (!get_encoder()) return fail(h, DMUON_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
+  if (!tensor_map_encoder()) return fail(h, DMUON_ERR_CUDA, "cuTensorMapEncodeTiled entry point not found");
   if (gram && (h->max_clusters <= 0 || !h->gram_ok))
     return fail(h, DMUON_ERR_UNSUPPORTED, "Gram-space backend needs 2-CTA clusters, unavailable on this device");
   h->plan_gram = gram;
@@ -510,35 +389,6 @@ float scale_of(const MatDesc& d, int mode) {
   if (mode == 1) return 1.f;
   if (mode == 2) return (float)(0.2 * std::sqrt(std::max(r, c)));
   return (float)std::sqrt(std::max(1.0, r / c));
-}
-
-cudaEvent_t pool_event(dmuon_ctx* h) {
-  if (!h->ev_pool.empty()) { cudaEvent_t e = h->ev_pool.back(); h->ev_pool.pop_back(); return e; }
-  cudaEvent_t e = nullptr;
-  cudaEventCreate(&e);
-  return e;
-}
-
-bool capturing(cudaStream_t s) {
-  cudaStreamCaptureStatus c = cudaStreamCaptureStatusNone;
-  return cudaStreamIsCapturing(s, &c) == cudaSuccess && c != cudaStreamCaptureStatusNone;
-}
-
-struct LaunchGuard {  // brackets one launch with profiling events (not under capture)
-  dmuon_ctx* h; cudaStream_t s; ProfRec r; bool on;
-  LaunchGuard(dmuon_ctx* h_, cudaStream_t s_, int kind) : h(h_), s(s_), on(h_->profiling && !capturing(s_)) {
-    if (on) { r.a = pool_event(h); r.b = pool_event(h); r.kind = kind; cudaEventRecord(r.a, s); }
-  }
-  ~LaunchGuard() {
-    ++h->launches;
-    if (on) { cudaEventRecord(r.b, s); h->prof.push_back(r); }
-  }
-};
-
-int check_ptr(const void* p) {
-  if (!p) return DMUON_ERR_ARG;
-  if (((uintptr_t)p & 15u) != 0) return DMUON_ERR_ALIGN;
-  return DMUON_OK;
 }
 
 int check_shapes(const dmuon_shape_t* shapes, int n) {
@@ -1144,7 +994,7 @@ int dmuon_create(dmuon_handle_t* out, int device) {
   cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, device);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device);
   if (major != 10 || minor != 3) return DMUON_ERR_UNSUPPORTED;
-  if (gemm_configure() != cudaSuccess) return DMUON_ERR_CUDA;
+  if (gemm_configure() != cudaSuccess || mx_gemm_configure() != cudaSuccess) return DMUON_ERR_CUDA;
   const bool small_ok = small_configure() == cudaSuccess;
   if (!small_ok) cudaGetLastError();
   int clusters = 0;
@@ -1179,6 +1029,7 @@ int dmuon_create(dmuon_handle_t* out, int device) {
     ok = ok && cudaEventCreateWithFlags(&h->ev_norm[b], cudaEventDisableTiming) == cudaSuccess;
     ok = ok && cudaEventCreateWithFlags(&h->ev_gemm[b], cudaEventDisableTiming) == cudaSuccess;
   }
+  ok = ok && cudaMalloc(&h->d_op_err, 256) == cudaSuccess && cudaMemset(h->d_op_err, 0, 256) == cudaSuccess;
   if (!ok) {
     dmuon_destroy(h);
     return DMUON_ERR_CUDA;
@@ -1200,6 +1051,8 @@ void dmuon_destroy(dmuon_handle_t h) {
   if (h->side) cudaStreamDestroy(h->side);
   if (h->aux_dev) cudaFree(h->aux_dev);
   if (h->aux_host) cudaFreeHost(h->aux_host);
+  if (h->op_ws) cudaFree(h->op_ws);
+  if (h->d_op_err) cudaFree(h->d_op_err);
   for (auto& r : h->prof) { cudaEventDestroy(r.a); cudaEventDestroy(r.b); }
   for (auto e : h->ev_pool) cudaEventDestroy(e);
   delete h;
@@ -1450,7 +1303,11 @@ int dmuon_get_status(dmuon_handle_t h, int* flags, int n_flags) {
   if (cudaSetDevice(h->device) != cudaSuccess) return DMUON_ERR_CUDA;
   cudaError_t e = h->last_stream ? cudaStreamSynchronize(h->last_stream) : cudaDeviceSynchronize();
   if (e != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "stream synchronize", e);
-  if (!h->small) return DMUON_OK;
+  int op_err = 0;
+  e = cudaMemcpy(&op_err, h->d_op_err, 4, cudaMemcpyDeviceToHost);
+  if (e == cudaSuccess && op_err) e = cudaMemset(h->d_op_err, 0, 4);
+  if (e != cudaSuccess) return DMUON_ERR_CUDA;
+  if (!h->small) return op_err ? DMUON_ERR_TIMEOUT : DMUON_OK;
   const int n = (int)h->shapes.size();
   std::vector<int> f(n, 0);
   int err = 0;
@@ -1463,7 +1320,7 @@ int dmuon_get_status(dmuon_handle_t h, int* flags, int n_flags) {
   if (e != cudaSuccess) return DMUON_ERR_CUDA;
   if (flags)
     for (int i = 0; i < std::min(n, n_flags); ++i) flags[i] = f[i];
-  if (err) return DMUON_ERR_TIMEOUT;
+  if (err || op_err) return DMUON_ERR_TIMEOUT;
   for (int i = 0; i < n; ++i)
     if (f[i]) return DMUON_ERR_NONFINITE;
   return DMUON_OK;
