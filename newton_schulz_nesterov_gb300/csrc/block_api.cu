@@ -47,15 +47,15 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, int dims, void* base, co
 }
 
 // Maps of one operand: boxes of box_rows x 128 bytes of codes (256 elements
-// of K) and of two scale tiles for each 128 of those rows.
+// of K) and of two scale tiles for each of `scale_tiles` x 128 rows.
 bool operand_maps(CUtensorMap* data_map, CUtensorMap* scale_map, const void* data, const void* scales, int64_t rows,
-                  int64_t k, int box_rows) {
+                  int64_t k, int box_rows, int scale_tiles) {
   const cuuint64_t pitch = (cuuint64_t)mx_pitch(k);
   const cuuint64_t dsize[2] = {pitch, (cuuint64_t)rows}, dstride[1] = {pitch};
   const cuuint32_t dbox[2] = {128, (cuuint32_t)box_rows};
   const cuuint64_t kt = (cuuint64_t)mx_scale_cols(k), rt = (cuuint64_t)((rows + 127) / 128);
   const cuuint64_t ssize[3] = {128, kt, rt}, sstride[2] = {kMxScaleTile, kt * kMxScaleTile};
-  const cuuint32_t sbox[3] = {128, 2, (cuuint32_t)((box_rows + 127) / 128)};
+  const cuuint32_t sbox[3] = {128, 2, (cuuint32_t)scale_tiles};
   return encode(data_map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dsize, dstride, dbox,
                 CU_TENSOR_MAP_SWIZZLE_128B) &&
          encode(scale_map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(scales), ssize, sstride, sbox,
@@ -165,33 +165,41 @@ int dmuon_mxfp4_gemm(dmuon_handle_t h, const void* a_data, const void* a_scales,
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
   cudaStream_t stream = (cudaStream_t)stream_;
   MxGemmArgs a{};
-  a.swapped = m <= 256;
-  a.p_rows = a.swapped ? n : m;
-  a.q_rows = a.swapped ? m : n;
-  // A Q of at most 128 rows is one tile (a tile of fewer than 128 rows has
-  // to start on a scale tile).
-  const int nt = a.q_rows <= 32 ? 32 : a.q_rows <= 64 ? 64 : a.q_rows <= 128 ? 128 : 256;
-  a.q_tiles = (int)((a.q_rows + nt - 1) / nt);
-  const int64_t tiles = (a.p_rows + 127) / 128 * a.q_tiles;
-  if (tiles > INT32_MAX / 8) return fail(h, DMUON_ERR_ARG, "mxfp4_gemm: too many tiles");
-  const int64_t stages = (k + 255) / 256;
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= h->num_sms && stages >= split * 4) split *= 2;
   a.k = k;
   a.d = d;
   a.ldd = ldd;
   a.alpha = alpha;
   a.beta = beta;
   a.dtype = dtype;
+  a.vec = aligned(d, 32) && (ldd * elem_size(dtype)) % 32 == 0;
   a.err = h->d_op_err;
   a.timeout_ns = h->wait_timeout_ns;
+  const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
+  const bool pairs = h->max_clusters > 0 && pair_tiles >= h->max_clusters && m > 256;
+  a.swapped = !pairs && m <= 256;
+  a.p_rows = a.swapped ? n : m;
+  a.q_rows = a.swapped ? m : n;
   const void *pd = a.swapped ? b_data : a_data, *ps = a.swapped ? b_scales : a_scales;
   const void *qd = a.swapped ? a_data : b_data, *qs = a.swapped ? a_scales : b_scales;
-  if (!operand_maps(&a.p_data, &a.p_scales, pd, ps, a.p_rows, k, 128) ||
-      !operand_maps(&a.q_data, &a.q_scales, qd, qs, a.q_rows, k, nt))
+  // A Q of at most 128 rows is one tile (a tile of fewer than 128 rows has
+  // to start on a scale tile).
+  const int nt = pairs ? 256 : a.q_rows <= 32 ? 32 : a.q_rows <= 64 ? 64 : a.q_rows <= 128 ? 128 : 256;
+  a.q_tiles = (int)((a.q_rows + nt - 1) / nt);
+  const int64_t tiles = (a.p_rows + 127) / 128 * a.q_tiles;
+  if (tiles > INT32_MAX / 8) return fail(h, DMUON_ERR_ARG, "mxfp4_gemm: too many tiles");
+  if (!operand_maps(&a.p_data, &a.p_scales, pd, ps, a.p_rows, k, 128, 1) ||
+      !operand_maps(&a.q_data, &a.q_scales, qd, qs, a.q_rows, k, pairs ? 128 : nt, (nt + 127) / 128))
     return fail(h, DMUON_ERR_CUDA, "mxfp4_gemm: tensor map");
+  cudaError_t e;
   LaunchGuard g(h, stream, DMUON_KIND_MX_GEMM);
-  const cudaError_t e = launch_mx_gemm(a, nt, split, stream);
+  if (pairs) {
+    e = launch_mx_gemm_pair(a, (int)std::min<int64_t>(pair_tiles, h->max_clusters), stream);
+  } else {
+    const int64_t stages = (k + 255) / 256;
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= h->num_sms && stages >= split * 4) split *= 2;
+    e = launch_mx_gemm(a, nt, split, stream);
+  }
   if (e != cudaSuccess) return fail(h, cuda_err(e), "mxfp4_gemm launch", e);
   h->last_stream = stream;
   return DMUON_OK;

@@ -57,6 +57,7 @@ struct MxGemmArgs {
   int swapped;
   int dtype;                   // DMUON_F32 / _BF16 / _F16
   int q_tiles;
+  int vec;                     // D's rows are 32-byte aligned
   int* err;
   unsigned long long timeout_ns;
 };
@@ -65,5 +66,6 @@ cudaError_t launch_mx_quant(const MxQuantArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_mx_dequant(const MxDequantArgs& a, int dtype, cudaStream_t s);
 cudaError_t mx_gemm_configure();
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, int nt, int split, cudaStream_t s);
+cudaError_t launch_mx_gemm_pair(const MxGemmArgs& a, int pairs, cudaStream_t s);
 
 }  // namespace dmuon

@@ -89,6 +89,8 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 
 // ------------------------------------------------------------ geometry
 
+constexpr int kScratch = 32 * 17;  // words of an epilogue warp's transposing scratch
+
 template <int NT>
 struct Cfg {
   static constexpr int kQBytes = NT * kStageK / 2;
@@ -96,7 +98,7 @@ struct Cfg {
   static constexpr int kScales = kScaleBytes * (1 + kQTiles);
   static constexpr int kStage = kPBytes + kQBytes + kScales;  // a multiple of 1024
   static constexpr int kN = NT == 256 ? 4 : (NT == 128 ? 5 : 6);
-  static constexpr int kSmem = 1024 + kN * kStage + 256;
+  static constexpr int kSmem = 1024 + kN * kStage + 4 * kScratch * 4 + 256;
   static constexpr int kScaleCols = 8 + 8 * kQTiles;        // of one stage
   static constexpr int kCols = NT + 2 * kScaleCols;
   static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
@@ -131,12 +133,95 @@ __device__ __forceinline__ void put(const MxGemmArgs& a, T* d, float acc) {
   *d = narrow<T>(v);
 }
 
+// Two values of a 32-bit word of D's type (16-bit types), or one (fp32).
+template <typename T>
+struct Pack;
+template <>
+struct Pack<float> {
+  static constexpr int kPer = 1;
+  static __device__ __forceinline__ uint32_t pack(const float* v) { return __float_as_uint(v[0]); }
+  static __device__ __forceinline__ void unpack(uint32_t w, float* v) { v[0] = __uint_as_float(w); }
+};
+template <>
+struct Pack<__nv_bfloat16> {
+  static constexpr int kPer = 2;
+  static __device__ __forceinline__ uint32_t pack(const float* v) {
+    const __nv_bfloat162 r = __floats2bfloat162_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ void unpack(uint32_t w, float* v) {
+    v[0] = __uint_as_float(w << 16);
+    v[1] = __uint_as_float(w & 0xFFFF0000u);
+  }
+};
+template <>
+struct Pack<__half> {
+  static constexpr int kPer = 2;
+  static __device__ __forceinline__ uint32_t pack(const float* v) {
+    const __half2 r = __floats2half2_rn(v[0], v[1]);
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
+  static __device__ __forceinline__ void unpack(uint32_t w, float* v) {
+    const float2 f = __half22float2(*reinterpret_cast<__half2*>(&w));
+    v[0] = f.x;
+    v[1] = f.y;
+  }
+};
+
+// 32 columns of D from one row a lane: rows row0 + lane, columns col0 ..
+// Aligned rows (a.vec) that are whole go out as 32-byte stores; the others
+// pass through the warp's scratch (32 x 17 words) so that the lanes of a
+// store cover consecutive columns.
+template <typename T>
+__device__ __forceinline__ void store_block(const MxGemmArgs& a, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
+                                            uint32_t (&v)[32], uint32_t* scratch, int lane) {
+  constexpr int kWords = 32 / Pack<T>::kPer;
+  T* d = (T*)a.d;
+  if (a.vec && col0 + 32 <= cols) {
+    if (row0 + lane >= rows) return;
+    T* dst = d + (row0 + lane) * a.ldd + col0;
+    uint32_t w[kWords];
+    if (a.beta != 0.f) {
+#pragma unroll
+      for (int q = 0; q < kWords / 4; ++q) {
+        const uint4 o = reinterpret_cast<const uint4*>(dst)[q];
+        w[4 * q] = o.x; w[4 * q + 1] = o.y; w[4 * q + 2] = o.z; w[4 * q + 3] = o.w;
+      }
+    }
+#pragma unroll
+    for (int q = 0; q < kWords; ++q) {
+      float f[2], o[2];
+      if (a.beta != 0.f) Pack<T>::unpack(w[q], o);
+#pragma unroll
+      for (int k = 0; k < Pack<T>::kPer; ++k) {
+        f[k] = a.alpha * __uint_as_float(v[q * Pack<T>::kPer + k]);
+        if (a.beta != 0.f) f[k] = fmaf(a.beta, o[k], f[k]);
+      }
+      w[q] = Pack<T>::pack(f);
+    }
+#pragma unroll
+    for (int q = 0; q < kWords / 8; ++q) ptx::st_global_v8(reinterpret_cast<uint32_t*>(dst) + 8 * q, w + 8 * q);
+    return;
+  }
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) scratch[lane * 17 + j] = v[half * 16 + j];
+    __syncwarp();
+    const int64_t col = col0 + half * 16 + (lane & 15);
+    for (int r = lane >> 4; r < 32; r += 2)
+      if (row0 + r < rows && col < cols) put<T>(a, d + (row0 + r) * a.ldd + col, __uint_as_float(scratch[r * 17 + (lane & 15)]));
+    __syncwarp();
+  }
+}
+
 template <int NT, typename T>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_constant__ MxGemmArgs a) {
   using C = Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(stages + C::kN * C::kStage);
+  uint32_t* scratch = reinterpret_cast<uint32_t*>(stages + C::kN * C::kStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + 4 * kScratch);
   uint64_t* empty = full + C::kN;
   uint64_t* done = empty + C::kN;       // the accumulator is complete
   uint64_t* drain = done + 1;
@@ -243,15 +328,14 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 #pragma unroll 1
       for (int c = 0; c < NT; c += 32) {
         if (q0 + c >= a.q_rows) break;
-        if constexpr (NT >= 32) {
-          uint32_t v[32];
-          ptx::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
-          if (p0 + p < a.p_rows)
+        uint32_t v[32];
+        ptx::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
+        if (!a.swapped) {
+          store_block<T>(a, p0 + quad * 32, q0 + c, a.p_rows, a.q_rows, v, scratch + (warp - 2) * kScratch, lane);
+        } else if (p0 + p < a.p_rows) {  // lanes hold consecutive columns of D
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (q0 + c + j < a.q_rows)
-                put<T>(a, a.swapped ? d + (q0 + c + j) * a.ldd + p0 + p : d + (p0 + p) * a.ldd + q0 + c + j,
-                       __uint_as_float(v[j]));
+          for (int j = 0; j < 32; ++j)
+            if (q0 + c + j < a.q_rows) put<T>(a, d + (q0 + c + j) * a.ldd + p0 + p, __uint_as_float(v[j]));
         }
       }
     }
@@ -290,6 +374,230 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmem);
   }
+}
+
+// ---------------------------------------------------------------------------
+// CTA pairs (cta_group::2) for products that fill the device: persistent
+// pairs, a 256 x 256 tile of D each, rank r holding rows [128 r, +128) of it
+// in its tensor memory.  Per stage a rank loads its 128 rows of A, 128 rows of
+// B, its A scales and the scales of all 256 rows of B (each rank's tensor core
+// multiplies its rows by the whole of B).
+//
+// Tensor memory: two 256-column accumulators and 24 scale columns do not fit
+// 512 columns side by side, so the accumulators share 32: accumulator 0 is
+// columns [0, 256), 1 is [224, 480), the scales are at 480.  The epilogue
+// drains the shared 32 columns of a tile first and signals that apart; the
+// next tile's products begin then, while the other 224 columns are stored.
+// ---------------------------------------------------------------------------
+constexpr int kPairScales = kScaleBytes * 3;              // A's 128 rows, B's 256
+constexpr int kPairStage = 2 * kPBytes + kPairScales;     // 35 KB
+constexpr int kPairN = 6;
+constexpr int kPairSmem = 1024 + kPairN * kPairStage + 4 * kScratch * 4 + 256;
+constexpr int kAccStride = 224, kPairScaleCol = 480;
+static_assert(kPairStage % 1024 == 0 && kPairSmem <= 227 * 1024, "pair geometry");
+
+__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// copy_scales in both ranks, each from its own shared memory.
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint32_t saddr) {
+  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+                                              uint32_t sfb, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      : "memory");
+}
+
+// Tile t of a pair's walk: groups of kGroup tile rows, column by column inside
+// a group, so that the pairs running together read a block of few tile rows
+// by few tile columns.
+constexpr int kGroup = 8;
+__device__ __forceinline__ void tile_of(int t, int tm, int tn, int& m, int& n) {
+  const int g = t / (kGroup * tn), rem = t - g * kGroup * tn, rows = min(kGroup, tm - g * kGroup);
+  m = g * kGroup + rem % rows;
+  n = rem / rows;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) mx_gemm_pair_kernel(const __grid_constant__ MxGemmArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
+  uint32_t* scratch = reinterpret_cast<uint32_t*>(stages + kPairN * kPairStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + 4 * kScratch);
+  uint64_t* empty = full + kPairN;
+  uint64_t* tfull = empty + kPairN;     // [2] accumulator complete
+  uint64_t* tempty = tfull + 2;         // [2] accumulator stored
+  uint64_t* tshared = tempty + 2;       // a tile's shared columns drained
+  uint64_t* drain = tshared + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t tmo = a.timeout_ns ? a.timeout_ns : kWaitNs;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const bool leader = rank == 0;
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int tm = (int)((a.p_rows + 255) / 256), tn = a.q_tiles, tiles = tm * tn;
+  const int kbn = (int)((a.k + kStageK - 1) / kStageK);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kPairN; ++s) {
+      ptx::mbar_init(ptx::smem_addr(full + s), 1);
+      ptx::mbar_init(ptx::smem_addr(empty + s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(ptx::smem_addr(tfull + i), 1);
+      ptx::mbar_init(ptx::smem_addr(tempty + i), 8);  // 4 epilogue warps x 2 ranks
+    }
+    ptx::mbar_init(ptx::smem_addr(tshared), 8);
+    ptx::mbar_init(ptx::smem_addr(drain), 1);
+    *abort_flag = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc_pair(ptx::smem_addr(tmem_slot), 512);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // both ranks' barriers exist before any remote signal
+  ptx::tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      bool ok = true;
+      for (int t = pair; ok && t < tiles; t += npairs) {
+        int mt, nt;
+        tile_of(t, tm, tn, mt, nt);
+        const int rowA = mt * 256 + (int)rank * 128, rowB = nt * 256 + (int)rank * 128;
+        for (int kb = 0; kb < kbn; ++kb, ++it) {
+          const uint32_t s = it % kPairN;
+          if (!bounded_wait(ptx::smem_addr(empty + s), ((it / kPairN) & 1u) ^ 1u, abort_flag, a.err, tmo)) { ok = false; break; }
+          const uint32_t fl = ptx::smem_addr(full + s), fb = ptx::mapa_shared(fl, 0);
+          if (leader) ptx::mbar_expect_tx(fl, 2 * kPairStage);
+          const uint32_t st = ptx::smem_addr(stages + s * kPairStage), sc = st + 2 * kPBytes;
+          ptx::tma_load_2d_pair(st, &a.p_data, kb * (kStageK / 2), rowA, fb);
+          ptx::tma_load_2d_pair(st + kPBytes, &a.q_data, kb * (kStageK / 2), rowB, fb);
+          tma_load_3d_pair(sc, &a.p_scales, 0, kb * 2, rowA / 128, fb);
+          tma_load_3d_pair(sc + kScaleBytes, &a.q_scales, 0, kb * 2, nt * 2, fb);
+        }
+      }
+      if (leader && (!ok || *abort_flag)) {  // both ranks' copies land before exit
+        const uint32_t out = it < (uint32_t)kPairN ? it : (uint32_t)kPairN;
+        for (uint32_t i = it - out; i < it; ++i)
+          bounded_wait_slow(ptx::smem_addr(full + i % kPairN), (i / kPairN) & 1u, abort_flag, a.err, false, kWaitNs);
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && leader) {
+      uint32_t it = 0, tc = 0;
+      bool ok = true, issued = false;
+      for (int t = pair; ok && t < tiles; t += npairs, ++tc) {
+        const uint32_t acc = tc & 1u;
+        if (!bounded_wait(ptx::smem_addr(tempty + acc), ((tc >> 1) & 1u) ^ 1u, abort_flag, a.err, tmo) ||
+            (tc > 0 && !bounded_wait(ptx::smem_addr(tshared), (tc - 1) & 1u, abort_flag, a.err, tmo))) { ok = false; break; }
+        ptx::tc_fence_after();
+        const uint32_t dt = tmem + acc * kAccStride;
+        for (int kb = 0; kb < kbn; ++kb, ++it) {
+          const uint32_t s = it % kPairN;
+          if (!bounded_wait(ptx::smem_addr(full + s), (it / kPairN) & 1u, abort_flag, a.err, tmo)) { ok = false; break; }
+          ptx::tc_fence_after();
+          const uint32_t st = ptx::smem_addr(stages + s * kPairStage), sc = st + 2 * kPBytes;
+          const uint32_t ta = tmem + kPairScaleCol, tb = ta + 8;
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            copy_scales_pair(ta + u * 4, sc + u * kMxScaleTile);
+            copy_scales_pair(tb + u * 8, sc + kScaleBytes + u * kMxScaleTile);
+            copy_scales_pair(tb + u * 8 + 4, sc + 2 * kScaleBytes + u * kMxScaleTile);
+          }
+          const int64_t left = a.k - (int64_t)kb * kStageK;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (j * 64 < left)
+              mma_mxf4_pair(dt, ptx::desc_sw128(st + j * 32, 16, 1024), ptx::desc_sw128(st + kPBytes + j * 32, 16, 1024),
+                            idesc_mxf4(256, 256, j & 1), ta + (j / 2) * 4, tb + (j / 2) * 8, (kb | j) != 0);
+          }
+          issued = true;
+          ptx::mma_commit_multicast(ptx::smem_addr(empty + s), 0x3);
+        }
+        if (!ok) break;
+        ptx::mma_commit_multicast(ptx::smem_addr(tfull + acc), 0x3);
+      }
+      if (issued && (!ok || *abort_flag)) {
+        ptx::mma_commit_pair(ptx::smem_addr(drain));
+        bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
+      }
+    }
+  } else {
+    const int quad = warp & 3;
+    uint32_t* mine = scratch + (warp - 2) * kScratch;
+    uint32_t tc = 0;
+    for (int t = pair; t < tiles; t += npairs, ++tc) {
+      const uint32_t acc = tc & 1u;
+      if (!bounded_wait(ptx::smem_addr(tfull + acc), (tc >> 1) & 1u, abort_flag, a.err, tmo)) break;
+      ptx::tc_fence_after();
+      int mt, nt;
+      tile_of(t, tm, tn, mt, nt);
+      const int64_t row0 = (int64_t)mt * 256 + rank * 128 + quad * 32, col0 = (int64_t)nt * 256;
+      const uint32_t tq = tmem + acc * kAccStride + ((uint32_t)(quad * 32) << 16);
+#pragma unroll 1
+      for (int i = 0; i < 8; ++i) {
+        const int c = (acc ? i : (i + 7) & 7) * 32;  // the shared columns first: the last 32 of accumulator 0, the first of 1
+        uint32_t v[32];
+        ptx::tmem_ld32(tq + c, v);
+        if (i == 0 || i == 7) {
+          ptx::tc_fence_before();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive_cluster(ptx::mapa_shared(ptx::smem_addr(i == 0 ? tshared : tempty + acc), 0));
+        }
+        if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, v, mine, lane);
+      }
+    }
+  }
+
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // no rank frees tensor memory or exits while its pair is busy
+  if (warp == 1) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, 512);
+  }
+}
+
+template <typename T>
+cudaError_t configure_pair() {
+  return cudaFuncSetAttribute(mx_gemm_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPairSmem);
+}
+
+template <typename T>
+cudaError_t launch_pair(const MxGemmArgs& a, int pairs, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2 * pairs, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = kPairSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mx_gemm_pair_kernel<T>, a);
 }
 
 template <int NT, typename T>
@@ -336,7 +644,16 @@ cudaError_t mx_gemm_configure() {
   if ((e = configure_nt<32>()) != cudaSuccess) return e;
   if ((e = configure_nt<64>()) != cudaSuccess) return e;
   if ((e = configure_nt<128>()) != cudaSuccess) return e;
-  return configure_nt<256>();
+  if ((e = configure_nt<256>()) != cudaSuccess) return e;
+  if ((e = configure_pair<float>()) != cudaSuccess) return e;
+  if ((e = configure_pair<__nv_bfloat16>()) != cudaSuccess) return e;
+  return configure_pair<__half>();
+}
+
+cudaError_t launch_mx_gemm_pair(const MxGemmArgs& a, int pairs, cudaStream_t s) {
+  if (a.dtype == DMUON_BF16) return launch_pair<__nv_bfloat16>(a, pairs, s);
+  if (a.dtype == DMUON_F16) return launch_pair<__half>(a, pairs, s);
+  return launch_pair<float>(a, pairs, s);
 }
 
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, int nt, int split, cudaStream_t s) {
