@@ -87,18 +87,31 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
-// 32 lanes x 64 columns of tensor memory, waited for.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
+// 32 lanes x 96 columns of tensor memory, waited for.
+__device__ __forceinline__ void tmem_ld96(uint32_t taddr, uint32_t (&v)[96]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
       "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
       "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
+      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%96];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {"
+      "%64, %65, %66, %67, %68, %69, %70, %71, %72, %73, %74, %75, %76, %77, %78, %79, "
+      "%80, %81, %82, %83, %84, %85, %86, %87, %88, %89, %90, %91, %92, %93, %94, %95}, [%97];\n\t"
       "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), 
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]), "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]), "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]), "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
-      : "r"(taddr)
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+        "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+        "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+        "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+        "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63]),
+        "=r"(v[64]), "=r"(v[65]), "=r"(v[66]), "=r"(v[67]), "=r"(v[68]), "=r"(v[69]), "=r"(v[70]), "=r"(v[71]),
+        "=r"(v[72]), "=r"(v[73]), "=r"(v[74]), "=r"(v[75]), "=r"(v[76]), "=r"(v[77]), "=r"(v[78]), "=r"(v[79]),
+        "=r"(v[80]), "=r"(v[81]), "=r"(v[82]), "=r"(v[83]), "=r"(v[84]), "=r"(v[85]), "=r"(v[86]), "=r"(v[87]),
+        "=r"(v[88]), "=r"(v[89]), "=r"(v[90]), "=r"(v[91]), "=r"(v[92]), "=r"(v[93]), "=r"(v[94]), "=r"(v[95])
+      : "r"(taddr), "r"(taddr + 64)
       : "memory");
 }
 
@@ -408,12 +421,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 // The scale copies have a warp of their own: issued by the thread that issues
 // the products they queue behind them, and a stage of four products (512
 // clocks) and six copies took 853 clocks; from another thread they run beside
-// them, and a stage takes 512.  Two sets of scale columns, the next stage's
-// copied during this one's products.
+// them.  From a set's last product to its next stage's first one goes by two
+// commits and the copies (about 960 clocks), so there are four sets of 24 scale
+// columns: with two a stage took that long.
 //
-// Tensor memory: two 256-column accumulators and 48 scale columns do not fit
-// 512 columns side by side, so the accumulators share 48: accumulator 0 is
-// columns [0, 256), 1 is [208, 464), the scales are at 464 and 488.  The
+// Tensor memory: two 256-column accumulators and 96 scale columns do not fit
+// 512 columns side by side, so the accumulators share 96: accumulator 0 is
+// columns [0, 256), 1 is [160, 416), the scales are from 416 on.  The
 // epilogue drains the shared columns of a tile first and signals that apart;
 // the next tile's products begin then, while the rest is stored.
 // ---------------------------------------------------------------------------
@@ -422,7 +436,7 @@ constexpr int kPairStage = 2 * kPBytes + kPairScales;     // 35 KB
 constexpr int kPairN = 6;
 constexpr int kPairSmem = 1024 + kPairN * kPairStage + 4 * kScratch * 4 + 256;
 constexpr int kPairThreads = 224;
-constexpr int kAccStride = 208, kPairScaleCol = 464;
+constexpr int kAccStride = 160, kPairScaleCol = 416, kPairSets = 4;
 static_assert(kPairStage % 1024 == 0 && kPairSmem <= 227 * 1024, "pair geometry");
 
 __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
@@ -469,8 +483,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   uint64_t* tfull = empty + kPairN;     // [2] accumulator complete
   uint64_t* tempty = tfull + 2;         // [2] accumulator stored
   uint64_t* tshared = tempty + 2;       // a tile's shared columns drained
-  uint64_t* sfull = tshared + 1;        // [2] a set of scales is in place
-  uint64_t* drain = sfull + 2;          // [2] MMA issuer's, scale copier's
+  uint64_t* sfull = tshared + 1;        // [kPairSets] a set of scales is in place
+  uint64_t* drain = sfull + kPairSets;          // [2] MMA issuer's, scale copier's
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
@@ -492,10 +506,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
       ptx::mbar_init(ptx::smem_addr(tempty + i), 8);  // 4 epilogue warps x 2 ranks
     }
     ptx::mbar_init(ptx::smem_addr(tshared), 8);
-    for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(ptx::smem_addr(sfull + i), 1);
-      ptx::mbar_init(ptx::smem_addr(drain + i), 1);
-    }
+    for (int i = 0; i < kPairSets; ++i) ptx::mbar_init(ptx::smem_addr(sfull + i), 1);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_addr(drain + i), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -548,10 +560,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
         for (int kb = 0; kb < kbn; ++kb, ++it) {
           const uint32_t s = it % kPairN;
           if (!bounded_wait(ptx::smem_addr(full + s), (it / kPairN) & 1u, abort_flag, a.err, tmo) ||
-              !bounded_wait(ptx::smem_addr(sfull + (it & 1)), (it >> 1) & 1u, abort_flag, a.err, tmo)) { ok = false; break; }
+              !bounded_wait(ptx::smem_addr(sfull + it % kPairSets), (it / kPairSets) & 1u, abort_flag, a.err, tmo)) { ok = false; break; }
           ptx::tc_fence_after();
           const uint32_t st = ptx::smem_addr(stages + s * kPairStage);
-          const uint32_t ta = tmem + kPairScaleCol + (it & 1) * 24, tb = ta + 8;
+          const uint32_t ta = tmem + kPairScaleCol + it % kPairSets * 24, tb = ta + 8;
           const int64_t left = a.k - (int64_t)kb * kStageK;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
@@ -576,22 +588,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
       bool ok = true;
       int it = 0;
       for (; it < stages_total; ++it) {
-        const uint32_t s = it % kPairN, back = it - 2;  // a set is free when stage it - 2 has been multiplied
+        const uint32_t s = it % kPairN, back = it - kPairSets;  // a set is free when the stage that had it last has been multiplied
         if (!bounded_wait(ptx::smem_addr(full + s), (it / kPairN) & 1u, abort_flag, a.err, tmo) ||
-            (it >= 2 && !bounded_wait(ptx::smem_addr(empty + back % kPairN), (back / kPairN) & 1u, abort_flag, a.err, tmo))) {
+            (it >= kPairSets && !bounded_wait(ptx::smem_addr(empty + back % kPairN), (back / kPairN) & 1u, abort_flag, a.err, tmo))) {
           ok = false;
           break;
         }
         ptx::tc_fence_after();
         const uint32_t sc = ptx::smem_addr(stages + s * kPairStage) + 2 * kPBytes;
-        const uint32_t ta = tmem + kPairScaleCol + (it & 1) * 24, tb = ta + 8;
+        const uint32_t ta = tmem + kPairScaleCol + it % kPairSets * 24, tb = ta + 8;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           copy_scales_pair(ta + u * 4, sc + u * kMxScaleTile);
           copy_scales_pair(tb + u * 8, sc + kScaleBytes + u * kMxScaleTile);
           copy_scales_pair(tb + u * 8 + 4, sc + 2 * kScaleBytes + u * kMxScaleTile);
         }
-        ptx::mma_commit_pair(ptx::smem_addr(sfull + (it & 1)));
+        ptx::mma_commit_pair(ptx::smem_addr(sfull + it % kPairSets));
       }
       if (it > 0 && (!ok || *abort_flag)) {
         ptx::mma_commit_pair(ptx::smem_addr(drain + 1));
@@ -610,18 +622,28 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
       tile_of(t, tm, tn, mt, nt);
       const int64_t row0 = (int64_t)mt * 256 + rank * 128 + quad * 32, col0 = (int64_t)nt * 256;
       const uint32_t tq = tmem + acc * kAccStride + ((uint32_t)(quad * 32) << 16);
+      {  // the shared columns first: the last 96 of accumulator 0, the first of 1
+        const int c = acc ? 0 : kAccStride;
+        uint32_t v[96];
+        tmem_ld96(tq + c, v);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tshared), 0));
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (col0 + c + q * 32 < a.q_rows) store_block<T>(a, row0, col0 + c + q * 32, a.p_rows, a.q_rows, v + q * 32, mine, lane);
+      }
 #pragma unroll 1
-      for (int i = 0; i < 4; ++i) {
-        const int c = (acc ? i : (i + 3) & 3) * 64;  // the shared columns first: the last of accumulator 0, the first of 1
-        uint32_t v[64];
-        tmem_ld64(tq + c, v);
-        if (i == 0 || i == 3) {
+      for (int i = 0; i < 5; ++i) {
+        const int c = (acc ? 96 : 0) + i * 32;
+        uint32_t v[32];
+        ptx::tmem_ld32(tq + c, v);
+        if (i == 4) {
           ptx::tc_fence_before();
           __syncwarp();
-          if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(i == 0 ? tshared : tempty + acc), 0));
+          if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tempty + acc), 0));
         }
         if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, v, mine, lane);
-        if (col0 + c + 32 < a.q_rows) store_block<T>(a, row0, col0 + c + 32, a.p_rows, a.q_rows, v + 32, mine, lane);
       }
     }
   }
