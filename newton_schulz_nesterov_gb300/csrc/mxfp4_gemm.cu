@@ -75,6 +75,11 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int half) {
          ((uint32_t)(m >> 4) << 24) | ((uint32_t)(half * 2) << 29);
 }
 
+// High word of a K-major, 128-byte-swizzled shared-memory descriptor
+// (1024 bytes between groups of eight rows).
+constexpr uint32_t desc_hi() { return (1024u >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
@@ -116,8 +121,9 @@ __device__ __forceinline__ void tmem_ld96(uint32_t taddr, uint32_t (&v)[96]) {
 }
 
 // Arrive on a barrier of another CTA of the cluster.  What it releases are
-// reads of tensor memory, which tcgen05.fence orders; release at cluster scope
-// would also wait for this thread's global stores (1200 clocks measured).
+// reads or writes of tensor memory, which are complete (tcgen05.wait) and
+// ordered by tcgen05.fence; release at cluster scope would wait for a memory
+// barrier besides (1200 clocks measured).
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       }
     }
   } else if (have) {
-    have = bounded_wait(ptx::smem_addr(done), 0, abort_flag, a.err, tmo);
+    have = bounded_wait_warp(ptx::smem_addr(done), 0, abort_flag, a.err, tmo);
     ptx::tc_fence_after();
   }
 
@@ -418,12 +424,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 // B, its A scales and the scales of all 256 rows of B (each rank's tensor core
 // multiplies its rows by the whole of B).
 //
-// The scale copies have a warp of their own: issued by the thread that issues
-// the products they queue behind them, and a stage of four products (512
-// clocks) and six copies took 853 clocks; from another thread they run beside
-// them.  From a set's last product to its next stage's first one goes by two
-// commits and the copies (about 960 clocks), so there are four sets of 24 scale
-// columns: with two a stage took that long.
+// Scales go to tensor memory by four warps' own stores (tcgen05.st; lane l of
+// each 32-lane group holds the words of rows l, l + 32, ..), not by
+// tcgen05.cp: copies queue with the products.  Per stage of four products (512
+// clocks) and six copies, issued by one thread they took 853 clocks, from two
+// threads 690; the stores run beside the products.  From a set's last product
+// to its next one goes by two barriers and the stores (several hundred
+// clocks), so there are four sets of 24 scale columns.
 //
 // Tensor memory: two 256-column accumulators and 96 scale columns do not fit
 // 512 columns side by side, so the accumulators share 96: accumulator 0 is
@@ -435,32 +442,43 @@ constexpr int kPairScales = kScaleBytes * 3;              // A's 128 rows, B's 2
 constexpr int kPairStage = 2 * kPBytes + kPairScales;     // 35 KB
 constexpr int kPairN = 6;
 constexpr int kPairSmem = 1024 + kPairN * kPairStage + 4 * kScratch * 4 + 256;
-constexpr int kPairThreads = 224;
+constexpr int kPairThreads = 320;
 constexpr int kAccStride = 160, kPairScaleCol = 416, kPairSets = 4;
 static_assert(kPairStage % 1024 == 0 && kPairSmem <= 227 * 1024, "pair geometry");
 
-__device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
-      : "memory");
+// Words of this warp's 32 lanes into columns of its lane group.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4& a, const uint4& b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 
-// copy_scales in both ranks, each from its own shared memory.
-__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint32_t saddr) {
-  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
-}
-
-__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sfa,
+// The four K = 64 products of a stage: shared-memory descriptors by their low
+// words (the high words are the same for every operand), 32 bytes of K apart.
+constexpr uint32_t kDescHi = desc_hi();
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint32_t alo, uint32_t blo, uint32_t idesc, uint32_t sfa,
                                               uint32_t sfb, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %7};\n\t"
+      "mov.b64 db, {%2, %7};\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "r"(alo), "r"(blo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHi)
       : "memory");
+}
+
+// One lane of a converged warp: the warp's loops stay uniform, so addresses
+// and descriptors are kept in uniform registers, which the tensor core and
+// TMA instructions take.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
 }
 
 // Tile t of a pair's walk: groups of kGroup tile rows, column by column inside
@@ -483,31 +501,34 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   uint64_t* tfull = empty + kPairN;     // [2] accumulator complete
   uint64_t* tempty = tfull + 2;         // [2] accumulator stored
   uint64_t* tshared = tempty + 2;       // a tile's shared columns drained
-  uint64_t* sfull = tshared + 1;        // [kPairSets] a set of scales is in place
-  uint64_t* drain = sfull + kPairSets;          // [2] MMA issuer's, scale copier's
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 2);
+  uint64_t* sfull = tshared + 1;        // [kPairSets] both ranks' scales are in tensor memory
+  uint64_t* sready = sfull + kPairSets; // [kPairN] this rank's scales are in shared memory
+  uint64_t* drain = sready + kPairN;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t tmo = a.timeout_ns ? a.timeout_ns : kWaitNs;
   const uint32_t rank = ptx::cluster_ctarank();
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
   const int tm = (int)((a.p_rows + 255) / 256), tn = a.q_tiles, tiles = tm * tn;
   const int kbn = (int)((a.k + kStageK - 1) / kStageK);
+  const int last_parts = (int)((a.k - (int64_t)(kbn - 1) * kStageK + 63) / 64);  // K = 64 products of the last stage
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kPairN; ++s) {
       ptx::mbar_init(ptx::smem_addr(full + s), 1);
       ptx::mbar_init(ptx::smem_addr(empty + s), 1);
+      ptx::mbar_init(ptx::smem_addr(sready + s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_addr(tfull + i), 1);
       ptx::mbar_init(ptx::smem_addr(tempty + i), 8);  // 4 epilogue warps x 2 ranks
     }
     ptx::mbar_init(ptx::smem_addr(tshared), 8);
-    for (int i = 0; i < kPairSets; ++i) ptx::mbar_init(ptx::smem_addr(sfull + i), 1);
-    for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_addr(drain + i), 1);
+    for (int i = 0; i < kPairSets; ++i) ptx::mbar_init(ptx::smem_addr(sfull + i), 8);  // 4 scale warps x 2 ranks
+    ptx::mbar_init(ptx::smem_addr(drain), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
   }
@@ -522,93 +543,102 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   const uint32_t tmem = *tmem_slot;
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      bool ok = true;
-      for (int t = pair; ok && t < tiles; t += npairs) {
-        int mt, nt;
-        tile_of(t, tm, tn, mt, nt);
-        const int rowA = mt * 256 + (int)rank * 128, rowB = nt * 256 + (int)rank * 128;
-        for (int kb = 0; kb < kbn; ++kb, ++it) {
-          const uint32_t s = it % kPairN;
-          if (!bounded_wait(ptx::smem_addr(empty + s), ((it / kPairN) & 1u) ^ 1u, abort_flag, a.err, tmo)) { ok = false; break; }
-          const uint32_t fl = ptx::smem_addr(full + s), fb = ptx::mapa_shared(fl, 0);
-          if (leader) ptx::mbar_expect_tx(fl, 2 * kPairStage);
-          const uint32_t st = ptx::smem_addr(stages + s * kPairStage), sc = st + 2 * kPBytes;
-          ptx::tma_load_2d_pair(st, &a.p_data, kb * (kStageK / 2), rowA, fb);
-          ptx::tma_load_2d_pair(st + kPBytes, &a.q_data, kb * (kStageK / 2), rowB, fb);
-          tma_load_3d_pair(sc, &a.p_scales, 0, kb * 2, rowA / 128, fb);
-          tma_load_3d_pair(sc + kScaleBytes, &a.q_scales, 0, kb * 2, nt * 2, fb);
+    // ------------------------------------------------------------ producer
+    const bool elected = elect_one();
+    const uint32_t full0 = ptx::smem_addr(full), remote = ptx::mapa_shared(full0, 0), ready0 = ptx::smem_addr(sready);
+    const uint32_t empty0 = ptx::smem_addr(empty), stage0 = ptx::smem_addr(stages);
+    uint32_t s = 0, ph = 0, issued = 0;
+    bool ok = true;
+    for (int t = pair; ok && t < tiles; t += npairs) {
+      int mt, nt;
+      tile_of(t, tm, tn, mt, nt);
+      const int rowA = mt * 256 + (int)rank * 128, rowB = nt * 256 + (int)rank * 128;
+      for (int kb = 0; kb < kbn; ++kb) {
+        if (!bounded_wait_warp(empty0 + s * 8, ph ^ 1u, abort_flag, a.err, tmo)) { ok = false; break; }
+        if (elected) {
+          const uint32_t st = stage0 + s * kPairStage, sc = st + 2 * kPBytes;
+          ptx::mbar_expect_tx(ready0 + s * 8, kPairScales);
+          if (leader) ptx::mbar_expect_tx(full0 + s * 8, 4 * kPBytes);
+          tma_load_3d(sc, &a.p_scales, 0, kb * 2, rowA / 128, ready0 + s * 8);
+          tma_load_3d(sc + kScaleBytes, &a.q_scales, 0, kb * 2, nt * 2, ready0 + s * 8);
+          ptx::tma_load_2d_pair(st, &a.p_data, kb * (kStageK / 2), rowA, remote + s * 8);
+          ptx::tma_load_2d_pair(st + kPBytes, &a.q_data, kb * (kStageK / 2), rowB, remote + s * 8);
         }
+        ++issued;
+        if (++s == kPairN) { s = 0; ph ^= 1u; }
       }
-      if (leader && (!ok || *abort_flag)) {  // both ranks' copies land before exit
-        const uint32_t out = it < (uint32_t)kPairN ? it : (uint32_t)kPairN;
-        for (uint32_t i = it - out; i < it; ++i)
-          bounded_wait_slow(ptx::smem_addr(full + i % kPairN), (i / kPairN) & 1u, abort_flag, a.err, false, kWaitNs);
+    }
+    if (!ok || *abort_flag) {  // every copy lands before exit: both ranks' codes on the leader, scales on each rank
+      const uint32_t out = issued < (uint32_t)kPairN ? issued : (uint32_t)kPairN;
+      for (uint32_t i = issued - out; i < issued; ++i) {
+        bounded_wait_slow(ready0 + i % kPairN * 8, (i / kPairN) & 1u, abort_flag, a.err, false, kWaitNs);
+        if (leader) bounded_wait_slow(full0 + i % kPairN * 8, (i / kPairN) & 1u, abort_flag, a.err, false, kWaitNs);
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && leader) {
-      uint32_t it = 0, tc = 0;
+    // ------------------------------------------------------------ MMA issuer
+    if (leader) {
+      const bool elected = elect_one();
+      const uint32_t full0 = ptx::smem_addr(full), empty0 = ptx::smem_addr(empty), sfull0 = ptx::smem_addr(sfull);
+      const uint32_t desc0 = desc_lo(ptx::smem_addr(stages));
+      uint32_t s = 0, ph = 0, set = 0, sph = 0, tc = 0;
       bool ok = true, issued = false;
       for (int t = pair; ok && t < tiles; t += npairs, ++tc) {
         const uint32_t acc = tc & 1u;
-        if (!bounded_wait(ptx::smem_addr(tempty + acc), ((tc >> 1) & 1u) ^ 1u, abort_flag, a.err, tmo) ||
-            (tc > 0 && !bounded_wait(ptx::smem_addr(tshared), (tc - 1) & 1u, abort_flag, a.err, tmo))) { ok = false; break; }
-        ptx::tc_fence_after();
+        if (!bounded_wait_warp(ptx::smem_addr(tempty + acc), ((tc >> 1) & 1u) ^ 1u, abort_flag, a.err, tmo) ||
+            (tc > 0 && !bounded_wait_warp(ptx::smem_addr(tshared), (tc - 1) & 1u, abort_flag, a.err, tmo))) { ok = false; break; }
         const uint32_t dt = tmem + acc * kAccStride;
-        for (int kb = 0; kb < kbn; ++kb, ++it) {
-          const uint32_t s = it % kPairN;
-          if (!bounded_wait(ptx::smem_addr(full + s), (it / kPairN) & 1u, abort_flag, a.err, tmo) ||
-              !bounded_wait(ptx::smem_addr(sfull + it % kPairSets), (it / kPairSets) & 1u, abort_flag, a.err, tmo)) { ok = false; break; }
+        for (int kb = 0; kb < kbn; ++kb) {
+          if (!bounded_wait_warp(full0 + s * 8, ph, abort_flag, a.err, tmo) ||
+              !bounded_wait_warp(sfull0 + set * 8, sph, abort_flag, a.err, tmo)) { ok = false; break; }
           ptx::tc_fence_after();
-          const uint32_t st = ptx::smem_addr(stages + s * kPairStage);
-          const uint32_t ta = tmem + kPairScaleCol + it % kPairSets * 24, tb = ta + 8;
-          const int64_t left = a.k - (int64_t)kb * kStageK;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j * 64 < left)
-              mma_mxf4_pair(dt, ptx::desc_sw128(st + j * 32, 16, 1024), ptx::desc_sw128(st + kPBytes + j * 32, 16, 1024),
-                            idesc_mxf4(256, 256, j & 1), ta + (j / 2) * 4, tb + (j / 2) * 8, (kb | j) != 0);
+          if (elected) {
+            const uint32_t da = desc0 + s * (kPairStage >> 4), db = da + (kPBytes >> 4);
+            const uint32_t ta = tmem + kPairScaleCol + set * 24, tb = ta + 8;
+            // A K tail: products past it would only add zeros.
+            const int parts = kb + 1 < kbn ? 4 : last_parts;
+            mma_mxf4_pair(dt, da, db, idesc_mxf4(256, 256, 0), ta, tb, kb != 0);
+            if (parts > 1) mma_mxf4_pair(dt, da + 2, db + 2, idesc_mxf4(256, 256, 1), ta, tb, 1);
+            if (parts > 2) mma_mxf4_pair(dt, da + 4, db + 4, idesc_mxf4(256, 256, 0), ta + 4, tb + 8, 1);
+            if (parts > 3) mma_mxf4_pair(dt, da + 6, db + 6, idesc_mxf4(256, 256, 1), ta + 4, tb + 8, 1);
+            ptx::mma_commit_multicast(empty0 + s * 8, 0x3);
+            if (kb + 1 == kbn) ptx::mma_commit_multicast(ptx::smem_addr(tfull + acc), 0x3);
           }
           issued = true;
-          ptx::mma_commit_multicast(ptx::smem_addr(empty + s), 0x3);
+          if (++s == kPairN) { s = 0; ph ^= 1u; }
+          if (++set == kPairSets) { set = 0; sph ^= 1u; }
         }
-        if (!ok) break;
-        ptx::mma_commit_multicast(ptx::smem_addr(tfull + acc), 0x3);
       }
       if (issued && (!ok || *abort_flag)) {
-        ptx::mma_commit_pair(ptx::smem_addr(drain));
+        if (elected) ptx::mma_commit_pair(ptx::smem_addr(drain));
         bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
       }
     }
-  } else if (warp == 6) {
-    if (lane == 0 && leader) {
-      const int stages_total = (tiles - pair + npairs - 1) / npairs * kbn;
-      bool ok = true;
-      int it = 0;
-      for (; it < stages_total; ++it) {
-        const uint32_t s = it % kPairN, back = it - kPairSets;  // a set is free when the stage that had it last has been multiplied
-        if (!bounded_wait(ptx::smem_addr(full + s), (it / kPairN) & 1u, abort_flag, a.err, tmo) ||
-            (it >= kPairSets && !bounded_wait(ptx::smem_addr(empty + back % kPairN), (back / kPairN) & 1u, abort_flag, a.err, tmo))) {
-          ok = false;
-          break;
-        }
-        ptx::tc_fence_after();
-        const uint32_t sc = ptx::smem_addr(stages + s * kPairStage) + 2 * kPBytes;
-        const uint32_t ta = tmem + kPairScaleCol + it % kPairSets * 24, tb = ta + 8;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          copy_scales_pair(ta + u * 4, sc + u * kMxScaleTile);
-          copy_scales_pair(tb + u * 8, sc + kScaleBytes + u * kMxScaleTile);
-          copy_scales_pair(tb + u * 8 + 4, sc + 2 * kScaleBytes + u * kMxScaleTile);
-        }
-        ptx::mma_commit_pair(ptx::smem_addr(sfull + it % kPairSets));
+  } else if (warp >= 6) {
+    // ------------------------------------------------------------ scales
+    const uint32_t ready0 = ptx::smem_addr(sready), empty0 = ptx::smem_addr(empty);
+    const uint32_t sfull0 = ptx::mapa_shared(ptx::smem_addr(sfull), 0);
+    const uint32_t cols = tmem + ((uint32_t)((warp & 3) * 32) << 16) + kPairScaleCol;
+    const int total = (tiles - pair + npairs - 1) / npairs * kbn;
+    uint32_t s = 0, ph = 0, set = 0, back = 0, bph = 0;  // back: the stage whose products had the set last
+    for (int it = 0; it < total; ++it) {
+      if (it >= kPairSets) {
+        if (!bounded_wait_warp(empty0 + back * 8, bph, abort_flag, a.err, tmo)) break;
+        if (++back == kPairN) { back = 0; bph ^= 1u; }
       }
-      if (it > 0 && (!ok || *abort_flag)) {
-        ptx::mma_commit_pair(ptx::smem_addr(drain + 1));
-        bounded_wait_slow(ptx::smem_addr(drain + 1), 0, abort_flag, a.err, false, kWaitNs);
-      }
+      if (!bounded_wait_warp(ready0 + s * 8, ph, abort_flag, a.err, tmo)) break;
+      ptx::tc_fence_after();
+      const uint4* sc = reinterpret_cast<const uint4*>(stages + s * kPairStage + 2 * kPBytes) + lane;  // 32 x 16 bytes a tile
+      const uint32_t ta = cols + set * 24;
+      tmem_st8(ta, sc[0], sc[32]);             // A: first, second 128 elements of K
+      tmem_st8(ta + 8, sc[64], sc[128]);       // B, first 128 elements: rows 0-127, 128-255
+      tmem_st8(ta + 16, sc[96], sc[160]);      // B, second
+      asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_remote(sfull0 + set * 8);
+      if (++s == kPairN) { s = 0; ph ^= 1u; }
+      if (++set == kPairSets) set = 0;
     }
   } else {
     const int quad = warp & 3;
@@ -616,7 +646,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
     uint32_t tc = 0;
     for (int t = pair; t < tiles; t += npairs, ++tc) {
       const uint32_t acc = tc & 1u;
-      if (!bounded_wait(ptx::smem_addr(tfull + acc), (tc >> 1) & 1u, abort_flag, a.err, tmo)) break;
+      if (!bounded_wait_warp(ptx::smem_addr(tfull + acc), (tc >> 1) & 1u, abort_flag, a.err, tmo)) break;
       ptx::tc_fence_after();
       int mt, nt;
       tile_of(t, tm, tn, mt, nt);
