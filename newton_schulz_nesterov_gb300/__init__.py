@@ -78,7 +78,14 @@ class BlockNormGrad(ctypes.Structure):
 
 BACKENDS = {"direct": 0, "gram": 1}
 SCALE_MODES = {"floor": 0, "ceil": 1}
-_DTYPES = {"torch.float32": 0, "torch.bfloat16": 1, "torch.float16": 2}
+_TYPES = {}  # torch dtype -> type code of include/dmuon.h, filled with the first tensor
+
+
+def _types():
+    if not _TYPES:
+        import torch
+        _TYPES.update({torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.uint8: 3})
+    return _TYPES
 
 
 def lib_path():
@@ -456,27 +463,32 @@ def dmuon_clip_grad_norm(h, grads, max_norm, buckets=None, n_buckets=None, stats
 # ------------------------------------------- 4-bit projections and their norms
 
 def _matrix(t, name, dtype=None, shape=None):
-    """(pointer, leading dimension, type code) of a 2-D CUDA tensor whose rows
-    are contiguous; ``dtype`` and ``shape``, where given, have to match."""
-    code = _DTYPES.get(str(t.dtype))
-    if code is None or not t.is_cuda or t.dim() != 2 or (dtype is not None and code != dtype):
+    """(pointer, leading dimension, type code, shape) of a 2-D CUDA tensor whose
+    rows are contiguous; ``dtype`` and ``shape``, where given, have to match."""
+    code = (_TYPES or _types()).get(t.dtype, 3)
+    size = t.shape
+    if code > 2 or not t.is_cuda or len(size) != 2 or (dtype is not None and code != dtype):
         raise ValueError("%s: a 2-D CUDA tensor of float32, bfloat16 or float16%s is wanted"
                          % (name, "" if dtype is None else " (the type of the others)"))
-    rows, cols = t.shape
-    if shape is not None and (rows, cols) != shape:
-        raise ValueError("%s: shape %s, %s wanted" % (name, (rows, cols), shape))
+    if shape is not None and size != shape:
+        raise ValueError("%s: shape %s, %s wanted" % (name, tuple(size), tuple(shape)))
+    return t.data_ptr(), _pitch(t, size, name), code, size
+
+
+def _pitch(t, size, name):
+    rows, cols = size
     ld, inner = t.stride()
     if cols > 1 and inner != 1 or rows > 1 and ld < cols:
         raise ValueError("%s: rows must be contiguous and not overlap" % name)
-    return t.data_ptr(), (ld if rows > 1 else max(ld, cols)), code
+    return ld if rows > 1 else max(ld, cols)
 
 
 def _floats(t, name, shape):
     """Pointer of a contiguous fp32 CUDA tensor of ``shape``; None stays None."""
     if t is None:
         return None
-    if not t.is_cuda or str(t.dtype) != "torch.float32" or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError("%s: a contiguous float32 CUDA tensor of shape %s is wanted" % (name, shape))
+    if (_TYPES or _types()).get(t.dtype) != 0 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s: a contiguous float32 CUDA tensor of shape %s is wanted" % (name, tuple(shape)))
     return t.data_ptr()
 
 
@@ -484,11 +496,28 @@ def _mxfp4(q, name, rows, k):
     """(data pointer, scales pointer) of an MXFP4 matrix (data, scales)."""
     data, scales = q
     nb = -(-k // 32)
-    for t, want in ((data, rows * nb * 16), (scales, -(-rows // 128) * -(-nb // 4) * 512)):
-        if not t.is_cuda or str(t.dtype) != "torch.uint8" or not t.is_contiguous() or t.numel() != want:
-            raise ValueError("%s: contiguous uint8 CUDA tensors of the sizes dmuon_mxfp4_empty(%d, %d) gives are wanted"
-                             % (name, rows, k))
+    types = _TYPES or _types()
+    if (types.get(data.dtype) != 3 or types.get(scales.dtype) != 3 or data.numel() != rows * nb * 16 or
+            scales.numel() != -(-rows // 128) * -(-nb // 4) * 512 or not data.is_cuda or not scales.is_cuda or
+            not data.is_contiguous() or not scales.is_contiguous()):
+        raise ValueError("%s: contiguous uint8 CUDA tensors of the sizes dmuon_mxfp4_empty(%d, %d) gives are wanted"
+                         % (name, rows, k))
     return data.data_ptr(), scales.data_ptr()
+
+
+_raw_stream = None  # torch's current stream of a device as an integer
+
+
+def _stream_of(stream, t):
+    """Handle of ``stream``, or of the current stream of t's device."""
+    global _raw_stream
+    if stream is not None:
+        return _stream_handle(stream)
+    if _raw_stream is None:
+        import torch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+    return _raw_stream(t.get_device())
 
 
 def dmuon_mxfp4_bytes(rows, k):
@@ -510,65 +539,61 @@ def dmuon_mxfp4_quantize(h, src, by_rows=None, by_cols=None, noise=None, scale="
     """Quantise the matrix ``src`` [r, c] along its rows into ``by_rows`` (an
     r x c MXFP4 matrix) and / or along its columns into ``by_cols`` (c x r).
     ``noise``: uint8 [r, c] of random bytes for stochastic rounding."""
-    ptr, ld, code = _matrix(src, "src")
-    r, c = src.shape
+    ptr, ld, code, size = _matrix(src, "src")
+    r, c = size
     nptr, nld = None, 0
     if noise is not None:
-        if not noise.is_cuda or str(noise.dtype) != "torch.uint8" or noise.shape != src.shape:
+        if not noise.is_cuda or (_TYPES or _types()).get(noise.dtype) != 3 or noise.shape != size:
             raise ValueError("noise: a uint8 CUDA tensor of src's shape is wanted")
-        nld, inner = noise.stride()
-        if c > 1 and inner != 1 or r > 1 and nld < c:
-            raise ValueError("noise: rows must be contiguous and not overlap")
-        nptr, nld = noise.data_ptr(), nld if r > 1 else max(nld, c)
+        nptr, nld = noise.data_ptr(), _pitch(noise, size, "noise")
     rd, rs = (None, None) if by_rows is None else _mxfp4(by_rows, "by_rows", r, c)
     cd, cs = (None, None) if by_cols is None else _mxfp4(by_cols, "by_cols", c, r)
+    mode = SCALE_MODES[scale]
     if r == 0 or c == 0:
         return
-    _check(load().dmuon_mxfp4_quantize(h, ptr, code, r, c, ld, SCALE_MODES[scale], nptr, nld, rd, rs, cd, cs,
-                                       _stream_handle(stream)), "dmuon_mxfp4_quantize", h)
+    rc = load().dmuon_mxfp4_quantize(h, ptr, code, r, c, ld, mode, nptr, nld, rd, rs, cd, cs, _stream_of(stream, src))
+    if rc:
+        _check(rc, "dmuon_mxfp4_quantize", h)
 
 
 def dmuon_mxfp4_dequantize(h, q, out, stream=None):
     """The values of the MXFP4 matrix ``q`` into ``out`` [rows, k]."""
-    ptr, ld, code = _matrix(out, "out")
-    r, k = out.shape
+    ptr, ld, code, (r, k) = _matrix(out, "out")
     d, s = _mxfp4(q, "q", r, k)
     if r == 0 or k == 0:
         return
-    _check(load().dmuon_mxfp4_dequantize(h, d, s, r, k, ptr, code, ld, _stream_handle(stream)),
-           "dmuon_mxfp4_dequantize", h)
+    rc = load().dmuon_mxfp4_dequantize(h, d, s, r, k, ptr, code, ld, _stream_of(stream, out))
+    if rc:
+        _check(rc, "dmuon_mxfp4_dequantize", h)
 
 
 def dmuon_mxfp4_gemm(h, a, b, out, k, alpha=1.0, beta=0.0, stream=None):
     """out = alpha * a b^T + beta * out of MXFP4 matrices a [m, k] and
     b [n, k]; out is [m, n] in float32, bfloat16 or float16."""
-    ptr, ld, code = _matrix(out, "out")
-    m, n = out.shape
+    ptr, ld, code, (m, n) = _matrix(out, "out")
     ad, as_ = _mxfp4(a, "a", m, k)
     bd, bs = _mxfp4(b, "b", n, k)
     if m == 0 or n == 0:
         return
-    _check(load().dmuon_mxfp4_gemm(h, ad, as_, bd, bs, m, n, k, ptr, code, ld, alpha, beta, _stream_handle(stream)),
-           "dmuon_mxfp4_gemm", h)
+    rc = load().dmuon_mxfp4_gemm(h, ad, as_, bd, bs, m, n, k, ptr, code, ld, alpha, beta, _stream_of(stream, out))
+    if rc:
+        _check(rc, "dmuon_mxfp4_gemm", h)
 
 
-def _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale):
-    """The fields that forward and backward share; x may be None."""
-    p = BlockNorm()
-    p.f, p.ldf, code = _matrix(f, "f")
-    rows, cols = shape = tuple(f.shape)
-    p.rows, p.cols, p.dtype = rows, cols, code
-    if x is not None:
-        p.x, p.ldx, _ = _matrix(x, "x", code, shape)
-    p.y, p.ldy, _ = _matrix(y, "y", code, shape)
-    p.post_w, p.pre_w = _floats(post_w, "post_w", (cols,)), _floats(pre_w, "pre_w", (cols,))
+def _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, eps, out):
+    """The fields that forward and backward share; x and out may be None."""
+    fp, ldf, code, shape = _matrix(f, "f")
+    rows, cols = shape
+    xp, ldx = _matrix(x, "x", code, shape)[:2] if x is not None else (None, 0)
+    yp, ldy = _matrix(y, "y", code, shape)[:2]
+    hp, ldh = _matrix(out, "out", code, shape)[:2] if out is not None else (None, 0)
     per = max(1, rows) if rows_per_gate is None else int(rows_per_gate)
     if per < 1:
         raise ValueError("rows_per_gate must be at least 1")
-    p.gate, p.rows_per_gate = _floats(gate, "gate", (-(-rows // per), cols)), per
-    p.res_scale = _floats(res_scale, "res_scale", (cols,))
-    p.rstd = _floats(rstd, "rstd", (2, rows))
-    return p, code, shape
+    line = (cols,)
+    return BlockNorm(rows, cols, code, eps, xp, ldx, fp, ldf, _floats(post_w, "post_w", line), _floats(pre_w, "pre_w", line),
+                     _floats(gate, "gate", (-(-rows // per), cols)), per, _floats(res_scale, "res_scale", line), yp, ldy,
+                     hp, ldh, _floats(rstd, "rstd", (2, rows))), code, shape
 
 
 def dmuon_block_norm_forward(h, x, f, post_w, pre_w, y, out, rstd, gate=None, rows_per_gate=None, res_scale=None,
@@ -576,32 +601,30 @@ def dmuon_block_norm_forward(h, x, f, post_w, pre_w, y, out, rstd, gate=None, ro
     """y = res_scale * x + gate * rms(f) * post_w and out = rms(y) * pre_w over
     the rows of x and f [rows, cols]; rstd [2, rows] is what the backward needs.
     ``gate`` [ceil(rows / rows_per_gate), cols] (rows_per_gate None: one row for all)."""
-    p, code, shape = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale)
-    p.h, p.ldh, _ = _matrix(out, "out", code, shape)
-    p.eps = eps
-    _check(load().dmuon_block_norm_forward(h, ctypes.byref(p), _stream_handle(stream)), "dmuon_block_norm_forward", h)
+    p, _, _ = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, eps, out)
+    rc = load().dmuon_block_norm_forward(h, p, _stream_of(stream, f))
+    if rc:
+        _check(rc, "dmuon_block_norm_forward", h)
 
 
 def dmuon_block_norm_backward(h, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d_post_w, d_pre_w, gate=None,
                               d_gate=None, rows_per_gate=None, res_scale=None, d_res_scale=None, stream=None):
     """Gradients of dmuon_block_norm_forward from dh (of its out) and dy (of y,
     None = 0).  x may be None unless d_res_scale is wanted."""
-    p, code, shape = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale)
-    q = BlockNormGrad()
-    if dy is not None:
-        q.dy, q.lddy, _ = _matrix(dy, "dy", code, shape)
-    q.dh, q.lddh, _ = _matrix(dh, "dh", code, shape)
-    q.dx, q.lddx, _ = _matrix(dx, "dx", code, shape)
-    q.df, q.lddf, _ = _matrix(df, "df", code, shape)
-    cols = shape[1]
-    q.d_post_w, q.d_pre_w = _floats(d_post_w, "d_post_w", (cols,)), _floats(d_pre_w, "d_pre_w", (cols,))
-    if d_gate is not None:
-        if gate is None:
-            raise ValueError("d_gate without a gate")
-        q.d_gate = _floats(d_gate, "d_gate", tuple(gate.shape))
-    q.d_res_scale = _floats(d_res_scale, "d_res_scale", (cols,))
-    _check(load().dmuon_block_norm_backward(h, ctypes.byref(p), ctypes.byref(q), _stream_handle(stream)),
-           "dmuon_block_norm_backward", h)
+    p, code, shape = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, 0.0, None)
+    if d_gate is not None and gate is None:
+        raise ValueError("d_gate without a gate")
+    dyp, lddy = _matrix(dy, "dy", code, shape)[:2] if dy is not None else (None, 0)
+    dhp, lddh = _matrix(dh, "dh", code, shape)[:2]
+    dxp, lddx = _matrix(dx, "dx", code, shape)[:2]
+    dfp, lddf = _matrix(df, "df", code, shape)[:2]
+    line = (shape[1],)
+    q = BlockNormGrad(dyp, lddy, dhp, lddh, dxp, lddx, dfp, lddf, _floats(d_post_w, "d_post_w", line),
+                      _floats(d_pre_w, "d_pre_w", line), None if d_gate is None else _floats(d_gate, "d_gate", gate.shape),
+                      _floats(d_res_scale, "d_res_scale", line))
+    rc = load().dmuon_block_norm_backward(h, p, q, _stream_of(stream, f))
+    if rc:
+        _check(rc, "dmuon_block_norm_backward", h)
 
 
 def dmuon_get_status(h, n_flags=0):

@@ -130,7 +130,7 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
 
 // ------------------------------------------------------------ geometry
 
-constexpr int kScratch = 32 * 17;  // words of an epilogue warp's transposing scratch
+constexpr int kScratch = 32 * 20;  // words of an epilogue warp's transposing scratch
 
 template <int NT>
 struct Cfg {
@@ -210,49 +210,81 @@ struct Pack<__half> {
 };
 
 // 32 columns of D from one row a lane: rows row0 + lane, columns col0 ..
-// Aligned rows (a.vec) that are whole go out as 32-byte stores; the others
-// pass through the warp's scratch (32 x 17 words) so that the lanes of a
-// store cover consecutive columns.
+//   beta = 0, aligned whole rows (a.vec): 32-byte stores, one row a lane
+//   beta != 0, aligned: through the warp's scratch, 16 columns at a time, so
+//     that the lanes of a 16-byte access cover whole rows (a row a lane touches
+//     32 lines an access; reading D that way took the epilogue longer than the
+//     products: 187 us against 140 at 14336 x 4096 x 8192 in fp32); all of the old D
+//     is loaded before any is used
+//   else: through the scratch, one element a lane
 template <typename T>
 __device__ __forceinline__ void store_block(const MxGemmArgs& a, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
                                             const uint32_t* v, uint32_t* scratch, int lane) {
-  constexpr int kWords = 32 / Pack<T>::kPer;
+  constexpr int kPer = Pack<T>::kPer, kWords = 32 / kPer;
   T* d = (T*)a.d;
-  if (a.vec && col0 + 32 <= cols) {
+  const bool whole = a.vec && col0 + 32 <= cols;
+  if (whole && a.beta == 0.f) {
     if (row0 + lane >= rows) return;
     T* dst = d + (row0 + lane) * a.ldd + col0;
     uint32_t w[kWords];
-    if (a.beta != 0.f) {
-#pragma unroll
-      for (int q = 0; q < kWords / 4; ++q) {
-        const uint4 o = reinterpret_cast<const uint4*>(dst)[q];
-        w[4 * q] = o.x; w[4 * q + 1] = o.y; w[4 * q + 2] = o.z; w[4 * q + 3] = o.w;
-      }
-    }
 #pragma unroll
     for (int q = 0; q < kWords; ++q) {
-      float f[2], o[2];
-      if (a.beta != 0.f) Pack<T>::unpack(w[q], o);
+      float f[2];
 #pragma unroll
-      for (int k = 0; k < Pack<T>::kPer; ++k) {
-        f[k] = a.alpha * __uint_as_float(v[q * Pack<T>::kPer + k]);
-        if (a.beta != 0.f) f[k] = fmaf(a.beta, o[k], f[k]);
-      }
+      for (int k = 0; k < kPer; ++k) f[k] = a.alpha * __uint_as_float(v[q * kPer + k]);
       w[q] = Pack<T>::pack(f);
     }
 #pragma unroll
     for (int q = 0; q < kWords / 8; ++q) ptx::st_global_v8(reinterpret_cast<uint32_t*>(dst) + 8 * q, w + 8 * q);
-    return;
-  }
+  } else if (whole) {
+    constexpr int kLanes = 4 / kPer, kRows = 32 / kLanes, kAcc = 32 / kRows;  // lanes a row, rows and accesses a half
+    const int lr = lane / kLanes, lc = lane % kLanes;
+    uint4 old[2][kAcc];
+    T* dst[2][kAcc];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
-    for (int j = 0; j < 16; ++j) scratch[lane * 17 + j] = v[half * 16 + j];
-    __syncwarp();
-    const int64_t col = col0 + half * 16 + (lane & 15);
-    for (int r = lane >> 4; r < 32; r += 2)
-      if (row0 + r < rows && col < cols) put<T>(a, d + (row0 + r) * a.ldd + col, __uint_as_float(scratch[r * 17 + (lane & 15)]));
-    __syncwarp();
+      for (int q = 0; q < kAcc; ++q) {
+        const int64_t r = row0 + q * kRows + lr;
+        dst[half][q] = d + r * a.ldd + col0 + half * 16 + lc * 4 * kPer;
+        old[half][q] = r < rows ? *reinterpret_cast<const uint4*>(dst[half][q]) : make_uint4(0, 0, 0, 0);
+      }
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<uint4*>(scratch + lane * 20 + 4 * q) =
+            make_uint4(v[half * 16 + 4 * q], v[half * 16 + 4 * q + 1], v[half * 16 + 4 * q + 2], v[half * 16 + 4 * q + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kAcc; ++q) {
+        const int r = q * kRows + lr;
+        uint32_t w[4] = {old[half][q].x, old[half][q].y, old[half][q].z, old[half][q].w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float f[2], o[2];
+          Pack<T>::unpack(w[k], o);
+#pragma unroll
+          for (int e = 0; e < kPer; ++e)
+            f[e] = fmaf(a.beta, o[e], a.alpha * __uint_as_float(scratch[r * 20 + (lc * 4 + k) * kPer + e]));
+          w[k] = Pack<T>::pack(f);
+        }
+        if (row0 + r < rows) *reinterpret_cast<uint4*>(dst[half][q]) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+    }
+  } else {
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) scratch[lane * 20 + j] = v[half * 16 + j];
+      __syncwarp();
+      const int64_t col = col0 + half * 16 + (lane & 15);
+      for (int r = lane >> 4; r < 32; r += 2)
+        if (row0 + r < rows && col < cols)
+          put<T>(a, d + (row0 + r) * a.ldd + col, __uint_as_float(scratch[r * 20 + (lane & 15)]));
+      __syncwarp();
+    }
   }
 }
 
@@ -646,11 +678,19 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
     uint32_t tc = 0;
     for (int t = pair; t < tiles; t += npairs, ++tc) {
       const uint32_t acc = tc & 1u;
-      if (!bounded_wait_warp(ptx::smem_addr(tfull + acc), (tc >> 1) & 1u, abort_flag, a.err, tmo)) break;
-      ptx::tc_fence_after();
       int mt, nt;
       tile_of(t, tm, tn, mt, nt);
       const int64_t row0 = (int64_t)mt * 256 + rank * 128 + quad * 32, col0 = (int64_t)nt * 256;
+      if (a.beta != 0.f && a.vec && row0 + lane < a.p_rows) {
+        // The tile's old D comes to L2 while its products run (whole rows of
+        // it: D's rows are 32-byte aligned).
+        const uint32_t bytes = (uint32_t)min((int64_t)256, a.q_rows - col0) * (uint32_t)sizeof(T) & ~15u;
+        if (bytes)
+          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((const T*)a.d + (row0 + lane) * a.ldd + col0), "r"(bytes)
+                       : "memory");
+      }
+      if (!bounded_wait_warp(ptx::smem_addr(tfull + acc), (tc >> 1) & 1u, abort_flag, a.err, tmo)) break;
+      ptx::tc_fence_after();
       const uint32_t tq = tmem + acc * kAccStride + ((uint32_t)(quad * 32) << 16);
       {  // the shared columns first: the last 96 of accumulator 0, the first of 1
         const int c = acc ? 0 : kAccStride;
