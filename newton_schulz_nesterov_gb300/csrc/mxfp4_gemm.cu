@@ -130,7 +130,7 @@ __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
 
 // ------------------------------------------------------------ geometry
 
-constexpr int kScratch = 32 * 20;  // words of an epilogue warp's transposing scratch
+constexpr int kScratch = 32 * 36;  // words of an epilogue warp's transposing scratch
 
 template <int NT>
 struct Cfg {
@@ -210,82 +210,73 @@ struct Pack<__half> {
 };
 
 // 32 columns of D from one row a lane: rows row0 + lane, columns col0 ..
-//   beta = 0, aligned whole rows (a.vec): 32-byte stores, one row a lane
-//   beta != 0, aligned: through the warp's scratch, 16 columns at a time, so
-//     that the lanes of a 16-byte access cover whole rows (a row a lane touches
-//     32 lines an access; reading D that way took the epilogue longer than the
-//     products: 187 us against 140 at 14336 x 4096 x 8192 in fp32); all of the old D
-//     is loaded before any is used
-//   else: through the scratch, one element a lane
+// The block passes through the warp's scratch so that the lanes of an access
+// cover whole rows: with a row a lane an access touches 32 lines, and at
+// 14336 x 4096 x 8192 in fp32 the stores took 33 us of 154, reading D another 20.
+// Rows 16 (packed, beta = 0) or 32 words long are kept 4 words apart, so that
+// 16-byte accesses by rows and by columns of lanes fall on distinct banks.
 template <typename T>
 __device__ __forceinline__ void store_block(const MxGemmArgs& a, int64_t row0, int64_t col0, int64_t rows, int64_t cols,
                                             const uint32_t* v, uint32_t* scratch, int lane) {
   constexpr int kPer = Pack<T>::kPer, kWords = 32 / kPer;
+  constexpr int kLanes = kWords / 4, kRows = 32 / kLanes;  // lanes a row, rows an access of 16 bytes a lane
   T* d = (T*)a.d;
-  const bool whole = a.vec && col0 + 32 <= cols;
-  if (whole && a.beta == 0.f) {
-    if (row0 + lane >= rows) return;
-    T* dst = d + (row0 + lane) * a.ldd + col0;
-    uint32_t w[kWords];
-#pragma unroll
-    for (int q = 0; q < kWords; ++q) {
-      float f[2];
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) f[k] = a.alpha * __uint_as_float(v[q * kPer + k]);
-      w[q] = Pack<T>::pack(f);
-    }
-#pragma unroll
-    for (int q = 0; q < kWords / 8; ++q) ptx::st_global_v8(reinterpret_cast<uint32_t*>(dst) + 8 * q, w + 8 * q);
-  } else if (whole) {
-    constexpr int kLanes = 4 / kPer, kRows = 32 / kLanes, kAcc = 32 / kRows;  // lanes a row, rows and accesses a half
+  if (a.vec && col0 + 32 <= cols) {
     const int lr = lane / kLanes, lc = lane % kLanes;
-    uint4 old[2][kAcc];
-    T* dst[2][kAcc];
+    T* dst = d + (row0 + lr) * a.ldd + col0 + lc * 4 * kPer;
+    const int64_t step = (int64_t)kRows * a.ldd;
+    if (a.beta == 0.f) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+      for (int q = 0; q < kLanes; ++q) {
+        uint32_t w[4];
 #pragma unroll
-      for (int q = 0; q < kAcc; ++q) {
-        const int64_t r = row0 + q * kRows + lr;
-        dst[half][q] = d + r * a.ldd + col0 + half * 16 + lc * 4 * kPer;
-        old[half][q] = r < rows ? *reinterpret_cast<const uint4*>(dst[half][q]) : make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < 4; ++k) {
+          float f[2];
+#pragma unroll
+          for (int e = 0; e < kPer; ++e) f[e] = a.alpha * __uint_as_float(v[(q * 4 + k) * kPer + e]);
+          w[k] = Pack<T>::pack(f);
+        }
+        *reinterpret_cast<uint4*>(scratch + lane * (kWords + 4) + q * 4) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<uint4*>(scratch + lane * 20 + 4 * q) =
-            make_uint4(v[half * 16 + 4 * q], v[half * 16 + 4 * q + 1], v[half * 16 + 4 * q + 2], v[half * 16 + 4 * q + 3]);
       __syncwarp();
 #pragma unroll
-      for (int q = 0; q < kAcc; ++q) {
-        const int r = q * kRows + lr;
-        uint32_t w[4] = {old[half][q].x, old[half][q].y, old[half][q].z, old[half][q].w};
+      for (int q = 0; q < kLanes; ++q) {
+        const uint4 w = *reinterpret_cast<const uint4*>(scratch + (q * kRows + lr) * (kWords + 4) + lc * 4);
+        if (row0 + q * kRows + lr < rows) *reinterpret_cast<uint4*>(dst + q * step) = w;
+      }
+    } else {
+      uint4 old[kLanes];
+#pragma unroll
+      for (int q = 0; q < kLanes; ++q)
+        old[q] = row0 + q * kRows + lr < rows ? *reinterpret_cast<const uint4*>(dst + q * step) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(scratch + lane * 36 + q * 4) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kLanes; ++q) {
+        const uint32_t* acc = scratch + (q * kRows + lr) * 36 + lc * 4 * kPer;
+        uint32_t w[4] = {old[q].x, old[q].y, old[q].z, old[q].w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           float f[2], o[2];
           Pack<T>::unpack(w[k], o);
 #pragma unroll
-          for (int e = 0; e < kPer; ++e)
-            f[e] = fmaf(a.beta, o[e], a.alpha * __uint_as_float(scratch[r * 20 + (lc * 4 + k) * kPer + e]));
+          for (int e = 0; e < kPer; ++e) f[e] = fmaf(a.beta, o[e], a.alpha * __uint_as_float(acc[k * kPer + e]));
           w[k] = Pack<T>::pack(f);
         }
-        if (row0 + r < rows) *reinterpret_cast<uint4*>(dst[half][q]) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (row0 + q * kRows + lr < rows) *reinterpret_cast<uint4*>(dst + q * step) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      __syncwarp();
     }
   } else {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-#pragma unroll
-      for (int j = 0; j < 16; ++j) scratch[lane * 20 + j] = v[half * 16 + j];
-      __syncwarp();
-      const int64_t col = col0 + half * 16 + (lane & 15);
-      for (int r = lane >> 4; r < 32; r += 2)
-        if (row0 + r < rows && col < cols)
-          put<T>(a, d + (row0 + r) * a.ldd + col, __uint_as_float(scratch[r * 20 + (lane & 15)]));
-      __syncwarp();
-    }
+    for (int j = 0; j < 32; ++j) scratch[lane * 33 + j] = v[j];
+    __syncwarp();
+    const int64_t col = col0 + lane;
+    for (int r = 0; r < 32; ++r)
+      if (row0 + r < rows && col < cols) put<T>(a, d + (row0 + r) * a.ldd + col, __uint_as_float(scratch[r * 33 + lane]));
   }
+  __syncwarp();
 }
 
 template <int NT, typename T>
@@ -472,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 constexpr int kPairScales = kScaleBytes * 3;              // A's 128 rows, B's 256
 constexpr int kPairStage = 2 * kPBytes + kPairScales;     // 35 KB
-constexpr int kPairN = 6;
+constexpr int kPairN = 5;
 constexpr int kPairSmem = 1024 + kPairN * kPairStage + 4 * kScratch * 4 + 256;
 constexpr int kPairThreads = 320;
 constexpr int kAccStride = 160, kPairScaleCol = 416, kPairSets = 4;
