@@ -25,6 +25,9 @@ int elem_size(int dtype) {
 
 bool aligned(const void* p, int bytes) { return ((uintptr_t)p & (uintptr_t)(bytes - 1)) == 0; }
 
+// Every row starts on 16 bytes.
+bool rows_aligned(const void* p, int64_t ld, int dtype) { return aligned(p, 16) && (ld * elem_size(dtype)) % 16 == 0; }
+
 // A rows x cols matrix of `dtype` at p with leading dimension ld: DMUON_OK or
 // the error code (also recorded).
 int check_matrix(dmuon_ctx* h, const void* p, int dtype, int64_t cols, int64_t ld, const char* what) {
@@ -244,6 +247,8 @@ int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p, void
   a.ldh = p->ldh;
   a.per_gate = p->rows_per_gate;
   a.eps = p->eps;
+  a.vec = cols % 8 == 0 && rows_aligned(p->x, p->ldx, p->dtype) && rows_aligned(p->f, p->ldf, p->dtype) &&
+          rows_aligned(p->y, p->ldy, p->dtype) && rows_aligned(p->h, p->ldh, p->dtype);
   LaunchGuard g(h, stream, DMUON_KIND_NORM_FWD);
   const cudaError_t e = launch_norm_fwd(a, p->dtype, h->num_sms, stream);
   if (e != cudaSuccess) return fail(h, cuda_err(e), "block_norm_forward launch", e);
@@ -313,12 +318,20 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   a.lddf = q->lddf;
   a.per_gate = p->gate ? std::min(p->rows_per_gate, std::max<int64_t>(rows, 1)) : std::max<int64_t>(rows, 1);
   a.groups = (rows + a.per_gate - 1) / a.per_gate;
-  a.ctas = norm_bwd_ctas(cols, h->num_sms);
-  a.chunk_rows = std::min(a.per_gate, std::max<int64_t>(1, (rows + a.ctas - 1) / a.ctas));
+  a.units = norm_bwd_units(rows, cols, h->num_sms);
+  // Chunks lie inside a group; no more of them than units where that can be,
+  // so that no unit has two while another has one.
+  a.chunks_per_group = std::max<int64_t>(1, std::min(a.per_gate, a.units / std::max<int64_t>(1, a.groups)));
+  a.chunk_rows = (a.per_gate + a.chunks_per_group - 1) / a.chunks_per_group;
   a.chunks_per_group = (a.per_gate + a.chunk_rows - 1) / a.chunk_rows;
+  a.vec = cols % 8 == 0;
+  const struct { const void* p; int64_t ld; } mats[] = {{q->dy, q->lddy}, {q->dh, q->lddh}, {q->d_res_scale ? p->x : nullptr, p->ldx},
+                                                        {p->f, p->ldf}, {p->y, p->ldy}, {q->dx, q->lddx}, {q->df, q->lddf}};
+  for (const auto& m : mats)
+    if (m.p && !rows_aligned(m.p, m.ld, p->dtype)) a.vec = 0;
   const size_t line = (size_t)cols * 4;
   const bool gate_parts = q->d_gate && a.chunks_per_group > 1;
-  const size_t need = line * ((size_t)a.ctas * (q->d_res_scale ? 3 : 2) +
+  const size_t need = line * ((size_t)a.units * (q->d_res_scale ? 3 : 2) +
                               (gate_parts ? (size_t)(a.groups * a.chunks_per_group) : 0));
   if (h->op_ws_cap < need) {
     if (capturing(stream)) return fail(h, DMUON_ERR_ARG, "block_norm_backward: first call of this size under capture");
@@ -338,9 +351,9 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   }
   float* w = (float*)h->op_ws;
   a.part_pre = w;
-  a.part_post = w + (size_t)a.ctas * cols;
-  a.part_res = a.part_post + (size_t)a.ctas * cols;
-  a.part_gate = a.part_post + (size_t)a.ctas * cols * (q->d_res_scale ? 2 : 1);
+  a.part_post = w + (size_t)a.units * cols;
+  a.part_res = a.part_post + (size_t)a.units * cols;
+  a.part_gate = a.part_post + (size_t)a.units * cols * (q->d_res_scale ? 2 : 1);
   LaunchGuard g(h, stream, DMUON_KIND_NORM_BWD);
   ++h->launches;  // rows, then column sums
   const cudaError_t e = launch_norm_bwd(a, p->dtype, stream);

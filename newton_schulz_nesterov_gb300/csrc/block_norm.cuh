@@ -24,6 +24,7 @@ struct NormFwdArgs {
   float* rstd;                                // [2][rows]
   int64_t rows, cols, ldx, ldf, ldy, ldh, per_gate;
   float eps;
+  int vec;                                    // 16-byte aligned rows, columns a multiple of 8
 };
 
 // Rows are cut into chunks that lie inside one gate group, so that a chunk's
@@ -35,14 +36,15 @@ struct NormBwdArgs {
   float *d_post_w, *d_pre_w, *d_gate, *d_res;  // d_gate, d_res may be nullptr
   int64_t rows, cols, lddy, lddh, ldx, ldf, ldy, lddx, lddf, per_gate;
   int64_t groups, chunk_rows, chunks_per_group;
-  int ctas;                                   // rows of each partial array
-  float *part_pre, *part_post, *part_res;     // [ctas][cols]
+  int64_t units;                              // rows of each partial array
+  int vec;
+  float *part_pre, *part_post, *part_res;     // [units][cols]
   float* part_gate;                           // [groups * chunks_per_group][cols] (several chunks a group)
 };
 
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, cudaStream_t s);
-// CTAs of the backward pass for this many columns.
-int norm_bwd_ctas(int64_t cols, int sms);
+// Row units of the backward pass: each writes one row of the partial arrays.
+int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms);
 
 }  // namespace dmuon
