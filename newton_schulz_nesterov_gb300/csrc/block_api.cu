@@ -248,7 +248,8 @@ int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p, void
   a.per_gate = p->rows_per_gate;
   a.eps = p->eps;
   a.vec = cols % 8 == 0 && rows_aligned(p->x, p->ldx, p->dtype) && rows_aligned(p->f, p->ldf, p->dtype) &&
-          rows_aligned(p->y, p->ldy, p->dtype) && rows_aligned(p->h, p->ldh, p->dtype);
+          rows_aligned(p->y, p->ldy, p->dtype) && rows_aligned(p->h, p->ldh, p->dtype) && aligned(p->post_w, 16) &&
+          aligned(p->pre_w, 16) && aligned(p->gate, 16) && aligned(p->res_scale, 16);
   LaunchGuard g(h, stream, DMUON_KIND_NORM_FWD);
   const cudaError_t e = launch_norm_fwd(a, p->dtype, h->num_sms, stream);
   if (e != cudaSuccess) return fail(h, cuda_err(e), "block_norm_forward launch", e);
@@ -329,6 +330,9 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
                                                         {p->f, p->ldf}, {p->y, p->ldy}, {q->dx, q->lddx}, {q->df, q->lddf}};
   for (const auto& m : mats)
     if (m.p && !rows_aligned(m.p, m.ld, p->dtype)) a.vec = 0;
+  for (const void* v : {(const void*)p->post_w, (const void*)p->pre_w, (const void*)p->gate, (const void*)p->res_scale,
+                        (const void*)q->d_gate})
+    if (!aligned(v, 16)) a.vec = 0;
   const size_t line = (size_t)cols * 4;
   const bool gate_parts = q->d_gate && a.chunks_per_group > 1;
   const size_t need = line * ((size_t)a.units * (q->d_res_scale ? 3 : 2) +

@@ -37,179 +37,263 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 
 // ------------------------------------------------------------ rows up to 32768 columns
 //
-// A row is held by a unit of threads, eight columns a thread, so that it is
-// read once: up to 4096 columns by one unit of a CTA (several units when rows
-// are short), longer rows by a cluster of CTAs with 4096 columns each, whose
+// A row is held by a unit of threads, two chunks of eight columns a thread, so
+// that it is read once.  Rows too long for a CTA go to a cluster of CTAs whose
 // row sums meet in distributed shared memory.  Both kernels are bound by HBM;
 // a thread copies its own columns of the coming rows into a private ring in
-// shared memory (cp.async: no registers, no barrier, kRing rows ahead) and
-// keeps its columns' weights, gate row and column sums in registers over a
-// run of consecutive rows.
+// shared memory (cp.async: no registers, no barrier) and keeps its columns'
+// weights, gate row and column sums in registers over consecutive rows.
+// Beside its traffic a row costs issue slots and the latency of its sums.  At
+// 16384 x 4096 bf16 the forward took 172 us with one chunk a thread (every
+// second instruction belongs to sums and loops) and 137 us with four and the
+// weights from L1.
 //
-// VEC: eight consecutive columns a thread, 16-byte accesses (every row 16-byte
-// aligned, columns a multiple of 8).  Otherwise columns a unit apart, so that
-// the scalar accesses of a warp are consecutive, loaded without the ring.
-constexpr int kMaxThreads = 512;
-constexpr int kPerThread = 8;
-constexpr int64_t kCtaCols = (int64_t)kMaxThreads * kPerThread;
+// VEC: chunks of eight consecutive columns, 16-byte accesses (every row and
+// parameter 16-byte aligned, columns a multiple of 8).  Otherwise columns a
+// unit apart, so that the scalar accesses of a warp are consecutive, loaded
+// without the ring.
+constexpr int V = 2;                             // chunks of eight columns a thread
+constexpr int kFwdThreads = 512, kBwdThreads = 256;  // of an SM: 128 and 255 registers a thread
 constexpr int kMaxCluster = 8;
 
 struct RowUnit {
   int tpr;        // threads of a unit
   int unit, t;    // this thread's unit in the CTA and place in it
   int warps;      // of a unit
-  int64_t col0, cols;  // columns of this CTA: [col0, col0 + cols)
+  int col0, cols; // columns of this CTA: [col0, col0 + cols)
 };
 
 __device__ __forceinline__ RowUnit row_unit(int64_t cols, int tpr) {
   RowUnit u;
-  const uint32_t rank = ptx::cluster_ctarank();
   u.tpr = tpr;
   u.unit = threadIdx.x / tpr;
   u.t = threadIdx.x % tpr;
   u.warps = tpr / 32;
-  u.col0 = rank * kCtaCols;
-  u.cols = min(kCtaCols, cols - u.col0);
+  u.col0 = (int)ptx::cluster_ctarank() * tpr * V * 8;
+  u.cols = max(0, min(tpr * V * 8, (int)cols - u.col0));
   return u;
 }
 
+// Column of value e of chunk v, in the CTA.
 template <bool VEC>
-__device__ __forceinline__ int64_t col_of(const RowUnit& u, int e) {
-  return VEC ? u.t * kPerThread + e : (int64_t)e * u.tpr + u.t;
+__device__ __forceinline__ int col_of(const RowUnit& u, int v, int e) {
+  return VEC ? (v * u.tpr + u.t) * 8 + e : (v * 8 + e) * u.tpr + u.t;
 }
 
-// Sums of N <= 4 values over a row's threads, in a fixed order, to all of them.
+// Sums of N values over a row's threads, in a fixed order, to all of them.
 // One barrier: consecutive calls alternate between two halves of `red`
-// ([2][units][kMaxCluster * 16] float4), and a half is written again only
-// after the next call's barrier, when every thread has read it.
+// ([2][units][3][kRedRow] floats), and a half is written again only after the
+// next call's barrier, when every thread has read it.
+constexpr int kRedRow = kMaxCluster * 16;  // warps of a row at most
 template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, float4* red, int& half, uint32_t clusters) {
+__device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, float* red, int& half, int clusters) {
 #pragma unroll
-  for (int k = 0; k < N; ++k)
+  for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if (clusters == 1 && u.warps == 1) return;
-  const int units = blockDim.x / u.tpr;
-  float4* mine = red + (half * units + u.unit) * (clusters == 1 ? 16 : kMaxCluster * 16);
+  const int lane = threadIdx.x & 31, warp = u.t >> 5;
+  float* mine = red + (half * (int)(blockDim.x / u.tpr) + u.unit) * 3 * kRedRow;
   half ^= 1;
-  const int warp = u.t >> 5;
-  const float4 w = make_float4(v[0], N > 1 ? v[N > 1 ? 1 : 0] : 0.f, N > 2 ? v[N > 2 ? 2 : 0] : 0.f, N > 3 ? v[N > 3 ? 3 : 0] : 0.f);
   int n = u.warps;
   if (clusters == 1) {
-    if ((u.t & 31) == 0) mine[warp] = w;
+    if (lane == 0)
+#pragma unroll
+      for (int k = 0; k < N; ++k) mine[k * kRedRow + warp] = v[k];
     asm volatile("bar.sync %0, %1;" ::"r"(u.unit + 1), "r"(u.tpr) : "memory");
   } else {
-    n = u.warps * (int)clusters;
-    const uint32_t rank = ptx::cluster_ctarank();
-    if ((u.t & 31) < (int)clusters) {  // lane r tells rank r
-      const uint32_t at = ptx::mapa_shared(ptx::smem_addr(mine + rank * u.warps + warp), u.t & 31);
-      asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(w.x), "f"(w.y), "f"(w.z), "f"(w.w) : "memory");
+    n = u.warps * clusters;
+    if (lane < clusters) {  // lane r tells rank r
+      const uint32_t rank = ptx::cluster_ctarank();
+#pragma unroll
+      for (int k = 0; k < N; ++k)
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                         ptx::mapa_shared(ptx::smem_addr(mine + k * kRedRow + rank * u.warps + warp), lane)),
+                     "f"(v[k])
+                     : "memory");
     }
     ptx::cluster_sync();
   }
+  if (n <= 4) {
 #pragma unroll
-  for (int k = 0; k < N; ++k) v[k] = 0.f;
-  for (int i = 0; i < n; ++i) {
-    const float4 p = mine[i];
-    const float q[4] = {p.x, p.y, p.z, p.w};
-#pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += q[k];
+    for (int k = 0; k < N; ++k) {
+      const float4 p = *reinterpret_cast<const float4*>(mine + k * kRedRow);
+      v[k] = p.x + (n > 1 ? p.y : 0.f) + ((n > 2 ? p.z : 0.f) + (n > 3 ? p.w : 0.f));
+    }
+    return;
   }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    v[k] = 0.f;
+    for (int i = lane; i < n; i += 32) v[k] += mine[k * kRedRow + i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
 }
 
-// This thread's eight values of one row.
+// Two fp32 values in one 64-bit register, for the packed fp32 instructions.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 pack2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
+__device__ __forceinline__ float2 unpack2(f2 v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float add_up(f2 v) {
+  const float2 p = unpack2(v);
+  return p.x + p.y;
+}
+
+// A chunk: eight values of one row in their type.
 template <typename T>
-struct Row8 {
+struct Chunk8 {
   uint32_t w[sizeof(T) * 2];
-  __device__ __forceinline__ float at(int e) const {
-    if constexpr (sizeof(T) == 4) return __uint_as_float(w[e]);
-    const uint32_t p = w[e >> 1];
+  __device__ __forceinline__ f2 pair(int i) const {  // values 2i, 2i + 1
+    if constexpr (sizeof(T) == 4) return pack2(__uint_as_float(w[2 * i]), __uint_as_float(w[2 * i + 1]));
     if constexpr (std::is_same<T, __half>::value) {
-      const __half2 h = *reinterpret_cast<const __half2*>(&p);
-      return (e & 1) ? __high2float(h) : __low2float(h);
-    } else {
-      return __uint_as_float((e & 1) ? (p & 0xFFFF0000u) : (p << 16));
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+      return pack2(f.x, f.y);
     }
+    return pack2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(T) * 2); ++i) w[i] = 0;
   }
 };
 
-constexpr int chunks_of(int size) { return size * kPerThread / 16; }  // 16-byte chunks a thread and row
+constexpr int parts_of(int size) { return size / 2; }  // 16-byte parts of a chunk
 
+// `row` is the first of this CTA's columns, here and below.
 template <typename T, bool VEC>
-__device__ __forceinline__ Row8<T> load_direct(const T* row, const RowUnit& u) {
-  Row8<T> r;
+__device__ __forceinline__ Chunk8<T> load_direct(const T* row, const RowUnit& u, int v) {
+  Chunk8<T> r;
+  r.zero();
 #pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) * 2); ++i) r.w[i] = 0;
-#pragma unroll
-  for (int e = 0; e < kPerThread; ++e) {
-    const int64_t c = col_of<VEC>(u, e);
+  for (int e = 0; e < 8; ++e) {
+    const int c = col_of<VEC>(u, v, e);
     if (c >= u.cols) continue;
-    if constexpr (sizeof(T) == 4) r.w[e] = reinterpret_cast<const uint32_t*>(row)[u.col0 + c];
-    else r.w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[u.col0 + c] << (16 * (e & 1));
+    if constexpr (sizeof(T) == 4) r.w[e] = reinterpret_cast<const uint32_t*>(row)[c];
+    else r.w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c] << (16 * (e & 1));
   }
   return r;
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_row(T* row, const RowUnit& u, const float (&v)[kPerThread]) {
+__device__ __forceinline__ void store_chunk(T* row, const RowUnit& u, int v, const f2 (&val)[4]) {
+  float o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack2(val[i]);
+    o[2 * i] = p.x;
+    o[2 * i + 1] = p.y;
+  }
   if constexpr (VEC) {
-    if (u.t * kPerThread >= u.cols) return;
-    __align__(16) T o[kPerThread];
+    const int c = col_of<VEC>(u, v, 0);
+    if (c >= u.cols) return;
+    uint4* dst = reinterpret_cast<uint4*>(row + c);
+    if constexpr (sizeof(T) == 4) {
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) o[e] = narrow<T>(v[e]);
-    uint4* dst = reinterpret_cast<uint4*>(row + u.col0 + u.t * kPerThread);
+      for (int i = 0; i < 2; ++i)
+        dst[i] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
+                            __float_as_uint(o[4 * i + 3]));
+    } else {
+      uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < chunks_of(sizeof(T)); ++i) dst[i] = reinterpret_cast<const uint4*>(o)[i];
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (std::is_same<T, __half>::value) {
+          const __half2 h = __floats2half2_rn(o[2 * i], o[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+          w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+      }
+      *dst = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   } else {
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      const int64_t c = col_of<VEC>(u, e);
-      if (c < u.cols) row[u.col0 + c] = narrow<T>(v[e]);
+    for (int e = 0; e < 8; ++e) {
+      const int c = col_of<VEC>(u, v, e);
+      if (c < u.cols) row[c] = narrow<T>(o[e]);
     }
   }
 }
 
-// A parameter's (fp32, per column) eight values; absent: `other`.
+// Eight fp32 values of a parameter (its first column is column 0 of the row);
+// 0 past the columns.
 template <bool VEC>
-__device__ __forceinline__ void load_param(float (&v)[kPerThread], const float* p, const RowUnit& u, float other) {
+__device__ __forceinline__ void load_param(f2 (&val)[4], const float* p, const RowUnit& u, int v) {
+  p += u.col0;
+  if constexpr (VEC) {
+    const int c = col_of<VEC>(u, v, 0);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
+    if (c < u.cols) {
+      a = *reinterpret_cast<const float4*>(p + c);
+      b = *reinterpret_cast<const float4*>(p + c + 4);
+    }
+    val[0] = pack2(a.x, a.y);
+    val[1] = pack2(a.z, a.w);
+    val[2] = pack2(b.x, b.y);
+    val[3] = pack2(b.z, b.w);
+  } else {
 #pragma unroll
-  for (int e = 0; e < kPerThread; ++e) {
-    const int64_t c = col_of<VEC>(u, e);
-    v[e] = c < u.cols ? (p ? p[u.col0 + c] : other) : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const int c0 = col_of<VEC>(u, v, 2 * i), c1 = col_of<VEC>(u, v, 2 * i + 1);
+      val[i] = pack2(c0 < u.cols ? p[c0] : 0.f, c1 < u.cols ? p[c1] : 0.f);
+    }
   }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store_param(float* p, const RowUnit& u, const float (&v)[kPerThread]) {
-#pragma unroll
-  for (int e = 0; e < kPerThread; ++e) {
-    const int64_t c = col_of<VEC>(u, e);
-    if (c < u.cols) p[u.col0 + c] = v[e];
-  }
+__device__ __forceinline__ void store_param(float* p, const RowUnit& u, int v, const f2 (&val)[4]) {
+  store_chunk<float, VEC>(p + u.col0, u, v, val);
 }
 
-// The private ring: slot s, array k, chunk i of this thread.
+// The private ring: slot s, array k, part i of chunk v of this thread.
 template <typename T, int ARRAYS>
 struct Ring {
-  uint8_t* base;
-  __device__ __forceinline__ uint8_t* at(int s, int k, int i) const {
-    return base + ((size_t)((s * ARRAYS + k) * chunks_of(sizeof(T)) + i) * blockDim.x + threadIdx.x) * 16;
-  }
-  __device__ __forceinline__ void fetch(int s, int k, const T* row, const RowUnit& u) const {
-    if (u.t * kPerThread >= u.cols) return;
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(row + u.col0 + u.t * kPerThread);
+  uint32_t base, step;  // this thread's part 0; bytes from one part to the next
+  __device__ __forceinline__ uint32_t slot(int s) const { return base + s * ARRAYS * V * parts_of(sizeof(T)) * step; }
+  __device__ __forceinline__ void fetch(uint32_t slot, int k, const T* row, const RowUnit& u) const {
 #pragma unroll
-    for (int i = 0; i < chunks_of(sizeof(T)); ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(ptx::smem_addr(at(s, k, i))), "l"(src + 16 * i) : "memory");
-  }
-  __device__ __forceinline__ Row8<T> take(int s, int k, const RowUnit& u) const {
-    Row8<T> r;
+    for (int v = 0; v < V; ++v) {
+      const int c = col_of<true>(u, v, 0);
+      if (c >= u.cols) break;
 #pragma unroll
-    for (int i = 0; i < chunks_of(sizeof(T)); ++i) {
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (u.t * kPerThread < u.cols) v = *reinterpret_cast<const uint4*>(at(s, k, i));
-      r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
+      for (int i = 0; i < parts_of(sizeof(T)); ++i)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + ((k * V + v) * parts_of(sizeof(T)) + i) * step),
+                     "l"(reinterpret_cast<const uint8_t*>(row + c) + 16 * i)
+                     : "memory");
     }
+  }
+  __device__ __forceinline__ Chunk8<T> take(uint32_t slot, int k, int v, const RowUnit& u) const {
+    Chunk8<T> r;
+    r.zero();
+    if (col_of<true>(u, v, 0) < u.cols)
+#pragma unroll
+      for (int i = 0; i < parts_of(sizeof(T)); ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(r.w[4 * i]), "=r"(r.w[4 * i + 1]), "=r"(r.w[4 * i + 2]), "=r"(r.w[4 * i + 3])
+                     : "r"(slot + ((k * V + v) * parts_of(sizeof(T)) + i) * step)
+                     : "memory");
     return r;
   }
 };
@@ -219,80 +303,117 @@ template <int N>
 __device__ __forceinline__ void wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <typename T>
-constexpr int fwd_ring() { return sizeof(T) == 4 ? 3 : 4; }
-template <typename T>
-constexpr int bwd_ring() { return sizeof(T) == 4 ? 2 : 4; }
-constexpr int red_bytes(int units, int clusters) { return 2 * units * (clusters == 1 ? 16 : kMaxCluster * 16) * 16; }
+constexpr int ring_depth() { return sizeof(T) == 4 ? 2 : 4; }
+constexpr int red_bytes(int units) { return 2 * units * 3 * kRedRow * 4; }
 
-// Unit u of all takes rows [u n, (u + 1) n): consecutive, so that the gate row
-// stays in registers.
+// Unit u of all takes rows [u n, (u + 1) n).
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads, 2) norm_fwd_rows_kernel(const NormFwdArgs a, int tpr, int clusters) {
+__global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const NormFwdArgs a, int tpr, int clusters) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kRing = fwd_ring<T>();
+  constexpr int kRing = ring_depth<T>();
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
-  float4* red = reinterpret_cast<float4*>(smem);
-  const Ring<T, 2> ring{smem + red_bytes(units, clusters)};
+  float* red = reinterpret_cast<float*>(smem);
+  const Ring<T, 2> ring{ptx::smem_addr(smem + red_bytes(units)) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   const int64_t per = (a.rows + all - 1) / all, row0 = id * per, row1 = min(row0 + per, a.rows);
-  auto fetch = [&](int64_t row, int s) {
-    if (row < row1) {
-      ring.fetch(s, 0, (const T*)a.x + row * a.ldx, u);
-      ring.fetch(s, 1, (const T*)a.f + row * a.ldf, u);
+  const T* x = (const T*)a.x + row0 * a.ldx + u.col0;  // the row that is fetched next (VEC), or this one
+  const T* f = (const T*)a.f + row0 * a.ldf + u.col0;
+  T* y_out = (T*)a.y + row0 * a.ldy + u.col0;
+  T* h_out = (T*)a.h + row0 * a.ldh + u.col0;
+  int64_t ahead = row0;
+  auto fetch = [&](int s) {
+    if (ahead < row1) {
+      const uint32_t slot = ring.slot(s);
+      ring.fetch(slot, 0, x, u);
+      ring.fetch(slot, 1, f, u);
+      x += a.ldx;
+      f += a.ldf;
+      ++ahead;
     }
     commit_group();
   };
   if constexpr (VEC)
-    for (int s = 0; s < kRing; ++s) fetch(row0 + s, s);
-  float post[kPerThread], pre[kPerThread], res[kPerThread], gw[kPerThread];
-  load_param<VEC>(post, a.post_w, u, 1.f);
-  load_param<VEC>(pre, a.pre_w, u, 1.f);
-  load_param<VEC>(res, a.res, u, 1.f);
-#pragma unroll
-  for (int e = 0; e < kPerThread; ++e) gw[e] = post[e];
+    for (int s = 0; s < kRing; ++s) fetch(s);
   const float inv = 1.f / (float)a.cols;
-  int64_t group = -1, group_end = a.gate ? 0 : INT64_MAX;  // first row past the gate row in gw
+  f2 pre[V][4], gw[V][4], res[V][4];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    load_param<VEC>(pre[v], a.pre_w, u, v);
+    load_param<VEC>(gw[v], a.post_w, u, v);
+    if (a.res) load_param<VEC>(res[v], a.res, u, v);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i) res[v][i] = both(1.f);
+  }
+  int64_t group_end = a.gate ? row0 : INT64_MAX;  // first row past the gate row in gw
   int slot = 0, half = 0;
   for (int64_t row = row0; row < row1; ++row) {
-    if (row >= group_end) {
-      group = row / a.per_gate;
+    if (row == group_end) {
+      const int64_t group = row / a.per_gate;
       group_end = (group + 1) * a.per_gate;
-      load_param<VEC>(gw, a.gate + group * a.cols, u, 1.f);
 #pragma unroll
-      for (int e = 0; e < kPerThread; ++e) gw[e] *= post[e];
+      for (int v = 0; v < V; ++v) {
+        f2 g[4];
+        load_param<VEC>(g, a.gate + group * a.cols, u, v);
+        load_param<VEC>(gw[v], a.post_w, u, v);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) gw[v][i] = mul2(gw[v][i], g[i]);
+      }
     }
-    Row8<T> x, f;
+    Chunk8<T> xr[V], fr[V];
     if constexpr (VEC) {
       wait_group<kRing - 1>();
-      x = ring.take(slot, 0, u);
-      f = ring.take(slot, 1, u);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        xr[v] = ring.take(ring.slot(slot), 0, v, u);
+        fr[v] = ring.take(ring.slot(slot), 1, v, u);
+      }
     } else {
-      x = load_direct<T, VEC>((const T*)a.x + row * a.ldx, u);
-      f = load_direct<T, VEC>((const T*)a.f + row * a.ldf, u);
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        xr[v] = load_direct<T, VEC>(x, u, v);
+        fr[v] = load_direct<T, VEC>(f, u, v);
+      }
+      x += a.ldx;
+      f += a.ldf;
     }
-    float s[1] = {0.f};
+    f2 q = 0;
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) s[0] = fmaf(f.at(e), f.at(e), s[0]);
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q = fma2(fr[v].pair(i), fr[v].pair(i), q);
+    float s[1] = {add_up(q)};
     row_sum<1>(s, u, red, half, clusters);
-    const float r1 = 1.f / sqrtf(s[0] * inv + a.eps);
-    float y[kPerThread];
-    s[0] = 0.f;
+    const float r1 = rsqrtf(fmaf(s[0], inv, a.eps));
+    const f2 rr1 = both(r1);
+    f2 y[V][4];
+    q = 0;
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      y[e] = fmaf(x.at(e), res[e], f.at(e) * r1 * gw[e]);
-      s[0] = fmaf(y[e], y[e], s[0]);
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[v][i] = fma2(mul2(fr[v].pair(i), rr1), gw[v][i], mul2(xr[v].pair(i), res[v][i]));
+        q = fma2(y[v][i], y[v][i], q);
+      }
+      store_chunk<T, VEC>(y_out, u, v, y[v]);
     }
     if constexpr (VEC) {
-      fetch(row + kRing, slot);  // this thread has taken its slot
+      fetch(slot);  // this thread has taken its slot
       if (++slot == kRing) slot = 0;
     }
-    store_row<T, VEC>((T*)a.y + row * a.ldy, u, y);
+    s[0] = add_up(q);
     row_sum<1>(s, u, red, half, clusters);
-    const float r2 = 1.f / sqrtf(s[0] * inv + a.eps);
+    const float r2 = rsqrtf(fmaf(s[0], inv, a.eps));
+    const f2 rr2 = both(r2);
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) y[e] *= r2 * pre[e];
-    store_row<T, VEC>((T*)a.h + row * a.ldh, u, y);
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[v][i] = mul2(mul2(y[v][i], rr2), pre[v][i]);
+      store_chunk<T, VEC>(h_out, u, v, y[v]);
+    }
+    y_out += a.ldy;
+    h_out += a.ldh;
     if (u.t == 0 && u.col0 == 0) {
       a.rstd[row] = r1;
       a.rstd[a.rows + row] = r2;
@@ -329,61 +450,84 @@ struct ChunkRows {
 // with t = dy + r2 (i - yn m2), i = dh w_pre, the second is
 //   mean(g w fn (dy + r2 i)) - r2 m2 mean(g w fn yn)
 // so that one round of three sums serves both (the rounding is that of t's own
-// terms).  Units' column sums go to their own rows of the partial arrays, in
-// a fixed order, and are added up by norm_bwd_sums_kernel.
+// terms).  Units' column sums stay in registers over their rows, go to their
+// own rows of the partial arrays and are added up, in a fixed order, by
+// norm_bwd_sums_kernel.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_rows_kernel(const NormBwdArgs a, int tpr, int clusters) {
+__global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const NormBwdArgs a, int tpr, int clusters) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kRing = bwd_ring<T>();
+  constexpr int kRing = ring_depth<T>();
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
-  float4* red = reinterpret_cast<float4*>(smem);
-  const Ring<T, 5> ring{smem + red_bytes(units, clusters)};
+  float* red = reinterpret_cast<float*>(smem);
+  const Ring<T, 5> ring{ptx::smem_addr(smem + red_bytes(units)) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   const bool with_x = a.d_res != nullptr;
   ChunkRows ahead(a, id, all), at(a, id, all);
   auto fetch = [&](int s) {
     if (!ahead.done()) {
       const int64_t row = ahead.row;
-      if (a.dy) ring.fetch(s, 0, (const T*)a.dy + row * a.lddy, u);
-      ring.fetch(s, 1, (const T*)a.dh + row * a.lddh, u);
-      ring.fetch(s, 2, (const T*)a.y + row * a.ldy, u);
-      ring.fetch(s, 3, (const T*)a.f + row * a.ldf, u);
-      if (with_x) ring.fetch(s, 4, (const T*)a.x + row * a.ldx, u);
+      const uint32_t slot = ring.slot(s);
+      if (a.dy) ring.fetch(slot, 0, (const T*)a.dy + row * a.lddy + u.col0, u);
+      ring.fetch(slot, 1, (const T*)a.dh + row * a.lddh + u.col0, u);
+      ring.fetch(slot, 2, (const T*)a.y + row * a.ldy + u.col0, u);
+      ring.fetch(slot, 3, (const T*)a.f + row * a.ldf + u.col0, u);
+      if (with_x) ring.fetch(slot, 4, (const T*)a.x + row * a.ldx + u.col0, u);
       ahead.next();
     }
     commit_group();
   };
   if constexpr (VEC)
     for (int s = 0; s < kRing; ++s) fetch(s);
-  float pre[kPerThread], res[kPerThread], gw[kPerThread];
-  load_param<VEC>(pre, a.pre_w, u, 1.f);
-  load_param<VEC>(res, a.res, u, 1.f);
-  float sum_pre[kPerThread], sum_post[kPerThread], sum_res[kPerThread], sum_t[kPerThread];
+  f2 sum_pre[V][4], sum_res[V][4], sum_t[V][4];
 #pragma unroll
-  for (int e = 0; e < kPerThread; ++e) sum_pre[e] = sum_post[e] = sum_res[e] = sum_t[e] = 0.f;
+  for (int v = 0; v < V; ++v)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sum_pre[v][i] = sum_res[v][i] = sum_t[v][i] = 0;
+  f2 pre[V][4], gw[V][4], res[V][4];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    load_param<VEC>(pre[v], a.pre_w, u, v);
+    if (a.res) load_param<VEC>(res[v], a.res, u, v);
+    else
+#pragma unroll
+      for (int i = 0; i < 4; ++i) res[v][i] = both(1.f);
+  }
   const float inv = 1.f / (float)a.cols;
+  float* part_post = a.part_post + id * a.cols;
+  bool post_written = false;
   int64_t chunk = -1;
+  const float* gate = nullptr;
   int slot = 0, half = 0;
-  // t fn summed over a chunk belongs to one gate row.
+  // t fn summed over a chunk belongs to one gate row.  The sum over a unit's
+  // chunks is kept in its row of part_post.
   auto flush = [&]() {
-    float g[kPerThread], w[kPerThread];
     const int64_t group = chunk / a.chunks_per_group;
-    load_param<VEC>(g, a.gate ? a.gate + group * a.cols : nullptr, u, 1.f);
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) sum_post[e] = fmaf(g[e], sum_t[e], sum_post[e]);
-    if (a.d_gate) {
-      if (a.chunks_per_group > 1) {
-        store_param<VEC>(a.part_gate + chunk * a.cols, u, sum_t);
-      } else {
-        load_param<VEC>(w, a.post_w, u, 1.f);
+    for (int v = 0; v < V; ++v) {
+      f2 w[4], o[4];
+      if (a.gate) load_param<VEC>(w, gate, u, v);
+      if (post_written) load_param<VEC>(o, part_post, u, v);
 #pragma unroll
-        for (int e = 0; e < kPerThread; ++e) w[e] *= sum_t[e];
-        store_param<VEC>(a.d_gate + group * a.cols, u, w);
+      for (int i = 0; i < 4; ++i) {
+        const f2 g = a.gate ? w[i] : both(1.f);
+        o[i] = post_written ? fma2(g, sum_t[v][i], o[i]) : mul2(g, sum_t[v][i]);
       }
-    }
+      store_param<VEC>(part_post, u, v, o);
+      if (a.d_gate) {
+        if (a.chunks_per_group > 1) {
+          store_param<VEC>(a.part_gate + chunk * a.cols, u, v, sum_t[v]);
+        } else {
+          load_param<VEC>(w, a.post_w, u, v);
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) sum_t[e] = 0.f;
+          for (int i = 0; i < 4; ++i) w[i] = mul2(w[i], sum_t[v][i]);
+          store_param<VEC>(a.d_gate + group * a.cols, u, v, w);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum_t[v][i] = 0;
+    }
+    post_written = true;
   };
   float n1 = 0.f, n2 = 0.f;
   if (!at.done()) {
@@ -396,12 +540,16 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_rows_kernel(const Nor
     if (at.chunk != chunk) {
       if (chunk >= 0) flush();
       chunk = at.chunk;
-      load_param<VEC>(gw, a.post_w, u, 1.f);
-      if (a.gate) {
-        float g[kPerThread];
-        load_param<VEC>(g, a.gate + chunk / a.chunks_per_group * a.cols, u, 1.f);
+      if (a.gate) gate = a.gate + chunk / a.chunks_per_group * a.cols;
 #pragma unroll
-        for (int e = 0; e < kPerThread; ++e) gw[e] *= g[e];
+      for (int v = 0; v < V; ++v) {
+        load_param<VEC>(gw[v], a.post_w, u, v);
+        if (a.gate) {
+          f2 g[4];
+          load_param<VEC>(g, gate, u, v);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) gw[v][i] = mul2(gw[v][i], g[i]);
+        }
       }
     }
     at.next();
@@ -409,55 +557,74 @@ __global__ void __launch_bounds__(kMaxThreads, 1) norm_bwd_rows_kernel(const Nor
       n1 = a.rstd[at.row];
       n2 = a.rstd[a.rows + at.row];
     }
-    Row8<T> dy, dh, y, f, x;
+    Chunk8<T> dy[V], dh[V], y[V], f[V], x[V];
+    if constexpr (VEC) wait_group<kRing - 1>();
+    const uint32_t from = ring.slot(slot);
 #pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) * 2); ++i) dy.w[i] = x.w[i] = 0;
-    if constexpr (VEC) {
-      wait_group<kRing - 1>();
-      if (a.dy) dy = ring.take(slot, 0, u);
-      dh = ring.take(slot, 1, u);
-      y = ring.take(slot, 2, u);
-      f = ring.take(slot, 3, u);
-      if (with_x) x = ring.take(slot, 4, u);
-    } else {
-      if (a.dy) dy = load_direct<T, VEC>((const T*)a.dy + row * a.lddy, u);
-      dh = load_direct<T, VEC>((const T*)a.dh + row * a.lddh, u);
-      y = load_direct<T, VEC>((const T*)a.y + row * a.ldy, u);
-      f = load_direct<T, VEC>((const T*)a.f + row * a.ldf, u);
-      if (with_x) x = load_direct<T, VEC>((const T*)a.x + row * a.ldx, u);
+    for (int v = 0; v < V; ++v) {
+      dy[v].zero();
+      x[v].zero();
+      if constexpr (VEC) {
+        if (a.dy) dy[v] = ring.take(from, 0, v, u);
+        dh[v] = ring.take(from, 1, v, u);
+        y[v] = ring.take(from, 2, v, u);
+        f[v] = ring.take(from, 3, v, u);
+        if (with_x) x[v] = ring.take(from, 4, v, u);
+      } else {
+        if (a.dy) dy[v] = load_direct<T, VEC>((const T*)a.dy + row * a.lddy + u.col0, u, v);
+        dh[v] = load_direct<T, VEC>((const T*)a.dh + row * a.lddh + u.col0, u, v);
+        y[v] = load_direct<T, VEC>((const T*)a.y + row * a.ldy + u.col0, u, v);
+        f[v] = load_direct<T, VEC>((const T*)a.f + row * a.ldf + u.col0, u, v);
+        if (with_x) x[v] = load_direct<T, VEC>((const T*)a.x + row * a.ldx + u.col0, u, v);
+      }
     }
-    float s[3] = {0.f, 0.f, 0.f};
+    const f2 rr1 = both(r1), rr2 = both(r2);
+    f2 s0 = 0, s1 = 0, s2 = 0;
 #pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      const float i = dh.at(e) * pre[e], yn = y.at(e) * r2, b = gw[e] * (f.at(e) * r1);
-      s[0] = fmaf(i, yn, s[0]);
-      s[1] = fmaf(b, fmaf(r2, i, dy.at(e)), s[1]);
-      s[2] = fmaf(b, yn, s[2]);
+    for (int v = 0; v < V; ++v) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 in = mul2(dh[v].pair(i), pre[v][i]), yn = mul2(y[v].pair(i), rr2);
+        const f2 b = mul2(gw[v][i], mul2(f[v].pair(i), rr1));
+        s0 = fma2(in, yn, s0);
+        s1 = fma2(b, fma2(rr2, in, dy[v].pair(i)), s1);
+        s2 = fma2(b, yn, s2);
+      }
     }
+    float s[3] = {add_up(s0), add_up(s1), add_up(s2)};
     row_sum<3>(s, u, red, half, clusters);
-    const float m2 = s[0] * inv, m1 = (s[1] - r2 * m2 * s[2]) * inv;
-    float dx[kPerThread], df[kPerThread];
-#pragma unroll
-    for (int e = 0; e < kPerThread; ++e) {
-      const float yn = y.at(e) * r2, fn = f.at(e) * r1;
-      const float t = fmaf(r2, fmaf(-yn, m2, dh.at(e) * pre[e]), dy.at(e));
-      sum_pre[e] = fmaf(dh.at(e), yn, sum_pre[e]);
-      sum_t[e] = fmaf(t, fn, sum_t[e]);
-      sum_res[e] = fmaf(t, x.at(e), sum_res[e]);
-      dx[e] = res[e] * t;
-      df[e] = r1 * fmaf(-fn, m1, gw[e] * t);
-    }
     if constexpr (VEC) {
-      fetch(slot);
+      fetch(slot);  // this thread has taken its slot
       if (++slot == kRing) slot = 0;
     }
-    store_row<T, VEC>((T*)a.dx + row * a.lddx, u, dx);
-    store_row<T, VEC>((T*)a.df + row * a.lddf, u, df);
+    const float m2 = s[0] * inv, m1 = (s[1] - r2 * m2 * s[2]) * inv;
+    const f2 nm2 = both(-m2), nm1 = both(-m1);
+    T* dx_row = (T*)a.dx + row * a.lddx + u.col0;
+    T* df_row = (T*)a.df + row * a.lddf + u.col0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      f2 dx[4], df[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 yn = mul2(y[v].pair(i), rr2), fn = mul2(f[v].pair(i), rr1);
+        const f2 t = fma2(rr2, fma2(yn, nm2, mul2(dh[v].pair(i), pre[v][i])), dy[v].pair(i));
+        sum_pre[v][i] = fma2(dh[v].pair(i), yn, sum_pre[v][i]);
+        sum_t[v][i] = fma2(t, fn, sum_t[v][i]);
+        if (with_x) sum_res[v][i] = fma2(t, x[v].pair(i), sum_res[v][i]);
+        dx[i] = mul2(res[v][i], t);
+        df[i] = mul2(rr1, fma2(fn, nm1, mul2(gw[v][i], t)));
+      }
+      store_chunk<T, VEC>(dx_row, u, v, dx);
+      store_chunk<T, VEC>(df_row, u, v, df);
+    }
   }
   if (chunk >= 0) flush();
-  store_param<VEC>(a.part_pre + id * a.cols, u, sum_pre);
-  store_param<VEC>(a.part_post + id * a.cols, u, sum_post);
-  if (with_x) store_param<VEC>(a.part_res + id * a.cols, u, sum_res);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (!post_written) store_param<VEC>(part_post, u, v, sum_t[v]);  // no rows: zeros
+    store_param<VEC>(a.part_pre + id * a.cols, u, v, sum_pre[v]);
+    if (with_x) store_param<VEC>(a.part_res + id * a.cols, u, v, sum_res[v]);
+  }
   if (clusters > 1) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
 }
 
@@ -629,18 +796,24 @@ __global__ void __launch_bounds__(1024) norm_bwd_sums_kernel(const NormBwdArgs a
 
 // ------------------------------------------------------------ launches
 
-// Threads of a unit, CTAs of a cluster and units of a CTA for rows of `cols`.
+// Threads of a unit, CTAs of a cluster, units of a CTA and CTAs of an SM for
+// rows of `cols`, with `threads` on an SM.
 struct RowShape {
-  int tpr, clusters, units;
+  int tpr, clusters, units, resident;
 };
-RowShape row_shape(int64_t cols) {
+RowShape row_shape(int64_t cols, int threads, int cta_threads) {
   RowShape r;
-  r.clusters = cols <= kCtaCols ? 1 : cols <= 2 * kCtaCols ? 2 : cols <= 4 * kCtaCols ? 4 : kMaxCluster;
-  r.tpr = cols <= kCtaCols ? (int)((cols + 32 * kPerThread - 1) / (32 * kPerThread)) * 32 : kMaxThreads;
-  r.units = r.clusters > 1 ? 1 : std::max(1, std::min(kMaxThreads / r.tpr, 15));
+  const int64_t cta = (int64_t)threads * V * 8;
+  r.clusters = cols <= cta ? 1 : cols <= 2 * cta ? 2 : cols <= 4 * cta ? 4 : kMaxCluster;
+  r.tpr = r.clusters > 1 ? threads : (int)((cols + 256 * V - 1) / (256 * V)) * 32;
+  r.units = r.clusters > 1 ? 1 : std::max(1, cta_threads / r.tpr);
+  r.resident = std::max(1, threads / (r.tpr * r.units));
   return r;
 }
-bool held(int64_t cols) { return cols <= kMaxCluster * kCtaCols; }
+RowShape fwd_shape(int64_t cols) { return row_shape(cols, kFwdThreads, 128); }
+RowShape bwd_shape(int64_t cols) { return row_shape(cols, kBwdThreads, kBwdThreads); }
+constexpr int64_t kHeld = 32768;  // longest rows held
+static_assert(kMaxCluster * kBwdThreads * V * 8 >= kHeld && kMaxCluster * kFwdThreads * V * 8 >= kHeld, "held rows");
 
 template <typename K, typename A>
 cudaError_t launch_rows(K kernel, const A& a, const RowShape& r, int64_t ctas, int smem, cudaStream_t s) {
@@ -662,34 +835,34 @@ cudaError_t launch_rows(K kernel, const A& a, const RowShape& r, int64_t ctas, i
 }
 
 template <typename T>
-int ring_bytes(const RowShape& r, int arrays, int depth) {
-  return red_bytes(r.units, r.clusters) + depth * arrays * chunks_of(sizeof(T)) * r.tpr * r.units * 16;
+int ring_bytes(const RowShape& r, int arrays) {
+  return red_bytes(r.units) + ring_depth<T>() * arrays * V * parts_of(sizeof(T)) * r.tpr * r.units * 16;
 }
 
 template <typename T>
 cudaError_t fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
-  if (!held(a.cols)) {
+  if (a.cols > kHeld) {
     const int64_t grid = std::min(a.rows, (int64_t)sms * 8);
     norm_fwd_kernel<T><<<(unsigned)grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
-  const RowShape r = row_shape(a.cols);
-  const int64_t ctas = std::min((a.rows + r.units - 1) / r.units, (int64_t)std::max(1, sms * 2 / r.clusters));
-  if (a.vec) return launch_rows(norm_fwd_rows_kernel<T, true>, a, r, ctas, ring_bytes<T>(r, 2, fwd_ring<T>()), s);
-  return launch_rows(norm_fwd_rows_kernel<T, false>, a, r, ctas, red_bytes(r.units, r.clusters), s);
+  const RowShape r = fwd_shape(a.cols);
+  const int64_t ctas = std::min((a.rows + r.units - 1) / r.units, (int64_t)std::max(1, sms * r.resident / r.clusters));
+  if (a.vec) return launch_rows(norm_fwd_rows_kernel<T, true>, a, r, ctas, ring_bytes<T>(r, 2), s);
+  return launch_rows(norm_fwd_rows_kernel<T, false>, a, r, ctas, red_bytes(r.units), s);
 }
 
 template <typename T>
 cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
   cudaError_t e;
-  if (!held(a.cols)) {
+  if (a.cols > kHeld) {
     norm_bwd_kernel<T><<<(unsigned)a.units, kThreads, 0, s>>>(a);
     e = cudaGetLastError();
   } else {
-    const RowShape r = row_shape(a.cols);
+    const RowShape r = bwd_shape(a.cols);
     const int64_t ctas = a.units / r.units;
-    if (a.vec) e = launch_rows(norm_bwd_rows_kernel<T, true>, a, r, ctas, ring_bytes<T>(r, 5, bwd_ring<T>()), s);
-    else e = launch_rows(norm_bwd_rows_kernel<T, false>, a, r, ctas, red_bytes(r.units, r.clusters), s);
+    if (a.vec) e = launch_rows(norm_bwd_rows_kernel<T, true>, a, r, ctas, ring_bytes<T>(r, 5), s);
+    else e = launch_rows(norm_bwd_rows_kernel<T, false>, a, r, ctas, red_bytes(r.units), s);
   }
   if (e != cudaSuccess) return e;
   const unsigned ys = 3 + (a.d_gate && a.chunks_per_group > 1 ? (unsigned)a.groups : 0u);
@@ -699,11 +872,11 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-// One CTA or cluster a SM share; no more units than rows.
+// As many units as are resident, no more than rows.
 int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms) {
-  if (!held(cols)) return std::min<int64_t>(std::max<int64_t>(rows, 1), (int64_t)sms * 4);
-  const RowShape r = row_shape(cols);
-  const int64_t ctas = std::min<int64_t>(std::max(1, sms / r.clusters), (std::max<int64_t>(rows, 1) + r.units - 1) / r.units);
+  if (cols > kHeld) return std::min<int64_t>(std::max<int64_t>(rows, 1), (int64_t)sms * 4);
+  const RowShape r = bwd_shape(cols);
+  const int64_t ctas = std::min<int64_t>(std::max(1, sms * r.resident / r.clusters), (std::max<int64_t>(rows, 1) + r.units - 1) / r.units);
   return ctas * r.units;
 }
 

@@ -24,7 +24,7 @@ struct NormFwdArgs {
   float* rstd;                                // [2][rows]
   int64_t rows, cols, ldx, ldf, ldy, ldh, per_gate;
   float eps;
-  int vec;                                    // 16-byte aligned rows, columns a multiple of 8
+  int vec;                                    // rows and parameters 16-byte aligned, columns a multiple of 8
 };
 
 // Rows are cut into chunks that lie inside one gate group, so that a chunk's
