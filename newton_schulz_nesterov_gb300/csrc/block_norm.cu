@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <climits>
 #include <type_traits>
 
 #include "../../include/dmuon.h"
@@ -82,9 +83,12 @@ __device__ __forceinline__ int col_of(const RowUnit& u, int v, int e) {
 
 // Sums of N values over a row's threads, in a fixed order, to all of them.
 // One barrier: consecutive calls alternate between two halves of `red`
-// ([2][units][3][kRedRow] floats), and a half is written again only after the
-// next call's barrier, when every thread has read it.
+// ([2][units][3][kRedRow] floats, zero at first), and a half is written again
+// only after the next call's barrier, when every thread has read it.
 constexpr int kRedRow = kMaxCluster * 16;  // warps of a row at most
+__device__ __forceinline__ void row_sum_init(float* red, int units) {
+  for (int i = threadIdx.x; i < 2 * units * 3 * kRedRow; i += blockDim.x) red[i] = 0.f;
+}
 template <int N>
 __device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, float* red, int& half, int clusters) {
 #pragma unroll
@@ -114,11 +118,11 @@ __device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, float* 
     }
     ptx::cluster_sync();
   }
-  if (n <= 4) {
+  if (n <= 8) {  // what no warp writes is zero
 #pragma unroll
     for (int k = 0; k < N; ++k) {
-      const float4 p = *reinterpret_cast<const float4*>(mine + k * kRedRow);
-      v[k] = p.x + (n > 1 ? p.y : 0.f) + ((n > 2 ? p.z : 0.f) + (n > 3 ? p.w : 0.f));
+      const float4 p = *reinterpret_cast<const float4*>(mine + k * kRedRow), q = *reinterpret_cast<const float4*>(mine + k * kRedRow + 4);
+      v[k] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
     }
     return;
   }
@@ -314,14 +318,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
   float* red = reinterpret_cast<float*>(smem);
+  row_sum_init(red, units);
   const Ring<T, 2> ring{ptx::smem_addr(smem + red_bytes(units)) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
-  const int64_t per = (a.rows + all - 1) / all, row0 = id * per, row1 = min(row0 + per, a.rows);
+  const int64_t per = (a.rows + all - 1) / all;
+  const int row0 = (int)min(id * per, a.rows), row1 = (int)min(row0 + per, a.rows);
   const T* x = (const T*)a.x + row0 * a.ldx + u.col0;  // the row that is fetched next (VEC), or this one
   const T* f = (const T*)a.f + row0 * a.ldf + u.col0;
   T* y_out = (T*)a.y + row0 * a.ldy + u.col0;
   T* h_out = (T*)a.h + row0 * a.ldh + u.col0;
-  int64_t ahead = row0;
+  int ahead = row0;
   auto fetch = [&](int s) {
     if (ahead < row1) {
       const uint32_t slot = ring.slot(s);
@@ -335,6 +341,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
   };
   if constexpr (VEC)
     for (int s = 0; s < kRing; ++s) fetch(s);
+  if (clusters > 1) ptx::cluster_sync();
+  else __syncthreads();
   const float inv = 1.f / (float)a.cols;
   f2 pre[V][4], gw[V][4], res[V][4];
 #pragma unroll
@@ -346,12 +354,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
 #pragma unroll
       for (int i = 0; i < 4; ++i) res[v][i] = both(1.f);
   }
-  int64_t group_end = a.gate ? row0 : INT64_MAX;  // first row past the gate row in gw
+  int group_end = a.gate ? row0 : INT_MAX;  // first row past the gate row in gw
   int slot = 0, half = 0;
-  for (int64_t row = row0; row < row1; ++row) {
+  for (int row = row0; row < row1; ++row) {
     if (row == group_end) {
       const int64_t group = row / a.per_gate;
-      group_end = (group + 1) * a.per_gate;
+      group_end = (int)min((group + 1) * a.per_gate, a.rows);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         f2 g[4];
@@ -422,26 +430,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
   if (clusters > 1) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
 }
 
-// The rows of a unit, chunk after chunk.
+// The rows of a unit, chunk after chunk (rows and chunks fit 31 bits).
 struct ChunkRows {
-  const NormBwdArgs& a;
-  int64_t all, chunk, row, end;
-  __device__ __forceinline__ ChunkRows(const NormBwdArgs& a_, int64_t id, int64_t all_) : a(a_), all(all_), chunk(id), row(0), end(0) { open(); }
-  __device__ __forceinline__ void open() {  // the first non-empty chunk from `chunk` on
-    const int64_t n = a.groups * a.chunks_per_group;
+  int all, chunk, row, end;
+  __device__ __forceinline__ void open(const NormBwdArgs& a) {  // the first non-empty chunk from `chunk` on
+    const int n = (int)(a.groups * a.chunks_per_group), cpg = (int)a.chunks_per_group;
     for (; chunk < n; chunk += all) {
-      const int64_t group = chunk / a.chunks_per_group, part = chunk % a.chunks_per_group;
-      row = group * a.per_gate + part * a.chunk_rows;
-      end = min(min(row + a.chunk_rows, (group + 1) * a.per_gate), a.rows);
-      if (row < end) return;
+      const int group = chunk / cpg, part = chunk - group * cpg;
+      const int64_t r = group * a.per_gate + part * a.chunk_rows;
+      const int64_t e = min(min(r + a.chunk_rows, (group + 1) * a.per_gate), a.rows);
+      if (r < e) {
+        row = (int)r;
+        end = (int)e;
+        return;
+      }
     }
-    chunk = INT64_MAX;
+    chunk = INT_MAX;
   }
-  __device__ __forceinline__ bool done() const { return chunk == INT64_MAX; }
-  __device__ __forceinline__ void next() {
+  __device__ __forceinline__ bool done() const { return chunk == INT_MAX; }
+  __device__ __forceinline__ void next(const NormBwdArgs& a) {
     if (++row == end) {
       chunk += all;
-      open();
+      open(a);
     }
   }
 };
@@ -453,32 +463,55 @@ struct ChunkRows {
 // terms).  Units' column sums stay in registers over their rows, go to their
 // own rows of the partial arrays and are added up, in a fixed order, by
 // norm_bwd_sums_kernel.
-template <typename T, bool VEC>
+template <typename T, bool VEC, bool DY, bool X>
 __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const NormBwdArgs a, int tpr, int clusters) {
   extern __shared__ __align__(16) uint8_t smem[];
   constexpr int kRing = ring_depth<T>();
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
   float* red = reinterpret_cast<float*>(smem);
+  row_sum_init(red, units);
   const Ring<T, 5> ring{ptx::smem_addr(smem + red_bytes(units)) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
-  const bool with_x = a.d_res != nullptr;
-  ChunkRows ahead(a, id, all), at(a, id, all);
+  ChunkRows at{(int)all, (int)id, 0, 0};
+  at.open(a);
+  ChunkRows ahead = at;
+  const T *f_dy = nullptr, *f_dh = nullptr, *f_y = nullptr, *f_f = nullptr, *f_x = nullptr;  // the row fetched next
+  auto seek = [&]() {
+    const int64_t row = ahead.row;
+    if (DY) f_dy = (const T*)a.dy + row * a.lddy + u.col0;
+    f_dh = (const T*)a.dh + row * a.lddh + u.col0;
+    f_y = (const T*)a.y + row * a.ldy + u.col0;
+    f_f = (const T*)a.f + row * a.ldf + u.col0;
+    if (X) f_x = (const T*)a.x + row * a.ldx + u.col0;
+  };
+  if (!ahead.done()) seek();
   auto fetch = [&](int s) {
     if (!ahead.done()) {
-      const int64_t row = ahead.row;
       const uint32_t slot = ring.slot(s);
-      if (a.dy) ring.fetch(slot, 0, (const T*)a.dy + row * a.lddy + u.col0, u);
-      ring.fetch(slot, 1, (const T*)a.dh + row * a.lddh + u.col0, u);
-      ring.fetch(slot, 2, (const T*)a.y + row * a.ldy + u.col0, u);
-      ring.fetch(slot, 3, (const T*)a.f + row * a.ldf + u.col0, u);
-      if (with_x) ring.fetch(slot, 4, (const T*)a.x + row * a.ldx + u.col0, u);
-      ahead.next();
+      if (DY) ring.fetch(slot, 0, f_dy, u);
+      ring.fetch(slot, 1, f_dh, u);
+      ring.fetch(slot, 2, f_y, u);
+      ring.fetch(slot, 3, f_f, u);
+      if (X) ring.fetch(slot, 4, f_x, u);
+      const int was = ahead.chunk;
+      ahead.next(a);
+      if (ahead.chunk == was) {
+        if (DY) f_dy += a.lddy;
+        f_dh += a.lddh;
+        f_y += a.ldy;
+        f_f += a.ldf;
+        if (X) f_x += a.ldx;
+      } else if (!ahead.done()) {
+        seek();
+      }
     }
     commit_group();
   };
   if constexpr (VEC)
     for (int s = 0; s < kRing; ++s) fetch(s);
+  if (clusters > 1) ptx::cluster_sync();
+  else __syncthreads();
   f2 sum_pre[V][4], sum_res[V][4], sum_t[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v)
@@ -496,13 +529,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
   const float inv = 1.f / (float)a.cols;
   float* part_post = a.part_post + id * a.cols;
   bool post_written = false;
-  int64_t chunk = -1;
+  T *dx_row = nullptr, *df_row = nullptr;
+  int chunk = -1;
   const float* gate = nullptr;
   int slot = 0, half = 0;
   // t fn summed over a chunk belongs to one gate row.  The sum over a unit's
   // chunks is kept in its row of part_post.
   auto flush = [&]() {
-    const int64_t group = chunk / a.chunks_per_group;
+    const int64_t group = chunk / (int)a.chunks_per_group;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       f2 w[4], o[4];
@@ -516,7 +550,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       store_param<VEC>(part_post, u, v, o);
       if (a.d_gate) {
         if (a.chunks_per_group > 1) {
-          store_param<VEC>(a.part_gate + chunk * a.cols, u, v, sum_t[v]);
+          store_param<VEC>(a.part_gate + (int64_t)chunk * a.cols, u, v, sum_t[v]);
         } else {
           load_param<VEC>(w, a.post_w, u, v);
 #pragma unroll
@@ -540,7 +574,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     if (at.chunk != chunk) {
       if (chunk >= 0) flush();
       chunk = at.chunk;
-      if (a.gate) gate = a.gate + chunk / a.chunks_per_group * a.cols;
+      dx_row = (T*)a.dx + row * a.lddx + u.col0;
+      df_row = (T*)a.df + row * a.lddf + u.col0;
+      if (a.gate) gate = a.gate + (int64_t)(chunk / (int)a.chunks_per_group) * a.cols;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         load_param<VEC>(gw[v], a.post_w, u, v);
@@ -552,43 +588,46 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
         }
       }
     }
-    at.next();
+    at.next(a);
     if (!at.done()) {  // the next row's, before it is needed
       n1 = a.rstd[at.row];
       n2 = a.rstd[a.rows + at.row];
     }
-    Chunk8<T> dy[V], dh[V], y[V], f[V], x[V];
+    // Kept over the sums: yn, fn and q = dy + r2 dh w_pre, from which t is one operation.
+    const f2 rr1 = both(r1), rr2 = both(r2);
+    f2 yn[V][4], fn[V][4], q[V][4], s0 = 0, s1 = 0, s2 = 0;
+    Chunk8<T> x[V];
     if constexpr (VEC) wait_group<kRing - 1>();
     const uint32_t from = ring.slot(slot);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      dy[v].zero();
+      Chunk8<T> dy, dh, y, f;
+      dy.zero();
       x[v].zero();
       if constexpr (VEC) {
-        if (a.dy) dy[v] = ring.take(from, 0, v, u);
-        dh[v] = ring.take(from, 1, v, u);
-        y[v] = ring.take(from, 2, v, u);
-        f[v] = ring.take(from, 3, v, u);
-        if (with_x) x[v] = ring.take(from, 4, v, u);
+        if (DY) dy = ring.take(from, 0, v, u);
+        dh = ring.take(from, 1, v, u);
+        y = ring.take(from, 2, v, u);
+        f = ring.take(from, 3, v, u);
+        if (X) x[v] = ring.take(from, 4, v, u);
       } else {
-        if (a.dy) dy[v] = load_direct<T, VEC>((const T*)a.dy + row * a.lddy + u.col0, u, v);
-        dh[v] = load_direct<T, VEC>((const T*)a.dh + row * a.lddh + u.col0, u, v);
-        y[v] = load_direct<T, VEC>((const T*)a.y + row * a.ldy + u.col0, u, v);
-        f[v] = load_direct<T, VEC>((const T*)a.f + row * a.ldf + u.col0, u, v);
-        if (with_x) x[v] = load_direct<T, VEC>((const T*)a.x + row * a.ldx + u.col0, u, v);
+        if (DY) dy = load_direct<T, VEC>((const T*)a.dy + row * a.lddy + u.col0, u, v);
+        dh = load_direct<T, VEC>((const T*)a.dh + row * a.lddh + u.col0, u, v);
+        y = load_direct<T, VEC>((const T*)a.y + row * a.ldy + u.col0, u, v);
+        f = load_direct<T, VEC>((const T*)a.f + row * a.ldf + u.col0, u, v);
+        if (X) x[v] = load_direct<T, VEC>((const T*)a.x + row * a.ldx + u.col0, u, v);
       }
-    }
-    const f2 rr1 = both(r1), rr2 = both(r2);
-    f2 s0 = 0, s1 = 0, s2 = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f2 in = mul2(dh[v].pair(i), pre[v][i]), yn = mul2(y[v].pair(i), rr2);
-        const f2 b = mul2(gw[v][i], mul2(f[v].pair(i), rr1));
-        s0 = fma2(in, yn, s0);
-        s1 = fma2(b, fma2(rr2, in, dy[v].pair(i)), s1);
-        s2 = fma2(b, yn, s2);
+        const f2 g = dh.pair(i), in = mul2(g, pre[v][i]);
+        yn[v][i] = mul2(y.pair(i), rr2);
+        fn[v][i] = mul2(f.pair(i), rr1);
+        q[v][i] = fma2(rr2, in, dy.pair(i));
+        const f2 b = mul2(gw[v][i], fn[v][i]);
+        sum_pre[v][i] = fma2(g, yn[v][i], sum_pre[v][i]);
+        s0 = fma2(in, yn[v][i], s0);
+        s1 = fma2(b, q[v][i], s1);
+        s2 = fma2(b, yn[v][i], s2);
       }
     }
     float s[3] = {add_up(s0), add_up(s1), add_up(s2)};
@@ -597,33 +636,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       fetch(slot);  // this thread has taken its slot
       if (++slot == kRing) slot = 0;
     }
-    const float m2 = s[0] * inv, m1 = (s[1] - r2 * m2 * s[2]) * inv;
+    const float m2 = r2 * s[0] * inv, m1 = (s[1] - m2 * s[2]) * inv;
     const f2 nm2 = both(-m2), nm1 = both(-m1);
-    T* dx_row = (T*)a.dx + row * a.lddx + u.col0;
-    T* df_row = (T*)a.df + row * a.lddf + u.col0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       f2 dx[4], df[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f2 yn = mul2(y[v].pair(i), rr2), fn = mul2(f[v].pair(i), rr1);
-        const f2 t = fma2(rr2, fma2(yn, nm2, mul2(dh[v].pair(i), pre[v][i])), dy[v].pair(i));
-        sum_pre[v][i] = fma2(dh[v].pair(i), yn, sum_pre[v][i]);
-        sum_t[v][i] = fma2(t, fn, sum_t[v][i]);
-        if (with_x) sum_res[v][i] = fma2(t, x[v].pair(i), sum_res[v][i]);
+        const f2 t = fma2(yn[v][i], nm2, q[v][i]);
+        sum_t[v][i] = fma2(t, fn[v][i], sum_t[v][i]);
+        if (X) sum_res[v][i] = fma2(t, x[v].pair(i), sum_res[v][i]);
         dx[i] = mul2(res[v][i], t);
-        df[i] = mul2(rr1, fma2(fn, nm1, mul2(gw[v][i], t)));
+        df[i] = mul2(rr1, fma2(fn[v][i], nm1, mul2(gw[v][i], t)));
       }
       store_chunk<T, VEC>(dx_row, u, v, dx);
       store_chunk<T, VEC>(df_row, u, v, df);
     }
+    dx_row += a.lddx;
+    df_row += a.lddf;
   }
   if (chunk >= 0) flush();
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     if (!post_written) store_param<VEC>(part_post, u, v, sum_t[v]);  // no rows: zeros
     store_param<VEC>(a.part_pre + id * a.cols, u, v, sum_pre[v]);
-    if (with_x) store_param<VEC>(a.part_res + id * a.cols, u, v, sum_res[v]);
+    if (X) store_param<VEC>(a.part_res + id * a.cols, u, v, sum_res[v]);
   }
   if (clusters > 1) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
 }
@@ -760,38 +797,43 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdArgs a)
 
 // Column sums over the units' partial rows (blockIdx.y: 0 pre, 1 post, 2 res)
 // and, from 3 on, over the chunks of gate group blockIdx.y - 3: 32 columns a
-// block, its 32 warps over the rows in turn, then the warps in order.
-__global__ void __launch_bounds__(1024) norm_bwd_sums_kernel(const NormBwdArgs a) {
-  __shared__ float red[32][33];
+// block, its eight warps over the rows in turn, eight loads in flight, then
+// the warps in order.
+__global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a) {
+  __shared__ float red[8][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   const float* src;
   float* dst;
-  int64_t n = a.units;
+  int n = (int)a.units;
   if (blockIdx.y == 0) { src = a.part_pre; dst = a.d_pre_w; }
   else if (blockIdx.y == 1) { src = a.part_post; dst = a.d_post_w; }
   else if (blockIdx.y == 2) { src = a.part_res; dst = a.d_res; }
   else {
     const int64_t g = blockIdx.y - 3;
     // The last group may be short: its chunks past the rows are not written.
-    n = (min(a.per_gate, a.rows - g * a.per_gate) + a.chunk_rows - 1) / a.chunk_rows;
+    n = (int)((min(a.per_gate, a.rows - g * a.per_gate) + a.chunk_rows - 1) / a.chunk_rows);
     src = a.part_gate + g * a.chunks_per_group * a.cols;
     dst = a.d_gate + g * a.cols;
   }
   if (!dst) return;
   float s = 0.f;
   if (c < a.cols) {
-#pragma unroll 8
-    for (int64_t i = warp; i < n; i += 32) s += src[i * a.cols + c];
+    src += c;
+    for (int i = warp; i < n; i += 64) {
+      float v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[k] = i + 8 * k < n ? src[(int64_t)(i + 8 * k) * a.cols] : 0.f;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s += v[k];
+    }
   }
   red[warp][lane] = s;
   __syncthreads();
-  // Transposed: warp w adds up column w, lane by lane in a fixed tree.
-  float v = red[lane][warp];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int64_t out = (int64_t)blockIdx.x * 32 + warp;
-  if (lane == 0 && out < a.cols) dst[out] = blockIdx.y >= 3 ? v * a.post_w[out] : v;
+  if (warp == 0 && c < a.cols) {
+    for (int w = 1; w < 8; ++w) s += red[w][lane];
+    dst[c] = blockIdx.y >= 3 ? s * a.post_w[c] : s;
+  }
 }
 
 // ------------------------------------------------------------ launches
@@ -861,12 +903,19 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
   } else {
     const RowShape r = bwd_shape(a.cols);
     const int64_t ctas = a.units / r.units;
-    if (a.vec) e = launch_rows(norm_bwd_rows_kernel<T, true>, a, r, ctas, ring_bytes<T>(r, 5), s);
-    else e = launch_rows(norm_bwd_rows_kernel<T, false>, a, r, ctas, red_bytes(r.units), s);
+    const int smem = a.vec ? ring_bytes<T>(r, 5) : red_bytes(r.units);
+    auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
+    const bool dy = a.dy != nullptr, x = a.d_res != nullptr;
+    if (a.vec)
+      e = dy ? (x ? go(norm_bwd_rows_kernel<T, true, true, true>) : go(norm_bwd_rows_kernel<T, true, true, false>))
+             : (x ? go(norm_bwd_rows_kernel<T, true, false, true>) : go(norm_bwd_rows_kernel<T, true, false, false>));
+    else
+      e = dy ? (x ? go(norm_bwd_rows_kernel<T, false, true, true>) : go(norm_bwd_rows_kernel<T, false, true, false>))
+             : (x ? go(norm_bwd_rows_kernel<T, false, false, true>) : go(norm_bwd_rows_kernel<T, false, false, false>));
   }
   if (e != cudaSuccess) return e;
   const unsigned ys = 3 + (a.d_gate && a.chunks_per_group > 1 ? (unsigned)a.groups : 0u);
-  norm_bwd_sums_kernel<<<dim3((unsigned)((a.cols + 31) / 32), ys), 1024, 0, s>>>(a);
+  norm_bwd_sums_kernel<<<dim3((unsigned)((a.cols + 31) / 32), ys), 256, 0, s>>>(a);
   return cudaGetLastError();
 }
 
