@@ -132,7 +132,7 @@ int dmuon_mxfp4_dequantize(dmuon_handle_t h, const void* data, const void* scale
   if ((rc = check_packed(h, data, scales, "mxfp4_dequantize: matrix"))) return rc;
   if ((rc = check_matrix(h, dst, dtype, k, ld, "mxfp4_dequantize: dst"))) return rc;
   if (dst == data || dst == scales) return fail(h, DMUON_ERR_ARG, "mxfp4_dequantize: dst is an input");
-  if (((rows + 31) / 32) * ((k + 511) / 512) > INT32_MAX) return fail(h, DMUON_ERR_ARG, "mxfp4_dequantize: too many tiles");
+  if (((rows + 31) / 32) * ((k + 255) / 256) > INT32_MAX) return fail(h, DMUON_ERR_ARG, "mxfp4_dequantize: too many tiles");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
   cudaStream_t stream = (cudaStream_t)stream_;
   MxDequantArgs a{};
@@ -142,7 +142,7 @@ int dmuon_mxfp4_dequantize(dmuon_handle_t h, const void* data, const void* scale
   a.k = k;
   a.dst = dst;
   a.ld = ld;
-  a.vec = aligned(dst, 16) && (ld * elem_size(dtype)) % 16 == 0;
+  a.vec = aligned(dst, 32) && (ld * elem_size(dtype)) % 32 == 0;
   LaunchGuard g(h, stream, DMUON_KIND_MX_DEQUANTIZE);
   const cudaError_t e = launch_mx_dequant(a, dtype, stream);
   if (e != cudaSuccess) return fail(h, cuda_err(e), "mxfp4_dequantize launch", e);
