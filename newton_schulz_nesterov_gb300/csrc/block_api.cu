@@ -174,11 +174,16 @@ int dmuon_mxfp4_gemm(dmuon_handle_t h, const void* a_data, const void* a_scales,
   a.alpha = alpha;
   a.beta = beta;
   a.dtype = dtype;
-  a.vec = aligned(d, 32) && (ldd * elem_size(dtype)) % 32 == 0;
+  a.vec = rows_aligned(d, ldd, dtype);
   a.err = h->d_op_err;
   a.timeout_ns = h->wait_timeout_ns;
+  // CTA pairs once the 128 x 128 tiles of the one-CTA kernel would need a
+  // second wave (an SM takes about 70 bytes a clock from L2 either way, and a
+  // pair's tile asks half as many of it for a product): 1024 x 4096 x 4096
+  // (256 tiles) 10.5 us against 15.0, 512 x 4096 x 4096 (128) 10.2 against 8.2.
+  const int64_t small_tiles = ((m + 127) / 128) * ((n + 127) / 128);
   const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
-  const bool pairs = h->max_clusters > 0 && pair_tiles >= h->max_clusters && m > 256;
+  const bool pairs = h->max_clusters > 0 && m > 128 && n > 128 && small_tiles > h->num_sms;
   a.swapped = !pairs && m <= 256;
   a.p_rows = a.swapped ? n : m;
   a.q_rows = a.swapped ? m : n;
@@ -186,7 +191,7 @@ int dmuon_mxfp4_gemm(dmuon_handle_t h, const void* a_data, const void* a_scales,
   const void *qd = a.swapped ? a_data : b_data, *qs = a.swapped ? a_scales : b_scales;
   // A Q of at most 128 rows is one tile (a tile of fewer than 128 rows has
   // to start on a scale tile).
-  const int nt = pairs ? 256 : a.q_rows <= 32 ? 32 : a.q_rows <= 64 ? 64 : a.q_rows <= 128 ? 128 : 256;
+  const int nt = pairs ? 256 : a.q_rows <= 32 ? 32 : a.q_rows <= 64 ? 64 : 128;
   a.q_tiles = (int)((a.q_rows + nt - 1) / nt);
   const int64_t tiles = (a.p_rows + 127) / 128 * a.q_tiles;
   if (tiles > INT32_MAX / 8) return fail(h, DMUON_ERR_ARG, "mxfp4_gemm: too many tiles");
@@ -198,9 +203,14 @@ int dmuon_mxfp4_gemm(dmuon_handle_t h, const void* a_data, const void* a_scales,
   if (pairs) {
     e = launch_mx_gemm_pair(a, (int)std::min<int64_t>(pair_tiles, h->max_clusters), stream);
   } else {
+    // K split over a cluster while that fills idle SMs.  Joining costs 0.3 us at
+    // NT = 32 and about 2 us at 128, a stage 0.25 us: 1 x 4096 x 4096 6.7 us
+    // whole, 4.6 in four; 512 x 512 x 512 4.4 whole, 6.2 in two.  Eight ranks of
+    // 210 KB each do not all find an SM at once (128 x 4096 x 4096: 22 us).
     const int64_t stages = (k + 255) / 256;
+    const int most = nt == 128 ? 4 : 8;
     int split = 1;
-    while (split < 8 && tiles * split * 2 <= h->num_sms && stages >= split * 4) split *= 2;
+    while (split < most && tiles * split * 2 <= h->num_sms && stages >= split * 2 && (nt == 32 || stages >= 8)) split *= 2;
     e = launch_mx_gemm(a, nt, split, stream);
   }
   if (e != cudaSuccess) return fail(h, cuda_err(e), "mxfp4_gemm launch", e);

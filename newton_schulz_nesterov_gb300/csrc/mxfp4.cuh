@@ -57,7 +57,7 @@ struct MxGemmArgs {
   int swapped;
   int dtype;                   // DMUON_F32 / _BF16 / _F16
   int q_tiles;
-  int vec;                     // D's rows are 32-byte aligned
+  int vec;                     // D's rows are 16-byte aligned
   int* err;
   unsigned long long timeout_ns;
 };

@@ -6,13 +6,16 @@
 // product is exact; what is rounded is the fp32 accumulation over blocks and
 // the store.
 //
-// One CTA computes a tile of 128 rows of P by NT rows of Q (P, Q = A, B, or
-// B, A when A has few rows: the tokens are then the MMA's N and the weights
-// fill its 128 lanes).  Few tiles leave SMs idle while K is long, so a cluster
-// of `split` CTAs may share a tile: each accumulates a run of K blocks, puts
-// its fp32 partial tile in its own shared memory, and each then adds up its
-// share of the columns over the cluster in rank order -- no workspace, no
-// second launch, and the same order every time.
+// Products that fill the device run on CTA pairs (below).  The others: one CTA
+// computes a tile of 128 rows of P by NT rows of Q (P, Q = A, B, or B, A when A
+// has few rows: the tokens are then the MMA's N and the weights fill its 128
+// lanes).  Few tiles leave SMs idle while K is long, so a cluster of `split`
+// CTAs may share a tile: each accumulates a run of K blocks, sends every rank
+// its share of the rows of the fp32 partial tile, and each rank then adds up
+// what it got, in rank order -- no workspace, no second launch, and the same
+// order every time.  The shares go by bulk copies from shared memory to shared
+// memory: with one remote store a value, halving K over two CTAs cost 8.4 us
+// more at 512 x 512 x 512.
 //
 // Warps: 0 TMA producer, 1 TMEM allocator and MMA issuer, 2-5 epilogue.
 // A stage is 256 elements of K: 128-byte rows of packed codes (128-byte
@@ -80,16 +83,33 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int half) {
 constexpr uint32_t desc_hi() { return (1024u >> 4) | (1u << 14) | (2u << 29); }
 __device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
 
+// One lane of a converged warp: the warp's loops stay uniform, so addresses
+// and descriptors are kept in uniform registers, which the tensor core and
+// TMA instructions take.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok));
+  return ok != 0;
+}
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Bulk copy of this CTA's shared memory to another's, counted on its barrier.
+__device__ __forceinline__ void send(uint32_t dst_cluster, uint32_t src, uint32_t bytes, uint32_t bar_cluster) {
+  asm volatile("cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst_cluster),
+               "r"(src), "r"(bytes), "r"(bar_cluster)
+               : "memory");
+}
+
 __device__ __forceinline__ uint32_t cluster_size() {
   uint32_t r;
   asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
   return r;
-}
-
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
 }
 
 // 32 lanes x 96 columns of tensor memory, waited for.
@@ -135,18 +155,16 @@ constexpr int kScratch = 32 * 36;  // words of an epilogue warp's transposing sc
 template <int NT>
 struct Cfg {
   static constexpr int kQBytes = NT * kStageK / 2;
-  static constexpr int kQTiles = (NT + 127) / 128;          // 128-row scale tiles of Q
-  static constexpr int kScales = kScaleBytes * (1 + kQTiles);
-  static constexpr int kStage = kPBytes + kQBytes + kScales;  // a multiple of 1024
-  static constexpr int kN = NT == 256 ? 4 : (NT == 128 ? 5 : 6);
-  static constexpr int kSmem = 1024 + kN * kStage + 4 * kScratch * 4 + 256;
-  static constexpr int kScaleCols = 8 + 8 * kQTiles;        // of one stage
-  static constexpr int kCols = NT + 2 * kScaleCols;
-  static constexpr int kTmem = kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static constexpr int kPitch = kPRows + 1;                 // floats of a partial tile's column
+  static constexpr int kStage = kPBytes + kQBytes + 2 * kScaleBytes;  // a multiple of 1024
+  static constexpr int kN = NT == 32 ? 8 : NT == 64 ? 6 : 4;  // stages
+  static constexpr int kShare = kPRows * (NT + 4) * 4;      // partial rows, here and from the ranks: row pitch NT + 4 floats
+  static constexpr int kEpi = kShare > 4 * kScratch * 4 ? kShare : 4 * kScratch * 4;
+  static constexpr int kSmem = 1024 + kN * kStage + kEpi + 256;
+  static constexpr int kTmem = NT <= 32 ? 64 : NT <= 64 ? 128 : 256;  // the accumulator, two sets of 16 scale columns
   static_assert(kStage % 1024 == 0, "128-byte swizzle atoms start on 1 KB");
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  static_assert(NT * kPitch * 4 <= kN * kStage, "the partial tile fits the stages");
+  static_assert(NT + 32 <= kTmem, "tensor memory");
+  static_assert(kShare <= kN * kStage, "this CTA's partial rows lie where its stages were");
 };
 
 template <typename T>
@@ -279,28 +297,107 @@ __device__ __forceinline__ void store_block(const MxGemmArgs& a, int64_t row0, i
   __syncwarp();
 }
 
+// Rows [p0, p0 + r_here) x columns [q0, q0 + q_here) of the product: the sum
+// of the SPLIT ranks' shares ([rank][128 / SPLIT][pitch], this rank's own at
+// `mine`) in rank order, by 128 threads, four columns and several rows a
+// thread in flight.
+template <int SPLIT, typename T>
+__device__ __forceinline__ void add_shares(const MxGemmArgs& a, const float* mine, const float* theirs, int rank, int pitch,
+                                           int r_here, int q_here, int p0, int q0, int t) {
+  constexpr int kRows = kPRows / SPLIT;
+  const float* from[SPLIT];
+#pragma unroll
+  for (int k = 0; k < SPLIT; ++k) from[k] = k == rank ? mine : theirs + k * kRows * pitch;
+  auto sum_at = [&](int off) {
+    float4 v[SPLIT];
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k) v[k] = *reinterpret_cast<const float4*>(from[k] + off);
+#pragma unroll
+    for (int k = 1; k < SPLIT; ++k) {
+      v[0].x += v[k].x; v[0].y += v[k].y; v[0].z += v[k].z; v[0].w += v[k].w;
+    }
+    return v[0];
+  };
+  T* d = (T*)a.d;
+  if (a.swapped) {  // lanes hold consecutive columns of D, four rows of it each
+    const int r = t % kRows;
+    if (r >= r_here) return;
+    T* dst = d + (int64_t)q0 * a.ldd + p0 + r;
+#pragma unroll 2
+    for (int q = t / kRows * 4; q < q_here; q += 128 / kRows * 4) {
+      const float4 v = sum_at(r * pitch + q);
+      const float o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (q + e < q_here) put<T>(a, dst + (int64_t)(q + e) * a.ldd, o[e]);
+    }
+  } else {
+    const int lane = t & 31;
+    for (int q = lane * 4; q < q_here; q += 128) {
+      T* dst = d + (int64_t)p0 * a.ldd + q0 + q;
+#pragma unroll 4
+      for (int r = t >> 5; r < r_here; r += 4) {
+        const float4 v = sum_at(r * pitch + q);
+        const float o[4] = {v.x, v.y, v.z, v.w};
+        T* at = dst + (int64_t)r * a.ldd;
+        if (a.vec && q + 4 <= q_here) {  // rows on 16 bytes: four columns whole
+          constexpr int kPer = Pack<T>::kPer, kWords = 4 / kPer;
+          uint32_t w[kWords];
+          float f[4];
+          if (a.beta != 0.f) {
+            if constexpr (kWords == 4) {
+              const uint4 x = *reinterpret_cast<const uint4*>(at);
+              w[0] = x.x; w[1] = x.y; w[kWords - 2] = x.z; w[kWords - 1] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(at);
+              w[0] = x.x; w[1] = x.y;
+            }
+#pragma unroll
+            for (int k = 0; k < kWords; ++k) Pack<T>::unpack(w[k], f + k * kPer);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f[e] = a.beta != 0.f ? fmaf(a.beta, f[e], a.alpha * o[e]) : a.alpha * o[e];
+#pragma unroll
+          for (int k = 0; k < kWords; ++k) w[k] = Pack<T>::pack(f + k * kPer);
+          if constexpr (kWords == 4) *reinterpret_cast<uint4*>(at) = make_uint4(w[0], w[1], w[kWords - 2], w[kWords - 1]);
+          else *reinterpret_cast<uint2*>(at) = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (q + e < q_here) put<T>(a, at + e, o[e]);
+        }
+      }
+    }
+  }
+}
+
 template <int NT, typename T>
 __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_constant__ MxGemmArgs a) {
   using C = Cfg<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
-  uint32_t* scratch = reinterpret_cast<uint32_t*>(stages + C::kN * C::kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + 4 * kScratch);
+  uint32_t* scratch = reinterpret_cast<uint32_t*>(stages + C::kN * C::kStage);  // or the ranks' partial rows
+  uint64_t* full = reinterpret_cast<uint64_t*>(stages + C::kN * C::kStage + C::kEpi);
   uint64_t* empty = full + C::kN;
   uint64_t* done = empty + C::kN;       // the accumulator is complete
   uint64_t* drain = done + 1;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  uint64_t* shares = drain + 1;         // the other ranks' partial rows are here
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(shares + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t tmo = a.timeout_ns ? a.timeout_ns : kWaitNs;
-  const uint32_t split = cluster_size(), rank = ptx::cluster_ctarank();
+  const int split = (int)cluster_size(), rank = (int)ptx::cluster_ctarank();
   const int tile = blockIdx.x / split;
   const int p0 = (tile / a.q_tiles) * kPRows, q0 = (tile % a.q_tiles) * NT;
-  // This CTA's run of K stages: the first `extra` ranks take one more.
+  const int q_here = min(NT, (int)a.q_rows - q0);  // columns of the accumulator that count
+  // This CTA's run of K stages: the first `extra` ranks take one more (the
+  // host never asks for more ranks than stages).
   const int total = (int)((a.k + kStageK - 1) / kStageK);
-  const int base = total / (int)split, extra = total % (int)split;
-  const int kb0 = (int)rank * base + min((int)rank, extra), kbn = base + ((int)rank < extra ? 1 : 0);
+  const int base = total / split, extra = total % split;
+  const int kb0 = rank * base + min(rank, extra), kbn = base + (rank < extra ? 1 : 0);
+  // Split: rank r adds up rows [r rows, (r + 1) rows) of the tile, `pitch` floats apart.
+  const int rows = kPRows / split, pitch = ((q_here + 3) & ~3) + 4;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kN; ++s) {
@@ -309,8 +406,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
     }
     ptx::mbar_init(ptx::smem_addr(done), 1);
     ptx::mbar_init(ptx::smem_addr(drain), 1);
+    ptx::mbar_init(ptx::smem_addr(shares), 1);
     *abort_flag = 0;
     ptx::fence_mbar_init();
+    if (split > 1) ptx::mbar_expect_tx(ptx::smem_addr(shares), (split - 1) * rows * pitch * 4);
   }
   if (warp == 1) {
     ptx::tmem_alloc(ptx::smem_addr(tmem_slot), C::kTmem);
@@ -318,18 +417,21 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
   }
   ptx::tc_fence_before();
   __syncthreads();
+  if (split > 1) cluster_arrive();  // this rank's barrier of shares is ready
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const uint32_t full0 = ptx::smem_addr(full), empty0 = ptx::smem_addr(empty), stage0 = ptx::smem_addr(stages);
 
-  bool have = kbn > 0;  // epilogue warps: the accumulator may be read
+  bool have = true;  // epilogue warps: the accumulator may be read
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
-      bool ok = true;
-      for (; it < kbn; ++it) {
-        const uint32_t s = it % C::kN;
-        if (!bounded_wait(ptx::smem_addr(empty + s), ((it / C::kN) & 1u) ^ 1u, abort_flag, a.err, tmo)) { ok = false; break; }
-        const uint32_t fb = ptx::smem_addr(full + s), st = ptx::smem_addr(stages + s * C::kStage);
+    const bool elected = elect_one();
+    uint32_t s = 0, ph = 0;
+    int it = 0;
+    bool ok = true;
+    for (; it < kbn; ++it) {
+      if (!bounded_wait_warp(empty0 + s * 8, ph ^ 1u, abort_flag, a.err, tmo)) { ok = false; break; }
+      if (elected) {
+        const uint32_t fb = full0 + s * 8, st = stage0 + s * C::kStage;
         const int kb = kb0 + it;
         ptx::mbar_expect_tx(fb, C::kStage);
         ptx::tma_load_2d(st, &a.p_data, kb * (kStageK / 2), p0, fb);
@@ -337,99 +439,105 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
         tma_load_3d(st + kPBytes + C::kQBytes, &a.p_scales, 0, kb * 2, p0 / 128, fb);
         tma_load_3d(st + kPBytes + C::kQBytes + kScaleBytes, &a.q_scales, 0, kb * 2, q0 / 128, fb);
       }
-      if (!ok || *abort_flag) {  // no copy may land after the CTA has gone
-        const int out = it < C::kN ? it : C::kN;
-        for (int i = it - out; i < it; ++i)
-          bounded_wait_slow(ptx::smem_addr(full + i % C::kN), (i / C::kN) & 1u, abort_flag, a.err, false, kWaitNs);
-      }
+      if (++s == (uint32_t)C::kN) { s = 0; ph ^= 1u; }
+    }
+    if (!ok || *abort_flag) {  // no copy may land after the CTA has gone
+      const int out = it < C::kN ? it : C::kN;
+      for (int i = it - out; i < it; ++i)
+        bounded_wait_slow(full0 + i % C::kN * 8, (i / C::kN) & 1u, abort_flag, a.err, false, kWaitNs);
     }
   } else if (warp == 1) {
-    if (lane == 0 && kbn > 0) {
-      // A tile of NT < 128 is Q's only one, so every tile starts on a scale tile.
-      bool ok = true, issued = false;
-      for (int it = 0; it < kbn; ++it) {
-        const uint32_t s = it % C::kN;
-        if (!bounded_wait(ptx::smem_addr(full + s), (it / C::kN) & 1u, abort_flag, a.err, tmo)) { ok = false; break; }
-        ptx::tc_fence_after();
-        const uint32_t st = ptx::smem_addr(stages + s * C::kStage);
-        const uint32_t sc = st + kPBytes + C::kQBytes;
-        const uint32_t tp = tmem + NT + (it & 1) * C::kScaleCols, tq = tp + 8;
-        // Scale columns: P [k tile][4], Q [k tile][row tile][4].
+    // A tile of NT < 128 is Q's only one, so every tile starts on a scale tile.
+    const bool elected = elect_one();
+    const int last_parts = (int)((a.k - (int64_t)(total - 1) * kStageK + 63) / 64);  // K = 64 products of the last stage
+    uint32_t s = 0, ph = 0;
+    bool ok = true, issued = false;
+    for (int it = 0; it < kbn; ++it) {
+      if (!bounded_wait_warp(full0 + s * 8, ph, abort_flag, a.err, tmo)) { ok = false; break; }
+      ptx::tc_fence_after();
+      if (elected) {
+        const uint32_t st = stage0 + s * C::kStage, sc = st + kPBytes + C::kQBytes;
+        const uint32_t tp = tmem + NT + (it & 1) * 16, tq = tp + 8;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           copy_scales(tp + t * 4, sc + t * kMxScaleTile);
-#pragma unroll
-          for (int r = 0; r < C::kQTiles; ++r)
-            copy_scales(tq + (t * C::kQTiles + r) * 4, sc + kScaleBytes + (r * 2 + t) * kMxScaleTile);
+          copy_scales(tq + t * 4, sc + kScaleBytes + t * kMxScaleTile);
         }
-        const int64_t left = a.k - (int64_t)(kb0 + it) * kStageK;  // elements of K from this stage on
+        const int parts = kb0 + it + 1 < total ? 4 : last_parts;  // products past K would only add zeros
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (j * 64 < left)
+        for (int j = 0; j < 4; ++j)
+          if (j < parts)
             mma_mxf4(tmem, ptx::desc_sw128(st + j * 32, 16, 1024), ptx::desc_sw128(st + kPBytes + j * 32, 16, 1024),
-                     idesc_mxf4(kPRows, NT, j & 1), tp + (j / 2) * 4, tq + (j / 2) * C::kQTiles * 4, (it | j) != 0);
-        }
-        issued = true;
-        ptx::mma_commit(ptx::smem_addr(empty + s));
+                     idesc_mxf4(kPRows, NT, j & 1), tp + (j / 2) * 4, tq + (j / 2) * 4, (it | j) != 0);
+        ptx::mma_commit(empty0 + s * 8);
+        if (it + 1 == kbn) ptx::mma_commit(ptx::smem_addr(done));
       }
-      if (ok) ptx::mma_commit(ptx::smem_addr(done));
-      if (issued && (!ok || *abort_flag)) {
-        ptx::mma_commit(ptx::smem_addr(drain));
-        bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
-      }
+      issued = true;
+      if (++s == (uint32_t)C::kN) { s = 0; ph ^= 1u; }
     }
-  } else if (have) {
+    if (issued && (!ok || *abort_flag)) {
+      if (elected) ptx::mma_commit(ptx::smem_addr(drain));
+      bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
+    }
+  } else {
     have = bounded_wait_warp(ptx::smem_addr(done), 0, abort_flag, a.err, tmo);
     ptx::tc_fence_after();
   }
 
   // ------------------------------------------------------------ epilogue
-  float* part = reinterpret_cast<float*>(stages);  // [NT][kPitch], once the stages are free
   const int quad = warp & 3, p = quad * 32 + lane;
+  T* d = (T*)a.d;
   if (split == 1) {
     if (warp >= 2 && have) {
-      T* d = (T*)a.d;
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 32) {
-        if (q0 + c >= a.q_rows) break;
+      for (int c = 0; c < q_here; c += 32) {
         uint32_t v[32];
         ptx::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
         if (!a.swapped) {
           store_block<T>(a, p0 + quad * 32, q0 + c, a.p_rows, a.q_rows, v, scratch + (warp - 2) * kScratch, lane);
         } else if (p0 + p < a.p_rows) {  // lanes hold consecutive columns of D
+          T* dst = d + (int64_t)(q0 + c) * a.ldd + p0 + p;
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (q0 + c + j < a.q_rows) put<T>(a, d + (q0 + c + j) * a.ldd + p0 + p, __uint_as_float(v[j]));
+            if (c + j < q_here) put<T>(a, dst + j * a.ldd, __uint_as_float(v[j]));
         }
       }
     }
   } else {
+    cluster_wait();  // every rank's barrier is
     if (warp >= 2) {
       // All MMAs of this CTA are complete, so its stages are free.
+      float* mine = reinterpret_cast<float*>(stages);
+      if (have) {
 #pragma unroll 1
-      for (int c = 0; c < NT; c += 32) {
-        uint32_t v[32];
-        if (have) ptx::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
+        for (int c = 0; c < q_here; c += 32) {
+          uint32_t v[32];
+          ptx::tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16) + c, v);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) part[(c + j) * C::kPitch + p] = have ? __uint_as_float(v[j]) : 0.f;
+          for (int j = 0; j < 32; j += 4)
+            if (c + j < q_here)
+              *reinterpret_cast<uint4*>(mine + p * pitch + c + j) = make_uint4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+        }
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      }
+      asm volatile("bar.sync 1, 128;" ::: "memory");
+      const uint32_t bytes = (uint32_t)(rows * pitch) * 4;
+      const float* theirs = reinterpret_cast<const float*>(scratch);  // [rank][rows][pitch]
+      const int t = threadIdx.x - 64;
+      if (have && t < split && t != rank)
+        send(ptx::mapa_shared(ptx::smem_addr(scratch) + rank * bytes, t), ptx::smem_addr(mine) + t * bytes, bytes,
+             ptx::mapa_shared(ptx::smem_addr(shares), t));
+      if (!have) bounded_wait_slow(ptx::smem_addr(shares), 0, abort_flag, a.err, false, kWaitNs);  // what is on its way lands
+      else have = bounded_wait_warp(ptx::smem_addr(shares), 0, abort_flag, a.err, tmo);
+      if (have) {
+        const int pr0 = p0 + rank * rows, r_here = min(rows, (int)a.p_rows - pr0);
+        mine += rank * rows * pitch;
+        if (split == 2) add_shares<2, T>(a, mine, theirs, rank, pitch, r_here, q_here, pr0, q0, t);
+        else if (split == 4) add_shares<4, T>(a, mine, theirs, rank, pitch, r_here, q_here, pr0, q0, t);
+        else add_shares<8, T>(a, mine, theirs, rank, pitch, r_here, q_here, pr0, q0, t);
       }
     }
-    ptx::cluster_sync();
-    if (!*abort_flag) {
-      // Rank r stores columns [r NT / split, (r + 1) NT / split), the sum over ranks in order.
-      const int c0 = NT * (int)rank / (int)split, c1 = NT * ((int)rank + 1) / (int)split;
-      const uint32_t mine = ptx::smem_addr(part);
-      T* d = (T*)a.d;
-      for (int i = threadIdx.x; i < (c1 - c0) * kPRows; i += kThreads) {
-        const int pp = a.swapped ? i % kPRows : i / (c1 - c0), q = c0 + (a.swapped ? i / kPRows : i % (c1 - c0));
-        if (p0 + pp >= a.p_rows || q0 + q >= a.q_rows) continue;
-        float sum = 0.f;
-        for (uint32_t r = 0; r < split; ++r)
-          sum += ld_cluster(ptx::mapa_shared(mine + (q * C::kPitch + pp) * 4, r));
-        put<T>(a, a.swapped ? d + (q0 + q) * a.ldd + p0 + pp : d + (p0 + pp) * a.ldd + q0 + q, sum);
-      }
-    }
-    ptx::cluster_sync();  // a peer may still read this CTA's tile
+    ptx::cluster_sync();  // no rank leaves while its shares are being read or written
   }
 
   ptx::tc_fence_before();
@@ -489,19 +597,6 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d, uint32_t alo, uint32_t
       "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], da, db, %3, [%4], [%5], p;\n\t}" ::"r"(d),
       "r"(alo), "r"(blo), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "n"(kDescHi)
       : "memory");
-}
-
-// One lane of a converged warp: the warp's loops stay uniform, so addresses
-// and descriptors are kept in uniform registers, which the tensor core and
-// TMA instructions take.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok));
-  return ok != 0;
 }
 
 // Tile t of a pair's walk: groups of kGroup tile rows, column by column inside
@@ -673,8 +768,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
       tile_of(t, tm, tn, mt, nt);
       const int64_t row0 = (int64_t)mt * 256 + rank * 128 + quad * 32, col0 = (int64_t)nt * 256;
       if (a.beta != 0.f && a.vec && row0 + lane < a.p_rows) {
-        // The tile's old D comes to L2 while its products run (whole rows of
-        // it: D's rows are 32-byte aligned).
+        // The tile's old D comes to L2 while its products run.
         const uint32_t bytes = (uint32_t)min((int64_t)256, a.q_rows - col0) * (uint32_t)sizeof(T) & ~15u;
         if (bytes)
           asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"((const T*)a.d + (row0 + lane) * a.ldd + col0), "r"(bytes)
@@ -784,7 +878,6 @@ cudaError_t mx_gemm_configure() {
   if ((e = configure_nt<32>()) != cudaSuccess) return e;
   if ((e = configure_nt<64>()) != cudaSuccess) return e;
   if ((e = configure_nt<128>()) != cudaSuccess) return e;
-  if ((e = configure_nt<256>()) != cudaSuccess) return e;
   if ((e = configure_pair<float>()) != cudaSuccess) return e;
   if ((e = configure_pair<__nv_bfloat16>()) != cudaSuccess) return e;
   return configure_pair<__half>();
@@ -799,8 +892,7 @@ cudaError_t launch_mx_gemm_pair(const MxGemmArgs& a, int pairs, cudaStream_t s) 
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, int nt, int split, cudaStream_t s) {
   if (nt == 32) return launch_nt<32>(a, split, s);
   if (nt == 64) return launch_nt<64>(a, split, s);
-  if (nt == 128) return launch_nt<128>(a, split, s);
-  return launch_nt<256>(a, split, s);
+  return launch_nt<128>(a, split, s);
 }
 
 }  // namespace dmuon

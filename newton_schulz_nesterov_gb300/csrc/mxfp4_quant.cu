@@ -64,29 +64,38 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&f)[8]) {
 // scaled up (v < 1 is a subnormal on either side): its bits are the code with
 // 22 bits of fraction, code(v) 2^22, linear inside every interval of the grid.
 // The code rounds up when fraction / 2^22 > (r + 1/2) / 256, so it is
-//   (bits + 2^22 - 1 - (2r + 1) 2^13) >> 22 = (4 bits + ((255 - r) << 16 | 0x7FFF)) >> 24
+//   (bits + 2^22 - 1 - (2r + 1) 2^13) >> 22 = (4 bits - (r << 16 | 0xFF008001)) >> 24
 // Scaling rounds up: a value that is not representable stays on its side of
-// every threshold.  Seven instructions an element instead of nineteen on
-// floats (quantising 16384 x 14336 bf16 in both directions with noise: 403 us
-// on floats).
+// every threshold.  In float arithmetic (nineteen instructions an element)
+// quantising 16384 x 14336 bf16 in both directions with noise took 403 us,
+// this 217; byte permutes and logic then fill 82 % of the ALU pipe's slots.
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126
 
-// 4 bits + threshold of an element: its code is the top byte (8 only for a
-// value past 6 that rounds up).  `sel` picks the element's byte of ~noise.
-__device__ __forceinline__ uint32_t stochastic(float v, float inv, uint32_t not_noise, uint32_t sel) {
+// 4 bits - threshold of an element: its code is the top byte (8 only for a
+// value past 6 that rounds up).  `sel` picks the element's byte of the noise.
+__device__ __forceinline__ uint32_t stochastic(float v, float inv, uint32_t noise, uint32_t sel) {
   const uint32_t bits = __float_as_uint(__fmul_ru(__fmul_ru(fabsf(v), inv), kTiny));
-  return (bits << 2) + __byte_perm(not_noise, 0x7FFFu, 0x7054u | (sel << 8));
+  return (bits << 2) - __byte_perm(noise, 0xFF008001u, 0x7054u | (sel << 8));
 }
 
-// Top bytes of eight results to eight 4-bit codes; above 7 saturates.  s0, s1
-// hold the elements' sign bits in bit 7 of their bytes (even, odd elements).
-__device__ __forceinline__ uint32_t gather_codes(const uint32_t (&a)[8], uint32_t s0, uint32_t s1) {
-  uint32_t even = __byte_perm(__byte_perm(a[0], a[2], 0x0073), __byte_perm(a[4], a[6], 0x0073), 0x5410);
-  uint32_t odd = __byte_perm(__byte_perm(a[1], a[3], 0x0073), __byte_perm(a[5], a[7], 0x0073), 0x5410);
-  even -= (even >> 3) & 0x01010101u;
-  odd -= (odd >> 3) & 0x01010101u;
-  return (even | ((s0 >> 4) & 0x08080808u)) | (((odd << 4)) | (s1 & 0x80808080u));
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
 }
+
+// Top bytes of eight results to eight 4-bit codes.  s0, s1 hold the elements'
+// sign bits in bit 7 of their bytes (even, odd elements).
+__device__ __forceinline__ uint32_t gather_codes(const uint32_t (&a)[8], uint32_t s0, uint32_t s1, int ceil_scale) {
+  uint32_t even = top_bytes(a[0], a[2], a[4], a[6]), odd = top_bytes(a[1], a[3], a[5], a[7]);
+  if (!ceil_scale) {  // 8 saturates
+    even -= (even >> 3) & 0x01010101u;
+    odd -= (odd >> 3) & 0x01010101u;
+  }
+  return (even | ((s0 >> 4) & 0x08080808u)) | ((odd << 4) | (s1 & 0x80808080u));
+}
+
+// Sign bytes of two pairs of 16-bit values: bytes 1 (low halves) of a, b, then
+// bytes 3 (high halves) of a, b.
+__device__ __forceinline__ uint32_t sign_bytes(uint32_t a, uint32_t b) { return __byte_perm(a, b, 0x7351); }
 
 // ------------------------------------------------------------ input types
 
@@ -99,10 +108,11 @@ struct In<float> {
 template <>
 struct In<__nv_bfloat16> {
   static constexpr int kSize = 2;
+  // Larger magnitude of each half (its sign means nothing), NaN if either is.
   static __device__ __forceinline__ uint32_t absmax(uint32_t m, uint32_t w) {
-    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<__nv_bfloat162*>(&m),
-                                         __habs2(*reinterpret_cast<__nv_bfloat162*>(&w)));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w));
+    return r;
   }
   static __device__ __forceinline__ float lo(uint32_t w) { return __uint_as_float(w << 16); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
@@ -111,16 +121,13 @@ template <>
 struct In<__half> {
   static constexpr int kSize = 2;
   static __device__ __forceinline__ uint32_t absmax(uint32_t m, uint32_t w) {
-    const __half2 r = __hmax2_nan(*reinterpret_cast<__half2*>(&m), __habs2(*reinterpret_cast<__half2*>(&w)));
-    return *reinterpret_cast<const uint32_t*>(&r);
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(m), "r"(w));
+    return r;
   }
   static __device__ __forceinline__ float lo(uint32_t w) { return __low2float(*reinterpret_cast<__half2*>(&w)); }
   static __device__ __forceinline__ float hi(uint32_t w) { return __high2float(*reinterpret_cast<__half2*>(&w)); }
 };
-
-__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
-}
 
 // |x| maxima as integers of the fp32 bits: NaN > Inf > every finite value.
 __device__ __forceinline__ uint32_t absbits(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
@@ -142,26 +149,41 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t b
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 
-// Tile rows of SIZE-byte elements into shared memory, zero outside the matrix.
+// Tile rows of SIZE-byte elements into shared memory, zero outside the matrix
+// (rows and cols: those that are left of it in this tile, at most kTile).
 template <int SIZE, bool NOISE>
-__device__ __forceinline__ void load_tile(uint8_t* tile, const uint8_t* src, int64_t ld, int64_t row0, int64_t col0,
-                                          int64_t rows, int64_t cols, int vec) {
+__device__ __forceinline__ void load_tile(uint8_t* tile, const uint8_t* src, int64_t pitch, int rows, int cols, int vec) {
   constexpr int kChunks = kTile * SIZE / 16;  // per row
   constexpr int kPer = 16 / SIZE;
-  for (int i = threadIdx.x; i < kTile * kChunks; i += kQThreads) {
-    const uint32_t r = i / kChunks, c = i % kChunks;
-    const int64_t row = row0 + r, col = col0 + c * kPer;
-    uint8_t* dst = tile + r * (kTile * SIZE) + (NOISE ? swz_noise(c, r) : swz<SIZE>(c, r)) * 16;
-    const int64_t left = row < rows ? min((int64_t)kPer, cols - col) : 0;
-    const uint8_t* p = src + (row * ld + col) * SIZE;
-    if (vec) {
-      copy16(ptx::smem_addr(dst), left > 0 ? p : src, left > 0 ? (uint32_t)left * SIZE : 0u);
-    } else {
+  auto place = [&](uint32_t r, uint32_t c) { return tile + r * (kTile * SIZE) + (NOISE ? swz_noise(c, r) : swz<SIZE>(c, r)) * 16; };
+  if (vec) {
+    for (int i = threadIdx.x; i < kTile * kChunks; i += kQThreads) {
+      const int r = i / kChunks, c = i % kChunks;
+      const int left = r < rows ? max(0, min(kPer, cols - c * kPer)) : 0;
+      copy16(ptx::smem_addr(place(r, c)), left ? src + r * pitch + c * 16 : src, left * SIZE);
+    }
+  } else {
+#pragma unroll 4
+    for (int i = threadIdx.x; i < kTile * kChunks; i += kQThreads) {
+      const int r = i / kChunks, c = i % kChunks;
+      const int left = r < rows ? min(kPer, cols - c * kPer) : 0;
+      const uint8_t* p = src + r * pitch + c * 16;
+      uint8_t* dst = place(r, c);
+      if constexpr (SIZE == 4) {  // four asynchronous words
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        if (SIZE == 4) reinterpret_cast<uint32_t*>(dst)[k] = k < left ? reinterpret_cast<const uint32_t*>(p)[k] : 0u;
-        else if (SIZE == 2) reinterpret_cast<uint16_t*>(dst)[k] = k < left ? reinterpret_cast<const uint16_t*>(p)[k] : (uint16_t)0;
-        else dst[k] = k < left ? p[k] : (uint8_t)0;
+        for (int k = 0; k < 4; ++k)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(dst) + 4 * k), "l"(k < left ? p + 4 * k : src),
+                       "r"(k < left ? 4u : 0u)
+                       : "memory");
+      } else {
+        uint32_t w[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+          if (k >= left) continue;
+          if constexpr (SIZE == 2) w[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + k) << (16 * (k & 1));
+          else w[k / 4] |= (uint32_t)__ldg(p + k) << (8 * (k & 3));
+        }
+        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
@@ -169,12 +191,17 @@ __device__ __forceinline__ void load_tile(uint8_t* tile, const uint8_t* src, int
 
 template <typename T, bool NOISE>
 __device__ __forceinline__ void row_phase(const MxQuantArgs& a, const uint8_t* tile, const uint8_t* noise,
-                                          uint8_t* scales, int64_t row0, int64_t col0) {
+                                          uint8_t* scales, int64_t row0, int64_t col0, int rows, int cols) {
   constexpr int S = In<T>::kSize;
-  const int64_t pitch = mx_pitch(a.cols), nb = mx_blocks(a.cols);
+  const int64_t pitch = mx_pitch(a.cols);
+  uint8_t* out_tile = a.row_data + row0 * pitch + col0 / kMxBlock * 16;
 #pragma unroll 1
   for (int q = threadIdx.x; q < kTile * 4; q += kQThreads) {
     const uint32_t r = q >> 2, b = q & 3;
+    if ((int)r >= rows || (int)b * kMxBlock >= cols) {  // padding
+      scales[(r & 31) * 16 + (r >> 5) * 4 + b] = 0;
+      continue;
+    }
     const uint8_t* line = tile + r * (kTile * S);
     uint32_t w[8 * S];
 #pragma unroll
@@ -209,15 +236,16 @@ __device__ __forceinline__ void row_phase(const MxQuantArgs& a, const uint8_t* t
         const uint2 n = *reinterpret_cast<const uint2*>(noise + r * kTile + swz_noise(b * 2 + g / 2, r) * 16 + (g & 1) * 8);
         uint32_t a8[8], s0, s1;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a8[i] = stochastic(f[i], inv, i < 4 ? ~n.x : ~n.y, i & 3);
+        for (int i = 0; i < 8; ++i) a8[i] = stochastic(f[i], inv, i < 4 ? n.x : n.y, i & 3);
         if constexpr (S == 4) {
           s0 = top_bytes(w[8 * g], w[8 * g + 2], w[8 * g + 4], w[8 * g + 6]);
           s1 = top_bytes(w[8 * g + 1], w[8 * g + 3], w[8 * g + 5], w[8 * g + 7]);
         } else {
-          s0 = __byte_perm(__byte_perm(w[4 * g], w[4 * g + 1], 0x0051), __byte_perm(w[4 * g + 2], w[4 * g + 3], 0x0051), 0x5410);
-          s1 = top_bytes(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+          const uint32_t p = sign_bytes(w[4 * g], w[4 * g + 1]), q = sign_bytes(w[4 * g + 2], w[4 * g + 3]);
+          s0 = __byte_perm(p, q, 0x5410);
+          s1 = __byte_perm(p, q, 0x7632);
         }
-        out[g] = gather_codes(a8, s0, s1);
+        out[g] = gather_codes(a8, s0, s1, a.ceil_scale);
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) f[i] *= inv;
@@ -225,17 +253,15 @@ __device__ __forceinline__ void row_phase(const MxQuantArgs& a, const uint8_t* t
       }
       if (byte == 255) out[g] = 0;
     }
-    const int64_t row = row0 + r, blk = col0 / kMxBlock + b;
-    if (row < a.rows && blk < nb)
-      *reinterpret_cast<uint4*>(a.row_data + row * pitch + blk * 16) = make_uint4(out[0], out[1], out[2], out[3]);
+    *reinterpret_cast<uint4*>(out_tile + r * pitch + b * 16) = make_uint4(out[0], out[1], out[2], out[3]);
   }
 }
 
 template <typename T, bool NOISE>
 __device__ __forceinline__ void col_phase(const MxQuantArgs& a, const uint8_t* tile, const uint8_t* noise,
-                                          uint8_t* scales, int64_t row0, int64_t col0) {
+                                          uint8_t* scales, int64_t row0, int64_t col0, int rows, int cols) {
   constexpr int S = In<T>::kSize;
-  const int64_t pitch = mx_pitch(a.rows), nb = mx_blocks(a.rows);
+  const int64_t pitch = mx_pitch(a.rows);
   const uint32_t pair = threadIdx.x >> 2, rb = threadIdx.x & 3;  // columns 2 pair, 2 pair + 1; rows 32 rb ..
   const uint32_t chunk = pair * 2 * S / 16, at = pair * 2 * S % 16;
   auto line = [&](uint32_t j) { const uint32_t r = rb * 32 + j; return tile + r * (kTile * S) + swz<S>(chunk, r) * 16 + at; };
@@ -288,15 +314,28 @@ __device__ __forceinline__ void col_phase(const MxQuantArgs& a, const uint8_t* t
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const uint32_t r = rb * 32 + 8 * g + i;
-        const uint32_t n = ~(uint32_t)*reinterpret_cast<const uint16_t*>(noise + r * kTile + swz_noise(pair / 8, r) * 16 + (pair % 8) * 2);
+        const uint32_t n = *reinterpret_cast<const uint16_t*>(noise + r * kTile + swz_noise(pair / 8, r) * 16 + (pair % 8) * 2);
         a8[0][i] = stochastic(f[0][i], inv[0], n, 0);
         a8[1][i] = stochastic(f[1][i], inv[1], n, 1);
       }
+      uint32_t s0[2], s1[2];  // signs of the even and odd rows, by column
+      if constexpr (S == 4) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const auto top = [&](int i) { return __float_as_uint(f[h][i]); };
-        out[h][g] = gather_codes(a8[h], top_bytes(top(0), top(2), top(4), top(6)), top_bytes(top(1), top(3), top(5), top(7)));
+        for (int h = 0; h < 2; ++h) {
+          const auto bits = [&](int i) { return __float_as_uint(f[h][i]); };
+          s0[h] = top_bytes(bits(0), bits(2), bits(4), bits(6));
+          s1[h] = top_bytes(bits(1), bits(3), bits(5), bits(7));
+        }
+      } else {
+        const uint32_t* p = w + 8 * g;
+        const uint32_t e0 = sign_bytes(p[0], p[2]), e1 = sign_bytes(p[4], p[6]), o0 = sign_bytes(p[1], p[3]), o1 = sign_bytes(p[5], p[7]);
+        s0[0] = __byte_perm(e0, e1, 0x5410);
+        s0[1] = __byte_perm(e0, e1, 0x7632);
+        s1[0] = __byte_perm(o0, o1, 0x5410);
+        s1[1] = __byte_perm(o0, o1, 0x7632);
       }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) out[h][g] = gather_codes(a8[h], s0[h], s1[h], a.ceil_scale);
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -309,13 +348,11 @@ __device__ __forceinline__ void col_phase(const MxQuantArgs& a, const uint8_t* t
     for (int h = 0; h < 2; ++h)
       if (byte[h] == 255) out[h][g] = 0;
   }
-  const int64_t blk = row0 / kMxBlock + rb;
+  uint8_t* dst = a.col_data + (col0 + 2 * pair) * pitch + (row0 / kMxBlock + rb) * 16;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const int64_t col = col0 + 2 * pair + h;
-    if (col < a.cols && blk < nb)
-      *reinterpret_cast<uint4*>(a.col_data + col * pitch + blk * 16) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
-  }
+  for (int h = 0; h < 2; ++h)
+    if ((int)pair * 2 + h < cols && (int)rb * 32 < rows)
+      *reinterpret_cast<uint4*>(dst + h * pitch) = make_uint4(out[h][0], out[h][1], out[h][2], out[h][3]);
 }
 
 template <typename T, bool NOISE>
@@ -328,12 +365,13 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) mx_quant_ke
   const int64_t ct = (a.cols + kTile - 1) / kTile;
   const int64_t tr = blockIdx.x / ct, tc = blockIdx.x % ct;
   const int64_t row0 = tr * kTile, col0 = tc * kTile;
-  load_tile<S, false>(tile, (const uint8_t*)a.src, a.ld, row0, col0, a.rows, a.cols, a.vec);
-  if constexpr (NOISE) load_tile<1, true>(noise, a.noise, a.noise_ld, row0, col0, a.rows, a.cols, a.noise_vec);
+  const int rows = (int)min((int64_t)kTile, a.rows - row0), cols = (int)min((int64_t)kTile, a.cols - col0);
+  load_tile<S, false>(tile, (const uint8_t*)a.src + (row0 * a.ld + col0) * S, a.ld * S, rows, cols, a.vec);
+  if constexpr (NOISE) load_tile<1, true>(noise, a.noise + row0 * a.noise_ld + col0, a.noise_ld, rows, cols, a.noise_vec);
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
-  if (a.row_data) row_phase<T, NOISE>(a, tile, noise, scales, row0, col0);
-  if (a.col_data) col_phase<T, NOISE>(a, tile, noise, scales + kMxScaleTile, row0, col0);
+  if (a.row_data) row_phase<T, NOISE>(a, tile, noise, scales, row0, col0, rows, cols);
+  if (a.col_data) col_phase<T, NOISE>(a, tile, noise, scales + kMxScaleTile, row0, col0, rows, cols);
   __syncthreads();
   const int t = threadIdx.x;
   if (t < 32 && a.row_data)

@@ -217,7 +217,7 @@ def test_gemm_alpha_beta_pitch(handle, m, n, k, dtype, alpha, beta, pad):
     _check_gemm(handle, m, n, k, dtype, alpha, beta, pad, seed=11)
 
 
-@pytest.mark.parametrize("m,n,k", [(2500, 2560, 1024), (4100, 1030, 2080), (777, 5000, 544)])
+@pytest.mark.parametrize("m,n,k", [(2500, 2560, 1024), (4100, 1030, 2080), (777, 5000, 544), (150, 12000, 320), (12001, 131, 96)])
 def test_gemm_many_tiles(handle, m, n, k):
     _check_gemm(handle, m, n, k, "f32", 1.0, 1.0, 2, seed=21)
     _check_gemm(handle, m, n, k, "bf16", seed=22)
