@@ -257,6 +257,7 @@ int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p, void
   a.ldh = p->ldh;
   a.per_gate = p->rows_per_gate;
   a.eps = p->eps;
+  a.err = h->d_op_err;
   a.vec = cols % 8 == 0 && rows_aligned(p->x, p->ldx, p->dtype) && rows_aligned(p->f, p->ldf, p->dtype) &&
           rows_aligned(p->y, p->ldy, p->dtype) && rows_aligned(p->h, p->ldh, p->dtype) && aligned(p->post_w, 16) &&
           aligned(p->pre_w, 16) && aligned(p->gate, 16) && aligned(p->res_scale, 16);
@@ -330,6 +331,8 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   a.per_gate = p->gate ? std::min(p->rows_per_gate, std::max<int64_t>(rows, 1)) : std::max<int64_t>(rows, 1);
   a.groups = (rows + a.per_gate - 1) / a.per_gate;
   a.units = norm_bwd_units(rows, cols, h->num_sms);
+  a.cta_units = norm_bwd_cta_units(cols);
+  a.err = h->d_op_err;
   // Chunks lie inside a group; no more of them than units where that can be,
   // so that no unit has two while another has one.
   a.chunks_per_group = std::max<int64_t>(1, std::min(a.per_gate, a.units / std::max<int64_t>(1, a.groups)));

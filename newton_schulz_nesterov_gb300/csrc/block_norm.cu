@@ -11,6 +11,7 @@
 
 #include "../../include/dmuon.h"
 #include "block_norm.cuh"
+#include "bounded_wait.cuh"
 #include "ptx.cuh"
 
 namespace dmuon {
@@ -58,7 +59,7 @@ constexpr int kFwdThreads = 512, kBwdThreads = 256;  // of an SM: 128 and 255 re
 constexpr int kMaxCluster = 8;
 
 struct RowUnit {
-  int tpr;        // threads of a unit
+  int tpr;        // threads of a unit: a power of two below 32, or whole warps
   int unit, t;    // this thread's unit in the CTA and place in it
   int warps;      // of a unit
   int col0, cols; // columns of this CTA: [col0, col0 + cols)
@@ -69,56 +70,101 @@ __device__ __forceinline__ RowUnit row_unit(int64_t cols, int tpr) {
   u.tpr = tpr;
   u.unit = threadIdx.x / tpr;
   u.t = threadIdx.x % tpr;
-  u.warps = tpr / 32;
+  u.warps = max(1, tpr / 32);
   u.col0 = (int)ptx::cluster_ctarank() * tpr * V * 8;
   u.cols = max(0, min(tpr * V * 8, (int)cols - u.col0));
   return u;
 }
 
-// Column of value e of chunk v, in the CTA.
-template <bool VEC>
+// Column of value e of chunk v, in the CTA: runs of E columns a thread (the 16
+// bytes of an access, or 1), runs of the unit's threads side by side.
+template <int E>
 __device__ __forceinline__ int col_of(const RowUnit& u, int v, int e) {
-  return VEC ? (v * u.tpr + u.t) * 8 + e : (v * 8 + e) * u.tpr + u.t;
+  return ((v * (8 / E) + e / E) * u.tpr + u.t) * E + e % E;
 }
+template <typename T, bool VEC>
+constexpr int run_of() { return VEC ? 16 / (int)sizeof(T) : 1; }
 
 // Sums of N values over a row's threads, in a fixed order, to all of them.
-// One barrier: consecutive calls alternate between two halves of `red`
-// ([2][units][3][kRedRow] floats, zero at first), and a half is written again
-// only after the next call's barrier, when every thread has read it.
+// Consecutive calls alternate between two halves of `red` ([2][units][3]
+// [kRedRow] floats, zero at first) and, in clusters, two barriers.  A half is
+// written again only after the next call's barrier, when every thread has read
+// it.  In a cluster every warp sends its sums to every CTA (st.async, counted
+// on that CTA's barrier): a cluster barrier a row would wait for the row's
+// global stores too (8192 columns: 135 us against 69).
 constexpr int kRedRow = kMaxCluster * 16;  // warps of a row at most
-__device__ __forceinline__ void row_sum_init(float* red, int units) {
-  for (int i = threadIdx.x; i < 2 * units * 3 * kRedRow; i += blockDim.x) red[i] = 0.f;
+// Kinds of units: narrower than a warp, of one CTA, of a cluster of CTAs.
+enum Kind { kSub, kCta, kCluster };
+struct RowSums {
+  float* red;
+  uint32_t bars;          // two mbarriers, in clusters
+  int clusters, units;
+  uint32_t calls;
+  int* err;
+  __device__ __forceinline__ void init(float* r, uint64_t* b, int cl, int un, int* e) {
+    red = r;
+    bars = ptx::smem_addr(b);
+    clusters = cl;
+    units = un;
+    calls = 0;
+    err = e;
+    if (cl > 1 || blockDim.x / un > 32)
+      for (int i = threadIdx.x; i < 2 * un * 3 * kRedRow; i += blockDim.x) r[i] = 0.f;
+    if (cl > 1 && threadIdx.x == 0) {
+      ptx::mbar_init(bars, 1);
+      ptx::mbar_init(bars + 8, 1);
+      ptx::fence_mbar_init();
+    }
+  }
+};
+
+// A wait of row_sum in a cluster that does not end in kWaitNs sets *err; the
+// kernel goes on with what is there, so that it ends.
+__device__ __forceinline__ void wait_sums(uint32_t bar, uint32_t parity, int* err) {
+  if (ptx::mbar_try(bar, parity)) return;
+  const uint64_t t0 = ptx::globaltimer();
+  while (!ptx::mbar_try(bar, parity)) {
+    if (ptx::globaltimer() - t0 > kWaitNs || *(volatile int*)err) {
+      atomicOr(err, 1);
+      return;
+    }
+  }
 }
-template <int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, float* red, int& half, int clusters) {
+
+template <int N, int KIND>
+__device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, RowSums& s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
+    if (KIND != kSub || o < u.tpr)
 #pragma unroll
-    for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (clusters == 1 && u.warps == 1) return;
-  const int lane = threadIdx.x & 31, warp = u.t >> 5;
-  float* mine = red + (half * (int)(blockDim.x / u.tpr) + u.unit) * 3 * kRedRow;
-  half ^= 1;
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if (KIND == kSub || (KIND == kCta && u.warps == 1)) return;
+  const int lane = threadIdx.x & 31, warp = u.t >> 5, half = s.calls & 1;
+  float* mine = s.red + (half * s.units + u.unit) * 3 * kRedRow;
   int n = u.warps;
-  if (clusters == 1) {
+  if constexpr (KIND == kCta) {
     if (lane == 0)
 #pragma unroll
       for (int k = 0; k < N; ++k) mine[k * kRedRow + warp] = v[k];
     asm volatile("bar.sync %0, %1;" ::"r"(u.unit + 1), "r"(u.tpr) : "memory");
   } else {
-    n = u.warps * clusters;
-    if (lane < clusters) {  // lane r tells rank r
-      const uint32_t rank = ptx::cluster_ctarank();
+    n = u.warps * s.clusters;
+    const uint32_t bar = s.bars + 8 * half;
+    if (threadIdx.x == 0) ptx::mbar_expect_tx(bar, n * N * 4);
+    if (lane < s.clusters) {  // lane r tells rank r
+      const uint32_t rank = ptx::cluster_ctarank(), there = ptx::mapa_shared(bar, lane);
 #pragma unroll
       for (int k = 0; k < N; ++k)
-        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+        asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(
                          ptx::mapa_shared(ptx::smem_addr(mine + k * kRedRow + rank * u.warps + warp), lane)),
-                     "f"(v[k])
+                     "r"(__float_as_uint(v[k])), "r"(there)
                      : "memory");
     }
-    ptx::cluster_sync();
+    wait_sums(bar, (s.calls >> 1) & 1, s.err);
+    __syncwarp();
   }
-  if (n <= 8) {  // what no warp writes is zero
+  ++s.calls;
+  if (KIND == kCta && n <= 8) {  // what no warp writes is zero
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       const float4 p = *reinterpret_cast<const float4*>(mine + k * kRedRow), q = *reinterpret_cast<const float4*>(mine + k * kRedRow + 4);
@@ -186,13 +232,13 @@ struct Chunk8 {
 constexpr int parts_of(int size) { return size / 2; }  // 16-byte parts of a chunk
 
 // `row` is the first of this CTA's columns, here and below.
-template <typename T, bool VEC>
+template <typename T>
 __device__ __forceinline__ Chunk8<T> load_direct(const T* row, const RowUnit& u, int v) {
   Chunk8<T> r;
   r.zero();
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const int c = col_of<VEC>(u, v, e);
+    const int c = col_of<1>(u, v, e);
     if (c >= u.cols) continue;
     if constexpr (sizeof(T) == 4) r.w[e] = reinterpret_cast<const uint32_t*>(row)[c];
     else r.w[e >> 1] |= (uint32_t)reinterpret_cast<const uint16_t*>(row)[c] << (16 * (e & 1));
@@ -200,7 +246,7 @@ __device__ __forceinline__ Chunk8<T> load_direct(const T* row, const RowUnit& u,
   return r;
 }
 
-template <typename T, bool VEC>
+template <typename T, int E>
 __device__ __forceinline__ void store_chunk(T* row, const RowUnit& u, int v, const f2 (&val)[4]) {
   float o[8];
 #pragma unroll
@@ -209,91 +255,88 @@ __device__ __forceinline__ void store_chunk(T* row, const RowUnit& u, int v, con
     o[2 * i] = p.x;
     o[2 * i + 1] = p.y;
   }
-  if constexpr (VEC) {
-    const int c = col_of<VEC>(u, v, 0);
-    if (c >= u.cols) return;
-    uint4* dst = reinterpret_cast<uint4*>(row + c);
-    if constexpr (sizeof(T) == 4) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        dst[i] = make_uint4(__float_as_uint(o[4 * i]), __float_as_uint(o[4 * i + 1]), __float_as_uint(o[4 * i + 2]),
-                            __float_as_uint(o[4 * i + 3]));
-    } else {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (std::is_same<T, __half>::value) {
-          const __half2 h = __floats2half2_rn(o[2 * i], o[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        } else {
-          const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-          w[i] = *reinterpret_cast<const uint32_t*>(&h);
-        }
-      }
-      *dst = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  } else {
+  if constexpr (E == 1) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = col_of<VEC>(u, v, e);
+      const int c = col_of<1>(u, v, e);
       if (c < u.cols) row[c] = narrow<T>(o[e]);
     }
+  } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const int c = col_of<E>(u, v, e);
+      if (c < u.cols)
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
+                                                        __float_as_uint(o[e + 3]));
+    }
+  } else {
+    const int c = col_of<E>(u, v, 0);
+    if (c >= u.cols) return;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(o[2 * i], o[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+    *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 // Eight fp32 values of a parameter (its first column is column 0 of the row);
 // 0 past the columns.
-template <bool VEC>
+template <int E>
 __device__ __forceinline__ void load_param(f2 (&val)[4], const float* p, const RowUnit& u, int v) {
   p += u.col0;
-  if constexpr (VEC) {
-    const int c = col_of<VEC>(u, v, 0);
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
-    if (c < u.cols) {
-      a = *reinterpret_cast<const float4*>(p + c);
-      b = *reinterpret_cast<const float4*>(p + c + 4);
+  if constexpr (E > 1) {
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const int c = col_of<E>(u, v, e);
+      const float4 a = c < u.cols ? *reinterpret_cast<const float4*>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+      val[e / 2] = pack2(a.x, a.y);
+      val[e / 2 + 1] = pack2(a.z, a.w);
     }
-    val[0] = pack2(a.x, a.y);
-    val[1] = pack2(a.z, a.w);
-    val[2] = pack2(b.x, b.y);
-    val[3] = pack2(b.z, b.w);
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int c0 = col_of<VEC>(u, v, 2 * i), c1 = col_of<VEC>(u, v, 2 * i + 1);
+      const int c0 = col_of<1>(u, v, 2 * i), c1 = col_of<1>(u, v, 2 * i + 1);
       val[i] = pack2(c0 < u.cols ? p[c0] : 0.f, c1 < u.cols ? p[c1] : 0.f);
     }
   }
 }
 
-template <bool VEC>
+template <int E>
 __device__ __forceinline__ void store_param(float* p, const RowUnit& u, int v, const f2 (&val)[4]) {
-  store_chunk<float, VEC>(p + u.col0, u, v, val);
+  store_chunk<float, E>(p + u.col0, u, v, val);
 }
 
 // The private ring: slot s, array k, part i of chunk v of this thread.
 template <typename T, int ARRAYS>
 struct Ring {
+  static constexpr int E = 16 / (int)sizeof(T);
   uint32_t base, step;  // this thread's part 0; bytes from one part to the next
   __device__ __forceinline__ uint32_t slot(int s) const { return base + s * ARRAYS * V * parts_of(sizeof(T)) * step; }
   __device__ __forceinline__ void fetch(uint32_t slot, int k, const T* row, const RowUnit& u) const {
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const int c = col_of<true>(u, v, 0);
-      if (c >= u.cols) break;
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int i = 0; i < parts_of(sizeof(T)); ++i)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + ((k * V + v) * parts_of(sizeof(T)) + i) * step),
-                     "l"(reinterpret_cast<const uint8_t*>(row + c) + 16 * i)
-                     : "memory");
-    }
+      for (int i = 0; i < parts_of(sizeof(T)); ++i) {
+        const int c = col_of<E>(u, v, i * E);
+        if (c < u.cols)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + ((k * V + v) * parts_of(sizeof(T)) + i) * step), "l"(row + c)
+                       : "memory");
+      }
   }
   __device__ __forceinline__ Chunk8<T> take(uint32_t slot, int k, int v, const RowUnit& u) const {
     Chunk8<T> r;
     r.zero();
-    if (col_of<true>(u, v, 0) < u.cols)
 #pragma unroll
-      for (int i = 0; i < parts_of(sizeof(T)); ++i)
+    for (int i = 0; i < parts_of(sizeof(T)); ++i)
+      if (col_of<E>(u, v, i * E) < u.cols)
         asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
                      : "=r"(r.w[4 * i]), "=r"(r.w[4 * i + 1]), "=r"(r.w[4 * i + 2]), "=r"(r.w[4 * i + 3])
                      : "r"(slot + ((k * V + v) * parts_of(sizeof(T)) + i) * step)
@@ -302,24 +345,37 @@ struct Ring {
   }
 };
 
+// Rows that are loaded directly: the whole 16-byte pieces of a coming one to L2.
+template <typename T>
+__device__ __forceinline__ void prefetch_row(const T* row, int cols) {
+  const uintptr_t from = ((uintptr_t)row + 15) & ~(uintptr_t)15, to = (uintptr_t)(row + cols) & ~(uintptr_t)15;
+  if (from < to)
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
+}
+
 __device__ __forceinline__ void commit_group() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <typename T>
 constexpr int ring_depth() { return sizeof(T) == 4 ? 2 : 4; }
-constexpr int red_bytes(int units) { return 2 * units * 3 * kRedRow * 4; }
+// Row sums (only of units of several warps), then two barriers; the ring after
+// them starts on 128 bytes (16 further on, every access of it took two lines:
+// norm_bwd 147 -> 158 us).
+__host__ __device__ constexpr int red_bytes(int units, int tpr) { return (tpr > 32 ? 2 * units * 3 * kRedRow * 4 : 0) + 128; }
 
-// Unit u of all takes rows [u n, (u + 1) n).
-template <typename T, bool VEC>
+// Unit u of all takes rows [u n, (u + 1) n).  Units narrower than a warp stay
+// together while any of them has rows.
+template <typename T, bool VEC, int KIND>
 __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const NormFwdArgs a, int tpr, int clusters) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kRing = ring_depth<T>();
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kRing = ring_depth<T>(), E = run_of<T, VEC>();
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
-  float* red = reinterpret_cast<float*>(smem);
-  row_sum_init(red, units);
-  const Ring<T, 2> ring{ptx::smem_addr(smem + red_bytes(units)) + threadIdx.x * 16, blockDim.x * 16};
+  uint8_t* after = smem + red_bytes(units, tpr);
+  RowSums sums;
+  sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err);
+  const Ring<T, 2> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   const int64_t per = (a.rows + all - 1) / all;
   const int row0 = (int)min(id * per, a.rows), row1 = (int)min(row0 + per, a.rows);
@@ -341,30 +397,32 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
   };
   if constexpr (VEC)
     for (int s = 0; s < kRing; ++s) fetch(s);
-  if (clusters > 1) ptx::cluster_sync();
+  if constexpr (KIND == kCluster) ptx::cluster_sync();
   else __syncthreads();
   const float inv = 1.f / (float)a.cols;
   f2 pre[V][4], gw[V][4], res[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    load_param<VEC>(pre[v], a.pre_w, u, v);
-    load_param<VEC>(gw[v], a.post_w, u, v);
-    if (a.res) load_param<VEC>(res[v], a.res, u, v);
+    load_param<E>(pre[v], a.pre_w, u, v);
+    load_param<E>(gw[v], a.post_w, u, v);
+    if (a.res) load_param<E>(res[v], a.res, u, v);
     else
 #pragma unroll
       for (int i = 0; i < 4; ++i) res[v][i] = both(1.f);
   }
   int group_end = a.gate ? row0 : INT_MAX;  // first row past the gate row in gw
-  int slot = 0, half = 0;
-  for (int row = row0; row < row1; ++row) {
-    if (row == group_end) {
+  int slot = 0;
+  const int last = KIND == kSub ? row0 + (int)per : row1;  // as often for every unit of a warp
+  for (int row = row0; row < last; ++row) {
+    const bool live = KIND != kSub || row < row1;
+    if (live && row == group_end) {
       const int64_t group = row / a.per_gate;
       group_end = (int)min((group + 1) * a.per_gate, a.rows);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         f2 g[4];
-        load_param<VEC>(g, a.gate + group * a.cols, u, v);
-        load_param<VEC>(gw[v], a.post_w, u, v);
+        load_param<E>(g, a.gate + group * a.cols, u, v);
+        load_param<E>(gw[v], a.post_w, u, v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) gw[v][i] = mul2(gw[v][i], g[i]);
       }
@@ -374,17 +432,22 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
       wait_group<kRing - 1>();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        xr[v] = ring.take(ring.slot(slot), 0, v, u);
+        xr[v] = ring.take(ring.slot(slot), 0, v, u);  // a unit past its rows sums what its slots hold and stores nothing
         fr[v] = ring.take(ring.slot(slot), 1, v, u);
       }
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        xr[v] = load_direct<T, VEC>(x, u, v);
-        fr[v] = load_direct<T, VEC>(f, u, v);
+        xr[v].zero();
+        fr[v].zero();
+        if (live) {
+          xr[v] = load_direct<T>(x, u, v);
+          fr[v] = load_direct<T>(f, u, v);
+        }
       }
       x += a.ldx;
       f += a.ldf;
+      if (row + 2 < row1 && u.t < 2) prefetch_row(u.t ? f + a.ldf : x + a.ldx, u.cols);
     }
     f2 q = 0;
 #pragma unroll
@@ -392,7 +455,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
 #pragma unroll
       for (int i = 0; i < 4; ++i) q = fma2(fr[v].pair(i), fr[v].pair(i), q);
     float s[1] = {add_up(q)};
-    row_sum<1>(s, u, red, half, clusters);
+    row_sum<1, KIND>(s, u, sums);
     const float r1 = rsqrtf(fmaf(s[0], inv, a.eps));
     const f2 rr1 = both(r1);
     f2 y[V][4];
@@ -404,30 +467,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
         y[v][i] = fma2(mul2(fr[v].pair(i), rr1), gw[v][i], mul2(xr[v].pair(i), res[v][i]));
         q = fma2(y[v][i], y[v][i], q);
       }
-      store_chunk<T, VEC>(y_out, u, v, y[v]);
+      if (live) store_chunk<T, E>(y_out, u, v, y[v]);
     }
     if constexpr (VEC) {
       fetch(slot);  // this thread has taken its slot
       if (++slot == kRing) slot = 0;
     }
     s[0] = add_up(q);
-    row_sum<1>(s, u, red, half, clusters);
+    row_sum<1, KIND>(s, u, sums);
     const float r2 = rsqrtf(fmaf(s[0], inv, a.eps));
     const f2 rr2 = both(r2);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[v][i] = mul2(mul2(y[v][i], rr2), pre[v][i]);
-      store_chunk<T, VEC>(h_out, u, v, y[v]);
+      if (live) store_chunk<T, E>(h_out, u, v, y[v]);
     }
     y_out += a.ldy;
     h_out += a.ldh;
-    if (u.t == 0 && u.col0 == 0) {
+    if (live && u.t == 0 && u.col0 == 0) {
       a.rstd[row] = r1;
       a.rstd[a.rows + row] = r2;
     }
   }
-  if (clusters > 1) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
+  if constexpr (KIND == kCluster) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
 }
 
 // The rows of a unit, chunk after chunk (rows and chunks fit 31 bits).
@@ -463,15 +526,20 @@ struct ChunkRows {
 // terms).  Units' column sums stay in registers over their rows, go to their
 // own rows of the partial arrays and are added up, in a fixed order, by
 // norm_bwd_sums_kernel.
-template <typename T, bool VEC, bool DY, bool X>
+// WHICH: 1 dy is given, 2 d_res is wanted; 4: asked at run time (the kinds of
+// units for which a variant of its own gains less).
+template <typename T, bool VEC, int KIND, int WHICH>
 __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const NormBwdArgs a, int tpr, int clusters) {
-  extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kRing = ring_depth<T>();
+  const bool DY = WHICH == 4 ? a.dy != nullptr : (WHICH & 1) != 0;
+  const bool X = WHICH == 4 ? a.d_res != nullptr : (WHICH & 2) != 0;
+  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kRing = ring_depth<T>(), E = run_of<T, VEC>();
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
-  float* red = reinterpret_cast<float*>(smem);
-  row_sum_init(red, units);
-  const Ring<T, 5> ring{ptx::smem_addr(smem + red_bytes(units)) + threadIdx.x * 16, blockDim.x * 16};
+  uint8_t* after = smem + red_bytes(units, tpr);
+  RowSums sums;
+  sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err);
+  const Ring<T, 5> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   ChunkRows at{(int)all, (int)id, 0, 0};
   at.open(a);
@@ -510,7 +578,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
   };
   if constexpr (VEC)
     for (int s = 0; s < kRing; ++s) fetch(s);
-  if (clusters > 1) ptx::cluster_sync();
+  if constexpr (KIND == kCluster) ptx::cluster_sync();
   else __syncthreads();
   f2 sum_pre[V][4], sum_res[V][4], sum_t[V][4];
 #pragma unroll
@@ -520,8 +588,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
   f2 pre[V][4], gw[V][4], res[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    load_param<VEC>(pre[v], a.pre_w, u, v);
-    if (a.res) load_param<VEC>(res[v], a.res, u, v);
+    load_param<E>(pre[v], a.pre_w, u, v);
+    if (a.res) load_param<E>(res[v], a.res, u, v);
     else
 #pragma unroll
       for (int i = 0; i < 4; ++i) res[v][i] = both(1.f);
@@ -532,7 +600,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
   T *dx_row = nullptr, *df_row = nullptr;
   int chunk = -1;
   const float* gate = nullptr;
-  int slot = 0, half = 0;
+  int slot = 0;
   // t fn summed over a chunk belongs to one gate row.  The sum over a unit's
   // chunks is kept in its row of part_post.
   auto flush = [&]() {
@@ -540,22 +608,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       f2 w[4], o[4];
-      if (a.gate) load_param<VEC>(w, gate, u, v);
-      if (post_written) load_param<VEC>(o, part_post, u, v);
+      if (a.gate) load_param<E>(w, gate, u, v);
+      if (post_written) load_param<E>(o, part_post, u, v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 g = a.gate ? w[i] : both(1.f);
         o[i] = post_written ? fma2(g, sum_t[v][i], o[i]) : mul2(g, sum_t[v][i]);
       }
-      store_param<VEC>(part_post, u, v, o);
+      store_param<E>(part_post, u, v, o);
       if (a.d_gate) {
         if (a.chunks_per_group > 1) {
-          store_param<VEC>(a.part_gate + (int64_t)chunk * a.cols, u, v, sum_t[v]);
+          store_param<E>(a.part_gate + (int64_t)chunk * a.cols, u, v, sum_t[v]);
         } else {
-          load_param<VEC>(w, a.post_w, u, v);
+          load_param<E>(w, a.post_w, u, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = mul2(w[i], sum_t[v][i]);
-          store_param<VEC>(a.d_gate + group * a.cols, u, v, w);
+          store_param<E>(a.d_gate + group * a.cols, u, v, w);
         }
       }
 #pragma unroll
@@ -568,10 +636,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     n1 = a.rstd[at.row];
     n2 = a.rstd[a.rows + at.row];
   }
-  while (!at.done()) {
+  while (KIND == kSub ? __any_sync(0xffffffffu, !at.done()) : !at.done()) {  // as long as any unit of the warp has rows
+    const bool live = KIND != kSub || !at.done();
     const int64_t row = at.row;
     const float r1 = n1, r2 = n2;
-    if (at.chunk != chunk) {
+    if (live && at.chunk != chunk) {
       if (chunk >= 0) flush();
       chunk = at.chunk;
       dx_row = (T*)a.dx + row * a.lddx + u.col0;
@@ -579,16 +648,16 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       if (a.gate) gate = a.gate + (int64_t)(chunk / (int)a.chunks_per_group) * a.cols;
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        load_param<VEC>(gw[v], a.post_w, u, v);
+        load_param<E>(gw[v], a.post_w, u, v);
         if (a.gate) {
           f2 g[4];
-          load_param<VEC>(g, gate, u, v);
+          load_param<E>(g, gate, u, v);
 #pragma unroll
           for (int i = 0; i < 4; ++i) gw[v][i] = mul2(gw[v][i], g[i]);
         }
       }
     }
-    at.next(a);
+    if (live) at.next(a);
     if (!at.done()) {  // the next row's, before it is needed
       n1 = a.rstd[at.row];
       n2 = a.rstd[a.rows + at.row];
@@ -603,19 +672,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     for (int v = 0; v < V; ++v) {
       Chunk8<T> dy, dh, y, f;
       dy.zero();
+      dh.zero();
+      y.zero();
+      f.zero();
       x[v].zero();
-      if constexpr (VEC) {
-        if (DY) dy = ring.take(from, 0, v, u);
-        dh = ring.take(from, 1, v, u);
-        y = ring.take(from, 2, v, u);
-        f = ring.take(from, 3, v, u);
-        if (X) x[v] = ring.take(from, 4, v, u);
-      } else {
-        if (DY) dy = load_direct<T, VEC>((const T*)a.dy + row * a.lddy + u.col0, u, v);
-        dh = load_direct<T, VEC>((const T*)a.dh + row * a.lddh + u.col0, u, v);
-        y = load_direct<T, VEC>((const T*)a.y + row * a.ldy + u.col0, u, v);
-        f = load_direct<T, VEC>((const T*)a.f + row * a.ldf + u.col0, u, v);
-        if (X) x[v] = load_direct<T, VEC>((const T*)a.x + row * a.ldx + u.col0, u, v);
+      if (live) {
+        if constexpr (VEC) {
+          if (DY) dy = ring.take(from, 0, v, u);
+          dh = ring.take(from, 1, v, u);
+          y = ring.take(from, 2, v, u);
+          f = ring.take(from, 3, v, u);
+          if (X) x[v] = ring.take(from, 4, v, u);
+        } else {
+          if (DY) dy = load_direct<T>((const T*)a.dy + row * a.lddy + u.col0, u, v);
+          dh = load_direct<T>((const T*)a.dh + row * a.lddh + u.col0, u, v);
+          y = load_direct<T>((const T*)a.y + row * a.ldy + u.col0, u, v);
+          f = load_direct<T>((const T*)a.f + row * a.ldf + u.col0, u, v);
+          if (X) x[v] = load_direct<T>((const T*)a.x + row * a.ldx + u.col0, u, v);
+        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -630,8 +704,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
         s2 = fma2(b, yn[v][i], s2);
       }
     }
+    if constexpr (!VEC) {
+      if (live && row + 2 < at.end) {  // the row after next, to L2
+        if (DY && u.t == 0) prefetch_row((const T*)a.dy + (row + 2) * a.lddy + u.col0, u.cols);
+        if (u.t == 1) prefetch_row((const T*)a.dh + (row + 2) * a.lddh + u.col0, u.cols);
+        if (u.t == 2) prefetch_row((const T*)a.y + (row + 2) * a.ldy + u.col0, u.cols);
+        if (u.t == 3) prefetch_row((const T*)a.f + (row + 2) * a.ldf + u.col0, u.cols);
+        if (X && u.t == 4) prefetch_row((const T*)a.x + (row + 2) * a.ldx + u.col0, u.cols);
+      }
+    }
     float s[3] = {add_up(s0), add_up(s1), add_up(s2)};
-    row_sum<3>(s, u, red, half, clusters);
+    row_sum<3, KIND>(s, u, sums);
     if constexpr (VEC) {
       fetch(slot);  // this thread has taken its slot
       if (++slot == kRing) slot = 0;
@@ -649,20 +732,45 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
         dx[i] = mul2(res[v][i], t);
         df[i] = mul2(rr1, fma2(fn[v][i], nm1, mul2(gw[v][i], t)));
       }
-      store_chunk<T, VEC>(dx_row, u, v, dx);
-      store_chunk<T, VEC>(df_row, u, v, df);
+      if (live) {
+        store_chunk<T, E>(dx_row, u, v, dx);
+        store_chunk<T, E>(df_row, u, v, df);
+      }
     }
     dx_row += a.lddx;
     df_row += a.lddf;
   }
   if (chunk >= 0) flush();
+  if (units == 1) {
 #pragma unroll
-  for (int v = 0; v < V; ++v) {
-    if (!post_written) store_param<VEC>(part_post, u, v, sum_t[v]);  // no rows: zeros
-    store_param<VEC>(a.part_pre + id * a.cols, u, v, sum_pre[v]);
-    if (X) store_param<VEC>(a.part_res + id * a.cols, u, v, sum_res[v]);
+    for (int v = 0; v < V; ++v) {
+      if (!post_written) store_param<E>(part_post, u, v, sum_t[v]);  // no rows: zeros
+      store_param<E>(a.part_pre + id * a.cols, u, v, sum_pre[v]);
+      if (X) store_param<E>(a.part_res + id * a.cols, u, v, sum_res[v]);
+    }
+  } else {  // one row of sums a CTA, in its first unit's place: added up where the ring was
+    float* fold = reinterpret_cast<float*>(after);  // [3][units][cols]
+    const int n = (int)a.cols;
+    if constexpr (VEC) wait_group<0>();
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      f2 post[4];
+      if (post_written) load_param<E>(post, part_post, u, v);
+      store_param<E>(fold + u.unit * n, u, v, sum_pre[v]);
+      store_param<E>(fold + (units + u.unit) * n, u, v, post_written ? post : sum_t[v]);
+      if (X) store_param<E>(fold + (2 * units + u.unit) * n, u, v, sum_res[v]);
+    }
+    __syncthreads();
+    const int64_t first = (id - u.unit) * n;
+    for (int c = threadIdx.x; c < (X ? 3 : 2) * n; c += blockDim.x) {
+      const int k = c / n, col = c - k * n;
+      float sum = 0.f;
+      for (int i = 0; i < units; ++i) sum += fold[(k * units + i) * n + col];
+      (k == 0 ? a.part_pre : k == 1 ? a.part_post : a.part_res)[first + col] = sum;
+    }
   }
-  if (clusters > 1) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
+  if constexpr (KIND == kCluster) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
 }
 
 // ------------------------------------------------------------ longer rows
@@ -805,7 +913,8 @@ __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a)
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   const float* src;
   float* dst;
-  int n = (int)a.units;
+  int n = (int)(a.units / a.cta_units);
+  int64_t step = a.cta_units * a.cols;  // a CTA's sums are in its first unit's row
   if (blockIdx.y == 0) { src = a.part_pre; dst = a.d_pre_w; }
   else if (blockIdx.y == 1) { src = a.part_post; dst = a.d_post_w; }
   else if (blockIdx.y == 2) { src = a.part_res; dst = a.d_res; }
@@ -813,6 +922,7 @@ __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a)
     const int64_t g = blockIdx.y - 3;
     // The last group may be short: its chunks past the rows are not written.
     n = (int)((min(a.per_gate, a.rows - g * a.per_gate) + a.chunk_rows - 1) / a.chunk_rows);
+    step = a.cols;
     src = a.part_gate + g * a.chunks_per_group * a.cols;
     dst = a.d_gate + g * a.cols;
   }
@@ -823,7 +933,7 @@ __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a)
     for (int i = warp; i < n; i += 64) {
       float v[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = i + 8 * k < n ? src[(int64_t)(i + 8 * k) * a.cols] : 0.f;
+      for (int k = 0; k < 8; ++k) v[k] = i + 8 * k < n ? src[(i + 8 * k) * step] : 0.f;
 #pragma unroll
       for (int k = 0; k < 8; ++k) s += v[k];
     }
@@ -847,7 +957,10 @@ RowShape row_shape(int64_t cols, int threads, int cta_threads) {
   RowShape r;
   const int64_t cta = (int64_t)threads * V * 8;
   r.clusters = cols <= cta ? 1 : cols <= 2 * cta ? 2 : cols <= 4 * cta ? 4 : kMaxCluster;
-  r.tpr = r.clusters > 1 ? threads : (int)((cols + 256 * V - 1) / (256 * V)) * 32;
+  const int lanes = r.clusters > 1 ? threads : (int)((cols + 8 * V - 1) / (8 * V));
+  r.tpr = 8;  // rows of up to 128 columns
+  while (r.tpr < lanes && r.tpr < 32) r.tpr *= 2;
+  if (lanes > 32) r.tpr = (lanes + 31) / 32 * 32;
   r.units = r.clusters > 1 ? 1 : std::max(1, cta_threads / r.tpr);
   r.resident = std::max(1, threads / (r.tpr * r.units));
   return r;
@@ -878,7 +991,7 @@ cudaError_t launch_rows(K kernel, const A& a, const RowShape& r, int64_t ctas, i
 
 template <typename T>
 int ring_bytes(const RowShape& r, int arrays) {
-  return red_bytes(r.units) + ring_depth<T>() * arrays * V * parts_of(sizeof(T)) * r.tpr * r.units * 16;
+  return red_bytes(r.units, r.tpr) + ring_depth<T>() * arrays * V * parts_of(sizeof(T)) * r.tpr * r.units * 16;
 }
 
 template <typename T>
@@ -890,8 +1003,11 @@ cudaError_t fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
   }
   const RowShape r = fwd_shape(a.cols);
   const int64_t ctas = std::min((a.rows + r.units - 1) / r.units, (int64_t)std::max(1, sms * r.resident / r.clusters));
-  if (a.vec) return launch_rows(norm_fwd_rows_kernel<T, true>, a, r, ctas, ring_bytes<T>(r, 2), s);
-  return launch_rows(norm_fwd_rows_kernel<T, false>, a, r, ctas, red_bytes(r.units), s);
+  const int smem = a.vec ? ring_bytes<T>(r, 2) : red_bytes(r.units, r.tpr);
+  auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
+  if (r.tpr < 32) return a.vec ? go(norm_fwd_rows_kernel<T, true, kSub>) : go(norm_fwd_rows_kernel<T, false, kSub>);
+  if (r.clusters > 1) return a.vec ? go(norm_fwd_rows_kernel<T, true, kCluster>) : go(norm_fwd_rows_kernel<T, false, kCluster>);
+  return a.vec ? go(norm_fwd_rows_kernel<T, true, kCta>) : go(norm_fwd_rows_kernel<T, false, kCta>);
 }
 
 template <typename T>
@@ -903,15 +1019,19 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
   } else {
     const RowShape r = bwd_shape(a.cols);
     const int64_t ctas = a.units / r.units;
-    const int smem = a.vec ? ring_bytes<T>(r, 5) : red_bytes(r.units);
+    // Ring, and then the sums of a CTA's units.
+    const int fold = r.units > 1 ? 3 * r.units * (int)a.cols * 4 : 0;
+    const int smem = std::max(a.vec ? ring_bytes<T>(r, 5) : 0, red_bytes(r.units, r.tpr) + fold);
     auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
     const bool dy = a.dy != nullptr, x = a.d_res != nullptr;
-    if (a.vec)
-      e = dy ? (x ? go(norm_bwd_rows_kernel<T, true, true, true>) : go(norm_bwd_rows_kernel<T, true, true, false>))
-             : (x ? go(norm_bwd_rows_kernel<T, true, false, true>) : go(norm_bwd_rows_kernel<T, true, false, false>));
-    else
-      e = dy ? (x ? go(norm_bwd_rows_kernel<T, false, true, true>) : go(norm_bwd_rows_kernel<T, false, true, false>))
-             : (x ? go(norm_bwd_rows_kernel<T, false, false, true>) : go(norm_bwd_rows_kernel<T, false, false, false>));
+    auto pick = [&](auto vec) {
+      constexpr bool kVec = decltype(vec)::value;
+      if (r.tpr < 32) return go(norm_bwd_rows_kernel<T, kVec, kSub, 4>);
+      if (r.clusters > 1) return go(norm_bwd_rows_kernel<T, kVec, kCluster, 4>);
+      return dy ? (x ? go(norm_bwd_rows_kernel<T, kVec, kCta, 3>) : go(norm_bwd_rows_kernel<T, kVec, kCta, 1>))
+                : (x ? go(norm_bwd_rows_kernel<T, kVec, kCta, 2>) : go(norm_bwd_rows_kernel<T, kVec, kCta, 0>));
+    };
+    e = a.vec ? pick(std::true_type()) : pick(std::false_type());
   }
   if (e != cudaSuccess) return e;
   const unsigned ys = 3 + (a.d_gate && a.chunks_per_group > 1 ? (unsigned)a.groups : 0u);
@@ -920,6 +1040,8 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+int norm_bwd_cta_units(int64_t cols) { return cols > kHeld ? 1 : bwd_shape(cols).units; }
 
 // As many units as are resident, no more than rows.
 int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms) {

@@ -24,6 +24,7 @@ struct NormFwdArgs {
   float* rstd;                                // [2][rows]
   int64_t rows, cols, ldx, ldf, ldy, ldh, per_gate;
   float eps;
+  int* err;                                   // a wait inside a cluster ran out
   int vec;                                    // rows and parameters 16-byte aligned, columns a multiple of 8
 };
 
@@ -37,6 +38,8 @@ struct NormBwdArgs {
   int64_t rows, cols, lddy, lddh, ldx, ldf, ldy, lddx, lddf, per_gate;
   int64_t groups, chunk_rows, chunks_per_group;
   int64_t units;                              // rows of each partial array
+  int cta_units;                              // units of a CTA
+  int* err;
   int vec;
   float *part_pre, *part_post, *part_res;     // [units][cols]
   float* part_gate;                           // [groups * chunks_per_group][cols] (several chunks a group)
@@ -46,5 +49,6 @@ cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, cudaStream
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, cudaStream_t s);
 // Row units of the backward pass: each writes one row of the partial arrays.
 int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms);
+int norm_bwd_cta_units(int64_t cols);
 
 }  // namespace dmuon

@@ -163,25 +163,41 @@ __device__ __forceinline__ void load_tile(uint8_t* tile, const uint8_t* src, int
       copy16(ptx::smem_addr(place(r, c)), left ? src + r * pitch + c * 16 : src, left * SIZE);
     }
   } else {
+    // Rows on any element: 4-byte elements asynchronously, 2-byte ones one by
+    // one, bytes as 32-bit words shifted together (8191 x 8191: 16-bit values
+    // 71 us one by one and 86 by words, noise 100 against 81).
 #pragma unroll 4
     for (int i = threadIdx.x; i < kTile * kChunks; i += kQThreads) {
       const int r = i / kChunks, c = i % kChunks;
-      const int left = r < rows ? min(kPer, cols - c * kPer) : 0;
+      const int left = r < rows ? max(0, min(16, cols * SIZE - c * 16)) : 0;  // bytes
       const uint8_t* p = src + r * pitch + c * 16;
       uint8_t* dst = place(r, c);
-      if constexpr (SIZE == 4) {  // four asynchronous words
+      if constexpr (SIZE == 4) {  // asynchronous words
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(dst) + 4 * k), "l"(k < left ? p + 4 * k : src),
-                       "r"(k < left ? 4u : 0u)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(dst) + 4 * k), "l"(4 * k < left ? p + 4 * k : src),
+                       "r"(4 * k < left ? 4u : 0u)
                        : "memory");
       } else {
         uint32_t w[4] = {0, 0, 0, 0};
+        const uint32_t off = (uint32_t)((uintptr_t)p & 3);
+        // Five words hold sixteen bytes; inside the row they run from before
+        // byte 0 (not in the first chunk) to past byte 15 (not in the last).
+        if (SIZE == 1 && left == 16 && (off == 0 || (c > 0 && cols - c * 16 >= 20))) {
+          const uint32_t* q = reinterpret_cast<const uint32_t*>(p - off);
+          uint32_t x[5];
 #pragma unroll
-        for (int k = 0; k < kPer; ++k) {
-          if (k >= left) continue;
-          if constexpr (SIZE == 2) w[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + k) << (16 * (k & 1));
-          else w[k / 4] |= (uint32_t)__ldg(p + k) << (8 * (k & 3));
+          for (int k = 0; k < 4; ++k) x[k] = __ldg(q + k);
+          x[4] = off ? __ldg(q + 4) : 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(x[k], x[k + 1], off * 8);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            if (k * SIZE >= left) continue;
+            if constexpr (SIZE == 2) w[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + k) << (16 * (k & 1));
+            else w[k / 4] |= (uint32_t)__ldg(p + k) << (8 * (k & 3));
+          }
         }
         *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
       }
@@ -451,7 +467,7 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const MxDequantArgs a) 
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = value_word<T>(q[i][kPer == 16 ? j / 4 : 0] >> (kPer == 16 ? 8 * (j & 3) : 4 * j), s);
     T* dst = (T*)a.dst + r * a.ld + col;
-    if (a.vec && col + kPer <= a.k) {
+    if (col + kPer <= a.k) {
       ptx::st_global_v8(dst, w);
     } else {
 #pragma unroll
@@ -460,6 +476,46 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const MxDequantArgs a) 
           if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(dst)[j] = w[j];
           else reinterpret_cast<uint16_t*>(dst)[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
         }
+    }
+  }
+}
+
+// Rows of dst that are not 32-byte aligned: a lane takes one byte of codes (two
+// elements), so that the stores of a warp are consecutive whatever their
+// alignment; four bytes 32 apart in flight.  With 32 bytes a lane stored
+// element by element, 8191 x 8191 bf16 took 350 us.
+constexpr int kDqAnyCols = 256;  // a warp's columns: 32 lanes x 2 x 4
+template <typename T>
+__global__ void __launch_bounds__(256) mx_dequant_any_kernel(const MxDequantArgs a) {
+  const int64_t ct = (a.k + kDqAnyCols - 1) / kDqAnyCols;
+  const int64_t row = (int64_t)(blockIdx.x / ct) * 8 + (threadIdx.x >> 5);
+  const int64_t col0 = (int64_t)(blockIdx.x % ct) * kDqAnyCols + (threadIdx.x & 31) * 2;
+  if (row >= a.rows) return;
+  const uint8_t* src = a.data + row * mx_pitch(a.k) + col0 / 2;
+  const uint8_t* scales = a.scales + (row >> 7) * mx_scale_cols(a.k) * kMxScaleTile + (row & 31) * 16 + ((row >> 5) & 3) * 4;
+  T* dst = (T*)a.dst + row * a.ld + col0;
+  const bool pairs = ((uintptr_t)dst & (2 * sizeof(T) - 1)) == 0;
+  uint32_t q[4], byte[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t col = col0 + 64 * j, blk = col / kMxBlock;
+    if (col >= a.k) continue;
+    q[j] = src[32 * j];
+    byte[j] = scales[(blk >> 2) * kMxScaleTile + (blk & 3)];
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int64_t col = col0 + 64 * j;
+    if (col >= a.k) continue;
+    const float s = scale_value(byte[j]);
+    const T v[2] = {narrow<T>(code_value(q[j], s)), narrow<T>(code_value(q[j] >> 4, s))};
+    if (pairs && col + 1 < a.k) {
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(dst + 64 * j) = make_float2(v[0], v[1]);
+      else *reinterpret_cast<uint32_t*>(dst + 64 * j) =
+          (uint32_t)*reinterpret_cast<const uint16_t*>(v) | ((uint32_t)*reinterpret_cast<const uint16_t*>(v + 1) << 16);
+    } else {
+      dst[64 * j] = v[0];
+      if (col + 1 < a.k) dst[64 * j + 1] = v[1];
     }
   }
 }
@@ -480,6 +536,11 @@ cudaError_t launch_quant(const MxQuantArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_dequant(const MxDequantArgs& a, cudaStream_t s) {
+  if (!a.vec) {
+    const int64_t ctas = (a.rows + 7) / 8 * ((a.k + kDqAnyCols - 1) / kDqAnyCols);
+    mx_dequant_any_kernel<T><<<(unsigned)ctas, 256, 0, s>>>(a);
+    return cudaGetLastError();
+  }
   const int64_t tiles = (a.rows + kDqRows - 1) / kDqRows * ((a.k + dq_cols<T>() - 1) / dq_cols<T>());
   mx_dequant_kernel<T><<<(unsigned)tiles, 256, 0, s>>>(a);
   return cudaGetLastError();
