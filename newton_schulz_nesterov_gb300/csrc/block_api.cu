@@ -331,7 +331,7 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   a.per_gate = p->gate ? std::min(p->rows_per_gate, std::max<int64_t>(rows, 1)) : std::max<int64_t>(rows, 1);
   a.groups = (rows + a.per_gate - 1) / a.per_gate;
   a.units = norm_bwd_units(rows, cols, h->num_sms);
-  a.cta_units = norm_bwd_cta_units(cols);
+  a.cta_units = norm_bwd_cta_units(cols, a.units);
   a.err = h->d_op_err;
   // Chunks lie inside a group; no more of them than units where that can be,
   // so that no unit has two while another has one.

@@ -741,7 +741,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     df_row += a.lddf;
   }
   if (chunk >= 0) flush();
-  if (units == 1) {
+  if (a.cta_units == 1) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (!post_written) store_param<E>(part_post, u, v, sum_t[v]);  // no rows: zeros
@@ -957,7 +957,7 @@ RowShape row_shape(int64_t cols, int threads, int cta_threads) {
   RowShape r;
   const int64_t cta = (int64_t)threads * V * 8;
   r.clusters = cols <= cta ? 1 : cols <= 2 * cta ? 2 : cols <= 4 * cta ? 4 : kMaxCluster;
-  const int lanes = r.clusters > 1 ? threads : (int)((cols + 8 * V - 1) / (8 * V));
+  const int lanes = (int)((cols + 8 * V * r.clusters - 1) / (8 * V * r.clusters));  // even shares of a cluster
   r.tpr = 8;  // rows of up to 128 columns
   while (r.tpr < lanes && r.tpr < 32) r.tpr *= 2;
   if (lanes > 32) r.tpr = (lanes + 31) / 32 * 32;
@@ -1020,7 +1020,7 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
     const RowShape r = bwd_shape(a.cols);
     const int64_t ctas = a.units / r.units;
     // Ring, and then the sums of a CTA's units.
-    const int fold = r.units > 1 ? 3 * r.units * (int)a.cols * 4 : 0;
+    const int fold = a.cta_units > 1 ? 3 * r.units * (int)a.cols * 4 : 0;
     const int smem = std::max(a.vec ? ring_bytes<T>(r, 5) : 0, red_bytes(r.units, r.tpr) + fold);
     auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
     const bool dy = a.dy != nullptr, x = a.d_res != nullptr;
@@ -1041,7 +1041,9 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-int norm_bwd_cta_units(int64_t cols) { return cols > kHeld ? 1 : bwd_shape(cols).units; }
+// Units whose sums a CTA adds up itself: its own where there are many units in
+// all (fewer are added up sooner by norm_bwd_sums_kernel alone: 3 us at two a CTA).
+int norm_bwd_cta_units(int64_t cols, int64_t units) { return cols > kHeld || units <= 512 ? 1 : bwd_shape(cols).units; }
 
 // As many units as are resident, no more than rows.
 int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms) {

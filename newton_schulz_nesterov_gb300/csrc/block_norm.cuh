@@ -38,7 +38,7 @@ struct NormBwdArgs {
   int64_t rows, cols, lddy, lddh, ldx, ldf, ldy, lddx, lddf, per_gate;
   int64_t groups, chunk_rows, chunks_per_group;
   int64_t units;                              // rows of each partial array
-  int cta_units;                              // units of a CTA
+  int cta_units;                              // units whose sums one CTA has added up in its first's row
   int* err;
   int vec;
   float *part_pre, *part_post, *part_res;     // [units][cols]
@@ -49,6 +49,6 @@ cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, cudaStream
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, cudaStream_t s);
 // Row units of the backward pass: each writes one row of the partial arrays.
 int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms);
-int norm_bwd_cta_units(int64_t cols);
+int norm_bwd_cta_units(int64_t cols, int64_t units);
 
 }  // namespace dmuon
