@@ -23,7 +23,8 @@
 // from shared memory to tensor memory (32 lanes x 16 bytes, repeated for the
 // four warps) ahead of the MMAs that read them; tcgen05 operations of one
 // thread run in order, and consecutive stages alternate between two sets of
-// scale columns.
+// scale columns.  Bound by launch and latency: 512 x 512 x 512 4.3 us; one
+// token, 1 x 14336 x 4096, 7.3 us for 31 MB of weights (4.3 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -568,6 +569,10 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 // columns [0, 256), 1 is [160, 416), the scales are from 416 on.  The
 // epilogue drains the shared columns of a tile first and signals that apart;
 // the next tile's products begin then, while the rest is stored.
+//
+// Bound by the tensor cores, and by what an SM takes from L2 (about 70 bytes a
+// clock: 70 KB a stage and pair in 560 clocks where the products alone are
+// 512): 16384 x 14336 x 4096 to bf16 265 us, 7.26 PFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kPairScales = kScaleBytes * 3;              // A's 128 rows, B's 256
 constexpr int kPairStage = 2 * kPBytes + kPairScales;     // 35 KB
