@@ -409,7 +409,7 @@ int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p,
  * not used.  Column sums run in a fixed order: the same inputs give the same
  * bits.  rows == 0 writes zero weight gradients.  The first call of a larger
  * size allocates workspace (synchronous; DMUON_ERR_ARG while `stream` is being
- * captured).
+ * captured); what a captured graph uses stays until the handle is destroyed.
  */
 typedef struct {
     const void* dy; int64_t lddy;
@@ -430,9 +430,8 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p,
  * recorded since the previous call of this function: per-matrix flags of
  * the last planned list (bit 0: non-finite input) are copied to
  * flags[0..min(n_flags, n_mats)) when flags != NULL, then cleared.
- * Returns DMUON_ERR_TIMEOUT if a kernel's bounded wait ran out (a wait of
- * dmuon_mxfp4_gemm too),
- * DMUON_ERR_NONFINITE if any flag is set, DMUON_OK otherwise.
+ * Returns DMUON_ERR_TIMEOUT if a kernel's bounded wait ran out (those of
+ * dmuon_mxfp4_gemm and of the block norms too), DMUON_ERR_NONFINITE if any flag is set, DMUON_OK otherwise.
  */
 int dmuon_get_status(dmuon_handle_t h, int* flags, int n_flags);
 

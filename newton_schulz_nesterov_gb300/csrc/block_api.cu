@@ -352,12 +352,15 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
                               (gate_parts ? (size_t)(a.groups * a.chunks_per_group) : 0));
   if (h->op_ws_cap < need) {
     if (capturing(stream)) return fail(h, DMUON_ERR_ARG, "block_norm_backward: first call of this size under capture");
-    if (h->op_ws) {
+    if (h->op_ws && h->op_ws_captured) {
+      h->op_ws_kept.push_back(h->op_ws);
+    } else if (h->op_ws) {
       cudaDeviceSynchronize();  // earlier work may still use it
       cudaFree(h->op_ws);
     }
     h->op_ws = nullptr;
     h->op_ws_cap = 0;
+    h->op_ws_captured = false;
     const cudaError_t e = cudaMalloc(&h->op_ws, need);
     if (e != cudaSuccess) {
       h->op_ws = nullptr;
@@ -366,6 +369,7 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
     }
     h->op_ws_cap = need;
   }
+  if (!h->op_ws_captured) h->op_ws_captured = capturing(stream);
   float* w = (float*)h->op_ws;
   a.part_pre = w;
   a.part_post = w + (size_t)a.units * cols;

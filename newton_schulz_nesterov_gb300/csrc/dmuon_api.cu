@@ -1052,6 +1052,7 @@ void dmuon_destroy(dmuon_handle_t h) {
   if (h->aux_dev) cudaFree(h->aux_dev);
   if (h->aux_host) cudaFreeHost(h->aux_host);
   if (h->op_ws) cudaFree(h->op_ws);
+  for (void* w : h->op_ws_kept) cudaFree(w);
   if (h->d_op_err) cudaFree(h->d_op_err);
   for (auto& r : h->prof) { cudaEventDestroy(r.a); cudaEventDestroy(r.b); }
   for (auto e : h->ev_pool) cudaEventDestroy(e);
