@@ -346,7 +346,8 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   for (const void* v : {(const void*)p->post_w, (const void*)p->pre_w, (const void*)p->gate, (const void*)p->res_scale,
                         (const void*)q->d_gate})
     if (!aligned(v, 16)) a.vec = 0;
-  const size_t line = (size_t)cols * 4;
+  a.part_ld = (cols + 3) / 4 * 4;
+  const size_t line = (size_t)a.part_ld * 4;
   const bool gate_parts = q->d_gate && a.chunks_per_group > 1;
   const size_t need = line * ((size_t)a.units * (q->d_res_scale ? 3 : 2) +
                               (gate_parts ? (size_t)(a.groups * a.chunks_per_group) : 0));
@@ -372,9 +373,9 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   if (!h->op_ws_captured) h->op_ws_captured = capturing(stream);
   float* w = (float*)h->op_ws;
   a.part_pre = w;
-  a.part_post = w + (size_t)a.units * cols;
-  a.part_res = a.part_post + (size_t)a.units * cols;
-  a.part_gate = a.part_post + (size_t)a.units * cols * (q->d_res_scale ? 2 : 1);
+  a.part_post = w + (size_t)a.units * a.part_ld;
+  a.part_res = a.part_post + (size_t)a.units * a.part_ld;
+  a.part_gate = a.part_post + (size_t)a.units * a.part_ld * (q->d_res_scale ? 2 : 1);
   LaunchGuard g(h, stream, DMUON_KIND_NORM_BWD);
   ++h->launches;  // rows, then column sums
   const cudaError_t e = launch_norm_bwd(a, p->dtype, stream);

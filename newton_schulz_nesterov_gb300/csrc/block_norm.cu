@@ -54,7 +54,12 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 // VEC: chunks of eight consecutive columns, 16-byte accesses (every row and
 // parameter 16-byte aligned, columns a multiple of 8).  Otherwise columns a
 // unit apart, so that the scalar accesses of a warp are consecutive, loaded
-// without the ring.
+// without the ring; but the backward of 2-byte types, whose loads and stores
+// these would bind, gives a thread sixteen consecutive columns: the ring takes
+// the three aligned 16-byte pieces around them, they are shifted together from
+// there, and shifted back for aligned stores with the neighbour's last words
+// (FIGURES).  The forward is no faster that way (16384 x 4095 bf16 134 us
+// against 128, and 4.4 against 3.3 at 300 x 501).
 constexpr int V = 2;                             // chunks of eight columns a thread
 constexpr int kFwdThreads = 512, kBwdThreads = 256;  // of an SM: 128 and 255 registers a thread
 constexpr int kMaxCluster = 8;
@@ -78,13 +83,16 @@ __device__ __forceinline__ RowUnit row_unit(int64_t cols, int tpr) {
 }
 
 // Column of value e of chunk v, in the CTA: runs of E columns a thread (the 16
-// bytes of an access, or 1), runs of the unit's threads side by side.
+// bytes of an access, 1, or all of them), runs of the unit's threads side by side.
 template <int E>
 __device__ __forceinline__ int col_of(const RowUnit& u, int v, int e) {
-  return ((v * (8 / E) + e / E) * u.tpr + u.t) * E + e % E;
+  if constexpr (E == 8 * V) return u.t * E + v * 8 + e;
+  else return ((v * (8 / E) + e / E) * u.tpr + u.t) * E + e % E;
 }
-template <typename T, bool VEC>
-constexpr int run_of() { return VEC ? 16 / (int)sizeof(T) : 1; }
+// How a thread's values come: whole chunks, one by one, or by shifted pieces.
+enum Access { kChunks, kSingles, kPieces };
+template <typename T>
+constexpr int run_of(Access how) { return how == kChunks ? 16 / (int)sizeof(T) : how == kSingles ? 1 : 8 * V; }
 
 // Sums of N values over a row's threads, in a fixed order, to all of them.
 // Consecutive calls alternate between two halves of `red` ([2][units][3]
@@ -232,6 +240,22 @@ struct Chunk8 {
 
 constexpr int parts_of(int size) { return size / 2; }  // 16-byte parts of a chunk
 
+// Eight values in their type.
+template <typename T>
+__device__ __forceinline__ void pack4(const f2 (&val)[4], uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack2(val[i]);
+    if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = __floats2half2_rn(p.x, p.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    } else {
+      const __nv_bfloat162 h = __floats2bfloat162_rn(p.x, p.y);
+      w[i] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+}
+
 // `row` is the first of this CTA's columns, here and below.
 template <typename T>
 __device__ __forceinline__ Chunk8<T> load_direct(const T* row, const RowUnit& u, int v) {
@@ -263,28 +287,99 @@ __device__ __forceinline__ void store_chunk(T* row, const RowUnit& u, int v, con
       if (c < u.cols) row[c] = narrow<T>(o[e]);
     }
   } else if constexpr (sizeof(T) == 4) {
+    const bool wide = E < 8 * V || ((uintptr_t)row & 15) == 0;
 #pragma unroll
     for (int e = 0; e < 8; e += 4) {
       const int c = col_of<E>(u, v, e);
-      if (c < u.cols)
+      if (wide && c + 3 < u.cols) {
         *reinterpret_cast<uint4*>(row + c) = make_uint4(__float_as_uint(o[e]), __float_as_uint(o[e + 1]), __float_as_uint(o[e + 2]),
                                                         __float_as_uint(o[e + 3]));
+      } else if (E == 8 * V) {
+#pragma unroll
+        for (int j = e; j < e + 4; ++j) {
+          const int cj = col_of<E>(u, v, j);
+          if (cj < u.cols) row[cj] = o[j];
+        }
+      }
     }
   } else {
     const int c = col_of<E>(u, v, 0);
     if (c >= u.cols) return;
     uint32_t w[4];
+    pack4<T>(val, w);
+    *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// Bytes of `row` past a 16-byte boundary.
+template <typename T>
+__device__ __forceinline__ uint32_t past16(const T* row) { return (uint32_t)(uintptr_t)row & 15u; }
+
+// out[i] = the word at byte 4 i + m of w (m even, below 16; N words).
+template <int N>
+__device__ __forceinline__ void shift_out(uint32_t (&out)[N], const uint32_t (&w)[N + 4], uint32_t m) {
+  const uint32_t sh = (m & 2) * 8;
+  auto from = [&](auto k) {
+    constexpr int K = decltype(k)::value;
+#pragma unroll
+    for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(w[K + i], w[K + i + 1], sh);
+  };
+  switch (m >> 2) {
+    case 0: from(std::integral_constant<int, 0>()); break;
+    case 1: from(std::integral_constant<int, 1>()); break;
+    case 2: from(std::integral_constant<int, 2>()); break;
+    default: from(std::integral_constant<int, 3>()); break;
+  }
+}
+
+// Sixteen values of 2 bytes a thread at any even address, by the aligned
+// 16-byte pieces that they begin in: a thread's first piece takes the last
+// words of the thread before.  Where that is another warp's (or another unit's)
+// either side stores its own bytes.  All lanes of a warp call it.
+template <typename T>
+__device__ __forceinline__ void store_shifted(T* row, const RowUnit& u, const f2 (&val)[V][4], bool live) {
+  uint32_t w[16];  // the thread before's last four words, this one's eight, and room
+#pragma unroll
+  for (int v = 0; v < V; ++v) pack4<T>(val[v], w + 4 + 4 * v);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = __shfl_up_sync(0xffffffffu, w[8 + i], 1);
+    w[12 + i] = 0;
+  }
+  const int lane = threadIdx.x & 31, c = u.t * 8 * V;
+  if (!live || c >= u.cols) return;
+  const uint32_t m = past16(row);
+  T* own = row + c;
+  if (c + 16 > u.cols) {  // the row's last columns
+#pragma unroll
+    for (int e = 0; e < 15; ++e)
+      if (c + e < u.cols) reinterpret_cast<uint16_t*>(own)[e] = (uint16_t)(w[4 + e / 2] >> (16 * (e & 1)));
+    return;
+  }
+  uint32_t o[12];  // words of the pieces from this thread's first on
+  if (m == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] = w[4 + i];
+  } else {
+    shift_out<12>(o, w, 16 - m);
+  }
+  uint32_t* piece = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(own) - m);
+  if (m == 0 || (lane > 0 && u.t > 0)) {
+    *reinterpret_cast<uint4*>(piece) = make_uint4(o[0], o[1], o[2], o[3]);
+  } else {  // from byte m on
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if constexpr (std::is_same<T, __half>::value) {
-        const __half2 h = __floats2half2_rn(o[2 * i], o[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      } else {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(o[2 * i], o[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t*>(&h);
-      }
+      if (4 * i >= (int)m) piece[i] = o[i];
+      else if (4 * i + 2 == (int)m) reinterpret_cast<uint16_t*>(piece)[2 * i + 1] = (uint16_t)(o[i] >> 16);
     }
-    *reinterpret_cast<uint4*>(row + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  *reinterpret_cast<uint4*>(piece + 4) = make_uint4(o[4], o[5], o[6], o[7]);
+  if (m && (lane == 31 || u.t + 1 == u.tpr || c + 32 > u.cols)) {  // the last m bytes
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (4 * i + 4 <= (int)m) piece[8 + i] = o[8 + i];
+      else if (4 * i + 2 == (int)m) reinterpret_cast<uint16_t*>(piece + 8)[2 * i] = (uint16_t)o[8 + i];
+    }
   }
 }
 
@@ -293,7 +388,24 @@ __device__ __forceinline__ void store_chunk(T* row, const RowUnit& u, int v, con
 template <int E>
 __device__ __forceinline__ void load_param(f2 (&val)[4], const float* p, const RowUnit& u, int v) {
   p += u.col0;
-  if constexpr (E > 1) {
+  if constexpr (E == 8 * V) {
+    const bool wide = ((uintptr_t)p & 15) == 0;
+#pragma unroll
+    for (int e = 0; e < 8; e += 4) {
+      const int c = col_of<E>(u, v, e);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (wide && c + 3 < u.cols) {
+        a = *reinterpret_cast<const float4*>(p + c);
+      } else {
+        if (c < u.cols) a.x = p[c];
+        if (c + 1 < u.cols) a.y = p[c + 1];
+        if (c + 2 < u.cols) a.z = p[c + 2];
+        if (c + 3 < u.cols) a.w = p[c + 3];
+      }
+      val[e / 2] = pack2(a.x, a.y);
+      val[e / 2 + 1] = pack2(a.z, a.w);
+    }
+  } else if constexpr (E > 1) {
 #pragma unroll
     for (int e = 0; e < 8; e += 4) {
       const int c = col_of<E>(u, v, e);
@@ -315,13 +427,31 @@ __device__ __forceinline__ void store_param(float* p, const RowUnit& u, int v, c
   store_chunk<float, E>(p + u.col0, u, v, val);
 }
 
-// The private ring: slot s, array k, part i of chunk v of this thread.
-template <typename T, int ARRAYS>
+// The private ring: slot s, array k, part i of chunk v of this thread, or
+// (rows on any element) piece i of the three around both chunks.
+template <typename T>
+constexpr int row_parts(Access how) { return how == kPieces ? 3 : V * parts_of(sizeof(T)); }
+template <typename T, int ARRAYS, Access HOW>
 struct Ring {
   static constexpr int E = 16 / (int)sizeof(T);
   uint32_t base, step;  // this thread's part 0; bytes from one part to the next
-  __device__ __forceinline__ uint32_t slot(int s) const { return base + s * ARRAYS * V * parts_of(sizeof(T)) * step; }
+  __device__ __forceinline__ uint32_t slot(int s) const { return base + s * ARRAYS * row_parts<T>(HOW) * step; }
   __device__ __forceinline__ void fetch(uint32_t slot, int k, const T* row, const RowUnit& u) const {
+    if constexpr (HOW == kPieces) {
+      // Aligned pieces, cut off at the row's end (zeros from there on); before
+      // the row they begin at most 14 bytes early, in the piece of its first byte.
+      if (u.t * 8 * V >= u.cols) return;
+      const uint32_t m = past16(row);
+      const uint8_t* from = reinterpret_cast<const uint8_t*>(row + u.t * 8 * V) - m;
+      const int left = (u.cols - u.t * 8 * V) * 2 + (int)m;  // bytes to the row's end
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        const int n = i == 2 && m == 0 ? 0 : max(0, min(16, left - 16 * i));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(slot + (k * 3 + i) * step), "l"(n ? from + 16 * i : from), "r"(n)
+                     : "memory");
+      }
+      return;
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -331,6 +461,22 @@ struct Ring {
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + ((k * V + v) * parts_of(sizeof(T)) + i) * step), "l"(row + c)
                        : "memory");
       }
+  }
+  // Both chunks of a row that is m bytes past a 16-byte boundary.
+  __device__ __forceinline__ void take_shifted(Chunk8<T> (&r)[V], uint32_t slot, int k, uint32_t m, const RowUnit& u) const {
+    uint32_t w[12], o[8];
+#pragma unroll
+    for (int i = 0; i < 12; ++i) w[i] = 0;
+    if (u.t * 8 * V < u.cols)
+#pragma unroll
+      for (int i = 0; i < 3; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[4 * i]), "=r"(w[4 * i + 1]), "=r"(w[4 * i + 2]), "=r"(w[4 * i + 3])
+                     : "r"(slot + (k * 3 + i) * step)
+                     : "memory");
+    shift_out<8>(o, w, m);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i / 4].w[i % 4] = o[i];
   }
   __device__ __forceinline__ Chunk8<T> take(uint32_t slot, int k, int v, const RowUnit& u) const {
     Chunk8<T> r;
@@ -359,7 +505,7 @@ template <int N>
 __device__ __forceinline__ void wait_group() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 template <typename T>
-constexpr int ring_depth() { return sizeof(T) == 4 ? 2 : 4; }
+constexpr int ring_depth(Access how) { return sizeof(T) == 4 ? 2 : how == kPieces ? 3 : 4; }
 // Row sums (only of units of several warps), then two barriers; the ring after
 // them starts on 128 bytes (16 further on, every access of it took two lines:
 // norm_bwd 147 -> 158 us).
@@ -370,13 +516,14 @@ __host__ __device__ constexpr int red_bytes(int units, int tpr) { return (tpr > 
 template <typename T, bool VEC, int KIND>
 __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const NormFwdArgs a, int tpr, int clusters) {
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kRing = ring_depth<T>(), E = run_of<T, VEC>();
+  constexpr Access kHow = VEC ? kChunks : kSingles;
+  constexpr int kRing = ring_depth<T>(kHow), E = run_of<T>(kHow);
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
   uint8_t* after = smem + red_bytes(units, tpr);
   RowSums sums;
   sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err);
-  const Ring<T, 2> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
+  const Ring<T, 2, kHow> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   const int64_t per = (a.rows + all - 1) / all;
   const int row0 = (int)min(id * per, a.rows), row1 = (int)min(row0 + per, a.rows);
@@ -520,6 +667,9 @@ struct ChunkRows {
   }
 };
 
+template <typename T, bool VEC>
+__host__ __device__ constexpr Access bwd_access() { return VEC ? kChunks : sizeof(T) == 2 ? kPieces : kSingles; }
+
 // One row needs mean(dh w_pre yn) for t and then mean(g t w_post fn) for df;
 // with t = dy + r2 (i - yn m2), i = dh w_pre, the second is
 //   mean(g w fn (dy + r2 i)) - r2 m2 mean(g w fn yn)
@@ -534,13 +684,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
   const bool DY = WHICH == 4 ? a.dy != nullptr : (WHICH & 1) != 0;
   const bool X = WHICH == 4 ? a.d_res != nullptr : (WHICH & 2) != 0;
   extern __shared__ __align__(128) uint8_t smem[];
-  constexpr int kRing = ring_depth<T>(), E = run_of<T, VEC>();
+  constexpr Access kHow = bwd_access<T, VEC>();
+  constexpr int kRing = ring_depth<T>(kHow), E = run_of<T>(kHow);
+  constexpr bool kHasRing = kHow != kSingles, kShifted = kHow == kPieces;
   const RowUnit u = row_unit(a.cols, tpr);
   const int units = blockDim.x / tpr;
   uint8_t* after = smem + red_bytes(units, tpr);
   RowSums sums;
   sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err);
-  const Ring<T, 5> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
+  const Ring<T, 5, kHow> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   ChunkRows at{(int)all, (int)id, 0, 0};
   at.open(a);
@@ -577,7 +729,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     }
     commit_group();
   };
-  if constexpr (VEC)
+  if constexpr (kHasRing)
     for (int s = 0; s < kRing; ++s) fetch(s);
   if constexpr (KIND == kCluster) ptx::cluster_sync();
   else __syncthreads();
@@ -596,7 +748,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       for (int i = 0; i < 4; ++i) res[v][i] = both(1.f);
   }
   const float inv = 1.f / (float)a.cols;
-  float* part_post = a.part_post + id * a.cols;
+  float* part_post = a.part_post + id * a.part_ld;
   bool post_written = false;
   T *dx_row = nullptr, *df_row = nullptr;
   int chunk = -1;
@@ -619,7 +771,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       store_param<E>(part_post, u, v, o);
       if (a.d_gate) {
         if (a.chunks_per_group > 1) {
-          store_param<E>(a.part_gate + (int64_t)chunk * a.cols, u, v, sum_t[v]);
+          store_param<E>(a.part_gate + (int64_t)chunk * a.part_ld, u, v, sum_t[v]);
         } else {
           load_param<E>(w, a.post_w, u, v);
 #pragma unroll
@@ -667,29 +819,54 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     const f2 rr1 = both(r1), rr2 = both(r2);
     f2 yn[V][4], fn[V][4], q[V][4], s0 = 0, s1 = 0, s2 = 0;
     Chunk8<T> x[V];
-    if constexpr (VEC) wait_group<kRing - 1>();
+    if constexpr (kHasRing) wait_group<kRing - 1>();
     const uint32_t from = ring.slot(slot);
+    Chunk8<T> s_dy[V], s_dh[V], s_y[V], s_f[V];
+    if constexpr (kShifted) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        s_dy[v].zero();
+        s_dh[v].zero();
+        s_y[v].zero();
+        s_f[v].zero();
+        x[v].zero();
+      }
+      if (live) {
+        if (DY) ring.take_shifted(s_dy, from, 0, past16((const T*)a.dy + row * a.lddy + u.col0), u);
+        ring.take_shifted(s_dh, from, 1, past16((const T*)a.dh + row * a.lddh + u.col0), u);
+        ring.take_shifted(s_y, from, 2, past16((const T*)a.y + row * a.ldy + u.col0), u);
+        ring.take_shifted(s_f, from, 3, past16((const T*)a.f + row * a.ldf + u.col0), u);
+        if (X) ring.take_shifted(x, from, 4, past16((const T*)a.x + row * a.ldx + u.col0), u);
+      }
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Chunk8<T> dy, dh, y, f;
-      dy.zero();
-      dh.zero();
-      y.zero();
-      f.zero();
-      x[v].zero();
-      if (live) {
-        if constexpr (VEC) {
-          if (DY) dy = ring.take(from, 0, v, u);
-          dh = ring.take(from, 1, v, u);
-          y = ring.take(from, 2, v, u);
-          f = ring.take(from, 3, v, u);
-          if (X) x[v] = ring.take(from, 4, v, u);
-        } else {
-          if (DY) dy = load_direct<T>((const T*)a.dy + row * a.lddy + u.col0, u, v);
-          dh = load_direct<T>((const T*)a.dh + row * a.lddh + u.col0, u, v);
-          y = load_direct<T>((const T*)a.y + row * a.ldy + u.col0, u, v);
-          f = load_direct<T>((const T*)a.f + row * a.ldf + u.col0, u, v);
-          if (X) x[v] = load_direct<T>((const T*)a.x + row * a.ldx + u.col0, u, v);
+      if constexpr (kShifted) {
+        dy = s_dy[v];
+        dh = s_dh[v];
+        y = s_y[v];
+        f = s_f[v];
+      } else {
+        dy.zero();
+        dh.zero();
+        y.zero();
+        f.zero();
+        x[v].zero();
+        if (live) {
+          if constexpr (VEC) {
+            if (DY) dy = ring.take(from, 0, v, u);
+            dh = ring.take(from, 1, v, u);
+            y = ring.take(from, 2, v, u);
+            f = ring.take(from, 3, v, u);
+            if (X) x[v] = ring.take(from, 4, v, u);
+          } else {
+            if (DY) dy = load_direct<T>((const T*)a.dy + row * a.lddy + u.col0, u, v);
+            dh = load_direct<T>((const T*)a.dh + row * a.lddh + u.col0, u, v);
+            y = load_direct<T>((const T*)a.y + row * a.ldy + u.col0, u, v);
+            f = load_direct<T>((const T*)a.f + row * a.ldf + u.col0, u, v);
+            if (X) x[v] = load_direct<T>((const T*)a.x + row * a.ldx + u.col0, u, v);
+          }
         }
       }
 #pragma unroll
@@ -705,7 +882,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
         s2 = fma2(b, yn[v][i], s2);
       }
     }
-    if constexpr (!VEC) {
+    if constexpr (!kHasRing) {
       if (live && row + 2 < at.end) {  // the row after next, to L2
         if (DY && u.t == 0) prefetch_row((const T*)a.dy + (row + 2) * a.lddy + u.col0, u.cols);
         if (u.t == 1) prefetch_row((const T*)a.dh + (row + 2) * a.lddh + u.col0, u.cols);
@@ -716,27 +893,31 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     }
     float s[3] = {add_up(s0), add_up(s1), add_up(s2)};
     row_sum<3, KIND>(s, u, sums);
-    if constexpr (VEC) {
+    if constexpr (kHasRing) {
       fetch(slot);  // this thread has taken its slot
       if (++slot == kRing) slot = 0;
     }
     const float m2 = r2 * s[0] * inv, m1 = (s[1] - m2 * s[2]) * inv;
     const f2 nm2 = both(-m2), nm1 = both(-m1);
+    f2 dx[V][4], df[V][4];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      f2 dx[4], df[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 t = fma2(yn[v][i], nm2, q[v][i]);
         sum_t[v][i] = fma2(t, fn[v][i], sum_t[v][i]);
         if (X) sum_res[v][i] = fma2(t, x[v].pair(i), sum_res[v][i]);
-        dx[i] = mul2(res[v][i], t);
-        df[i] = mul2(rr1, fma2(fn[v][i], nm1, mul2(gw[v][i], t)));
+        dx[v][i] = mul2(res[v][i], t);
+        df[v][i] = mul2(rr1, fma2(fn[v][i], nm1, mul2(gw[v][i], t)));
       }
-      if (live) {
-        store_chunk<T, E>(dx_row, u, v, dx);
-        store_chunk<T, E>(df_row, u, v, df);
+      if (!kShifted && live) {
+        store_chunk<T, E>(dx_row, u, v, dx[v]);
+        store_chunk<T, E>(df_row, u, v, df[v]);
       }
+    }
+    if constexpr (kShifted) {
+      store_shifted(dx_row, u, dx, live);
+      store_shifted(df_row, u, df, live);
     }
     dx_row += a.lddx;
     df_row += a.lddf;
@@ -746,13 +927,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (!post_written) store_param<E>(part_post, u, v, sum_t[v]);  // no rows: zeros
-      store_param<E>(a.part_pre + id * a.cols, u, v, sum_pre[v]);
-      if (X) store_param<E>(a.part_res + id * a.cols, u, v, sum_res[v]);
+      store_param<E>(a.part_pre + id * a.part_ld, u, v, sum_pre[v]);
+      if (X) store_param<E>(a.part_res + id * a.part_ld, u, v, sum_res[v]);
     }
   } else {  // one row of sums a CTA, in its first unit's place: added up where the ring was
     float* fold = reinterpret_cast<float*>(after);  // [3][units][cols]
     const int n = (int)a.cols;
-    if constexpr (VEC) wait_group<0>();
+    if constexpr (kHasRing) wait_group<0>();
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -763,7 +944,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       if (X) store_param<E>(fold + (2 * units + u.unit) * n, u, v, sum_res[v]);
     }
     __syncthreads();
-    const int64_t first = (id - u.unit) * n;
+    const int64_t first = (id - u.unit) * a.part_ld;
     for (int c = threadIdx.x; c < (X ? 3 : 2) * n; c += blockDim.x) {
       const int k = c / n, col = c - k * n;
       float sum = 0.f;
@@ -846,9 +1027,9 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdArgs a) {
   __shared__ float red[3 * kThreads / 32];
   const int64_t n_chunks = a.groups * a.chunks_per_group;
-  float* pre = a.part_pre + (int64_t)blockIdx.x * a.cols;
-  float* post = a.part_post + (int64_t)blockIdx.x * a.cols;
-  float* res = a.d_res ? a.part_res + (int64_t)blockIdx.x * a.cols : nullptr;
+  float* pre = a.part_pre + (int64_t)blockIdx.x * a.part_ld;
+  float* post = a.part_post + (int64_t)blockIdx.x * a.part_ld;
+  float* res = a.d_res ? a.part_res + (int64_t)blockIdx.x * a.part_ld : nullptr;
   for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) {
     pre[c] = post[c] = 0.f;
     if (res) res[c] = 0.f;
@@ -861,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdArgs a)
     const float* gate = a.gate ? a.gate + group * a.cols : nullptr;
     // Column sums of t fn over the chunk: where they are wanted for the gate
     // they go to the chunk's own row, else straight to the CTA's sum.
-    float* own = a.d_gate ? (a.chunks_per_group > 1 ? a.part_gate + chunk * a.cols : a.d_gate + group * a.cols) : nullptr;
+    float* own = a.d_gate ? (a.chunks_per_group > 1 ? a.part_gate + chunk * a.part_ld : a.d_gate + group * a.cols) : nullptr;
     if (own)
       for (int64_t c = threadIdx.x; c < a.cols; c += kThreads) own[c] = 0.f;
     for (int64_t row = r0; row < r1_; ++row) {
@@ -915,7 +1096,7 @@ __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a)
   const float* src;
   float* dst;
   int n = (int)(a.units / a.cta_units);
-  int64_t step = a.cta_units * a.cols;  // a CTA's sums are in its first unit's row
+  int64_t step = a.cta_units * a.part_ld;  // a CTA's sums are in its first unit's row
   if (blockIdx.y == 0) { src = a.part_pre; dst = a.d_pre_w; }
   else if (blockIdx.y == 1) { src = a.part_post; dst = a.d_post_w; }
   else if (blockIdx.y == 2) { src = a.part_res; dst = a.d_res; }
@@ -923,8 +1104,8 @@ __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a)
     const int64_t g = blockIdx.y - 3;
     // The last group may be short: its chunks past the rows are not written.
     n = (int)((min(a.per_gate, a.rows - g * a.per_gate) + a.chunk_rows - 1) / a.chunk_rows);
-    step = a.cols;
-    src = a.part_gate + g * a.chunks_per_group * a.cols;
+    step = a.part_ld;
+    src = a.part_gate + g * a.chunks_per_group * a.part_ld;
     dst = a.d_gate + g * a.cols;
   }
   if (!dst) return;
@@ -991,8 +1172,8 @@ cudaError_t launch_rows(K kernel, const A& a, const RowShape& r, int64_t ctas, i
 }
 
 template <typename T>
-int ring_bytes(const RowShape& r, int arrays) {
-  return red_bytes(r.units, r.tpr) + ring_depth<T>() * arrays * V * parts_of(sizeof(T)) * r.tpr * r.units * 16;
+int ring_bytes(const RowShape& r, int arrays, Access how) {
+  return red_bytes(r.units, r.tpr) + (how == kSingles ? 0 : ring_depth<T>(how) * arrays * row_parts<T>(how) * r.tpr * r.units * 16);
 }
 
 template <typename T>
@@ -1004,7 +1185,7 @@ cudaError_t fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
   }
   const RowShape r = fwd_shape(a.cols);
   const int64_t ctas = std::min((a.rows + r.units - 1) / r.units, (int64_t)std::max(1, sms * r.resident / r.clusters));
-  const int smem = a.vec ? ring_bytes<T>(r, 2) : red_bytes(r.units, r.tpr);
+  const int smem = ring_bytes<T>(r, 2, a.vec ? kChunks : kSingles);
   auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
   if (r.tpr < 32) return a.vec ? go(norm_fwd_rows_kernel<T, true, kSub>) : go(norm_fwd_rows_kernel<T, false, kSub>);
   if (r.clusters > 1) return a.vec ? go(norm_fwd_rows_kernel<T, true, kCluster>) : go(norm_fwd_rows_kernel<T, false, kCluster>);
@@ -1022,7 +1203,7 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
     const int64_t ctas = a.units / r.units;
     // Ring, and then the sums of a CTA's units.
     const int fold = a.cta_units > 1 ? 3 * r.units * (int)a.cols * 4 : 0;
-    const int smem = std::max(a.vec ? ring_bytes<T>(r, 5) : 0, red_bytes(r.units, r.tpr) + fold);
+    const int smem = std::max(ring_bytes<T>(r, 5, a.vec ? bwd_access<T, true>() : bwd_access<T, false>()), red_bytes(r.units, r.tpr) + fold);
     auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
     const bool dy = a.dy != nullptr, x = a.d_res != nullptr;
     auto pick = [&](auto vec) {

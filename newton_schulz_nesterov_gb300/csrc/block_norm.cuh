@@ -38,6 +38,7 @@ struct NormBwdArgs {
   int64_t rows, cols, lddy, lddh, ldx, ldf, ldy, lddx, lddf, per_gate;
   int64_t groups, chunk_rows, chunks_per_group;
   int64_t units;                              // rows of each partial array
+  int64_t part_ld;                            // pitch of the partial arrays: columns to a multiple of 4
   int cta_units;                              // units whose sums one CTA has added up in its first's row
   int* err;
   int vec;
