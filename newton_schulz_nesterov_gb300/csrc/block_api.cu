@@ -262,7 +262,7 @@ int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p, void
           rows_aligned(p->y, p->ldy, p->dtype) && rows_aligned(p->h, p->ldh, p->dtype) && aligned(p->post_w, 16) &&
           aligned(p->pre_w, 16) && aligned(p->gate, 16) && aligned(p->res_scale, 16);
   LaunchGuard g(h, stream, DMUON_KIND_NORM_FWD);
-  const cudaError_t e = launch_norm_fwd(a, p->dtype, h->num_sms, stream);
+  const cudaError_t e = launch_norm_fwd(a, p->dtype, h->num_sms, h->norm_places, stream);
   if (e != cudaSuccess) return fail(h, cuda_err(e), "block_norm_forward launch", e);
   h->last_stream = stream;
   return DMUON_OK;
@@ -330,7 +330,7 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   a.lddf = q->lddf;
   a.per_gate = p->gate ? std::min(p->rows_per_gate, std::max<int64_t>(rows, 1)) : std::max<int64_t>(rows, 1);
   a.groups = (rows + a.per_gate - 1) / a.per_gate;
-  a.units = norm_bwd_units(rows, cols, h->num_sms);
+  a.units = norm_bwd_units(rows, cols, h->num_sms, h->norm_places);
   a.cta_units = norm_bwd_cta_units(cols, a.units);
   a.err = h->d_op_err;
   // Chunks lie inside a group; no more of them than units where that can be,

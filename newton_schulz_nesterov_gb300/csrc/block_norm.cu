@@ -58,7 +58,8 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 // these would bind, gives a thread sixteen consecutive columns: the ring takes
 // the three aligned 16-byte pieces around them, they are shifted together from
 // there, and shifted back for aligned stores with the neighbour's last words
-// (FIGURES).  The forward is no faster that way (16384 x 4095 bf16 134 us
+// (16384 x 4095 bf16 backward 290 us one by one, 232 so; 65535 x 255 182 and
+// 84).  The forward is no faster that way (16384 x 4095 bf16 134 us
 // against 128, and 4.4 against 3.3 at 300 x 501).
 constexpr int V = 2;                             // chunks of eight columns a thread
 constexpr int kFwdThreads = 512, kBwdThreads = 256;  // of an SM: 128 and 255 registers a thread
@@ -1176,15 +1177,49 @@ int ring_bytes(const RowShape& r, int arrays, Access how) {
   return red_bytes(r.units, r.tpr) + (how == kSingles ? 0 : ring_depth<T>(how) * arrays * row_parts<T>(how) * r.tpr * r.units * 16);
 }
 
+// CTAs (clusters) of rows that are resident together.  How many clusters of
+// four or more fit depends on how the device's SMs are grouped: it is asked
+// once and kept (2048 x 16384 bf16 backward, clusters of four, a grid of SMs / 4
+// of them took 204 us, the last ones alone; 126 with as many as fit).
+int places(const RowShape& r, int sms, int* kept, bool backward) {
+  if (r.clusters == 1) return std::max(1, sms * r.resident);
+  int& n = kept[(backward ? 0 : 4) + (r.clusters == 2 ? 0 : r.clusters == 4 ? 1 : 2)];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = r.clusters;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(sms / r.clusters * r.clusters, 1, 1);
+    cfg.blockDim = dim3(backward ? kBwdThreads : kFwdThreads, 1, 1);  // the most: one CTA an SM
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const RowShape full{(int)cfg.blockDim.x, r.clusters, 1, 1};
+    auto ask = [&](auto kernel, int arrays) {
+      cfg.dynamicSmemBytes = ring_bytes<__nv_bfloat16>(full, arrays, kChunks);
+      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) == cudaSuccess)
+        return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
+      return cudaErrorInvalidValue;
+    };
+    const cudaError_t e = backward ? ask(norm_bwd_rows_kernel<__nv_bfloat16, true, kCluster, 4>, 5)
+                                   : ask(norm_fwd_rows_kernel<__nv_bfloat16, true, kCluster>, 2);
+    if (e != cudaSuccess || n < 1) {
+      cudaGetLastError();
+      n = std::max(1, sms / r.clusters);
+    }
+  }
+  return n;
+}
+
 template <typename T>
-cudaError_t fwd(const NormFwdArgs& a, int sms, cudaStream_t s) {
+cudaError_t fwd(const NormFwdArgs& a, int sms, int* kept, cudaStream_t s) {
   if (a.cols > kHeld) {
     const int64_t grid = std::min(a.rows, (int64_t)sms * 8);
     norm_fwd_kernel<T><<<(unsigned)grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
   const RowShape r = fwd_shape(a.cols);
-  const int64_t ctas = std::min((a.rows + r.units - 1) / r.units, (int64_t)std::max(1, sms * r.resident / r.clusters));
+  const int64_t ctas = std::min((a.rows + r.units - 1) / r.units, (int64_t)places(r, sms, kept, false));
   const int smem = ring_bytes<T>(r, 2, a.vec ? kChunks : kSingles);
   auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
   if (r.tpr < 32) return a.vec ? go(norm_fwd_rows_kernel<T, true, kSub>) : go(norm_fwd_rows_kernel<T, false, kSub>);
@@ -1228,17 +1263,17 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
 int norm_bwd_cta_units(int64_t cols, int64_t units) { return cols > kHeld || units <= 512 ? 1 : bwd_shape(cols).units; }
 
 // As many units as are resident, no more than rows.
-int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms) {
+int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms, int* kept) {
   if (cols > kHeld) return std::min<int64_t>(std::max<int64_t>(rows, 1), (int64_t)sms * 4);
   const RowShape r = bwd_shape(cols);
-  const int64_t ctas = std::min<int64_t>(std::max(1, sms * r.resident / r.clusters), (std::max<int64_t>(rows, 1) + r.units - 1) / r.units);
+  const int64_t ctas = std::min<int64_t>(places(r, sms, kept, true), (std::max<int64_t>(rows, 1) + r.units - 1) / r.units);
   return ctas * r.units;
 }
 
-cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, cudaStream_t s) {
-  if (dtype == DMUON_BF16) return fwd<__nv_bfloat16>(a, sms, s);
-  if (dtype == DMUON_F16) return fwd<__half>(a, sms, s);
-  return fwd<float>(a, sms, s);
+cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, int* kept, cudaStream_t s) {
+  if (dtype == DMUON_BF16) return fwd<__nv_bfloat16>(a, sms, kept, s);
+  if (dtype == DMUON_F16) return fwd<__half>(a, sms, kept, s);
+  return fwd<float>(a, sms, kept, s);
 }
 
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, cudaStream_t s) {

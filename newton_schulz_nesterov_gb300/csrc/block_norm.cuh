@@ -46,10 +46,11 @@ struct NormBwdArgs {
   float* part_gate;                           // [groups * chunks_per_group][cols] (several chunks a group)
 };
 
-cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, cudaStream_t s);
+// kept: what is asked of the device once, eight integers of the handle, 0 at first.
+cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, int* kept, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, cudaStream_t s);
 // Row units of the backward pass: each writes one row of the partial arrays.
-int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms);
+int64_t norm_bwd_units(int64_t rows, int64_t cols, int sms, int* kept);
 int norm_bwd_cta_units(int64_t cols, int64_t units);
 
 }  // namespace dmuon

@@ -130,6 +130,7 @@ struct dmuon_ctx {
   int* d_op_err = nullptr;
   void* op_ws = nullptr;
   size_t op_ws_cap = 0;
+  int norm_places[8] = {};
   bool op_ws_captured = false;         // a graph holds op_ws: it stays until the handle goes
   std::vector<void*> op_ws_kept;
 };
