@@ -153,58 +153,73 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, uint32_t b
 
 // Tile rows of SIZE-byte elements into shared memory, zero outside the matrix
 // (rows and cols: those that are left of it in this tile, at most kTile).
+// Rows on any element: 4-byte elements one by one; the others by the aligned
+// 16-byte pieces around a row, the last of which goes to `extra` (16 bytes a
+// row), and realign() shifts them into place.  A piece is cut off at the row's
+// end and begins at most 15 bytes before the row, in the piece of its first byte.
+// 8191 x 8191 in both directions, bf16: 54 us, with noise 87, loaded one by one
+// 71 and 164; fp32 83 either way, and 777 x 2061 4.8 one by one, 6.2 by pieces.
 template <int SIZE, bool NOISE>
-__device__ __forceinline__ void load_tile(uint8_t* tile, const uint8_t* src, int64_t pitch, int rows, int cols, int vec) {
+__device__ __forceinline__ uint8_t* place(uint8_t* tile, uint32_t r, uint32_t c) {
+  return tile + r * (kTile * SIZE) + (NOISE ? swz_noise(c, r) : swz<SIZE>(c, r)) * 16;
+}
+template <int SIZE, bool NOISE>
+__device__ __forceinline__ void load_tile(uint8_t* tile, uint8_t* extra, const uint8_t* src, int64_t pitch, int rows, int cols, int vec) {
   constexpr int kChunks = kTile * SIZE / 16;  // per row
   constexpr int kPer = 16 / SIZE;
-  auto place = [&](uint32_t r, uint32_t c) { return tile + r * (kTile * SIZE) + (NOISE ? swz_noise(c, r) : swz<SIZE>(c, r)) * 16; };
   if (vec) {
     for (int i = threadIdx.x; i < kTile * kChunks; i += kQThreads) {
       const int r = i / kChunks, c = i % kChunks;
       const int left = r < rows ? max(0, min(kPer, cols - c * kPer)) : 0;
-      copy16(ptx::smem_addr(place(r, c)), left ? src + r * pitch + c * 16 : src, left * SIZE);
+      copy16(ptx::smem_addr(place<SIZE, NOISE>(tile, r, c)), left ? src + r * pitch + c * 16 : src, left * SIZE);
     }
-  } else {
-    // Rows on any element: 4-byte elements asynchronously, 2-byte ones one by
-    // one, bytes as 32-bit words shifted together.  8191 x 8191 bf16 in both
-    // directions: values one by one 71 us, by words 86; with noise 164 us with
-    // its bytes one by one, 145 by words.
+  } else if constexpr (SIZE == 4) {
 #pragma unroll 4
     for (int i = threadIdx.x; i < kTile * kChunks; i += kQThreads) {
       const int r = i / kChunks, c = i % kChunks;
       const int left = r < rows ? max(0, min(16, cols * SIZE - c * 16)) : 0;  // bytes
       const uint8_t* p = src + r * pitch + c * 16;
-      uint8_t* dst = place(r, c);
-      if constexpr (SIZE == 4) {  // asynchronous words
+      const uint32_t dst = ptx::smem_addr(place<SIZE, NOISE>(tile, r, c));
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(ptx::smem_addr(dst) + 4 * k), "l"(4 * k < left ? p + 4 * k : src),
-                       "r"(4 * k < left ? 4u : 0u)
-                       : "memory");
-      } else {
-        uint32_t w[4] = {0, 0, 0, 0};
-        const uint32_t off = (uint32_t)((uintptr_t)p & 3);
-        // Five words hold sixteen bytes; inside the row they run from before
-        // byte 0 (not in the first chunk) to past byte 15 (not in the last).
-        if (SIZE == 1 && left == 16 && (off == 0 || (c > 0 && cols - c * 16 >= 20))) {
-          const uint32_t* q = reinterpret_cast<const uint32_t*>(p - off);
-          uint32_t x[5];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = __ldg(q + k);
-          x[4] = off ? __ldg(q + 4) : 0u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(x[k], x[k + 1], off * 8);
-        } else {
-#pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            if (k * SIZE >= left) continue;
-            if constexpr (SIZE == 2) w[k / 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p) + k) << (16 * (k & 1));
-            else w[k / 4] |= (uint32_t)__ldg(p + k) << (8 * (k & 3));
-          }
-        }
-        *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+      for (int k = 0; k < 16; k += 4)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + k), "l"(k < left ? p + k : src), "r"(k < left ? 4u : 0u)
+                     : "memory");
     }
+  } else {
+    auto piece = [&](uint8_t* dst, int r, int c) {
+      const uint8_t* row = src + r * pitch;
+      const int m = (int)((uintptr_t)row & 15);
+      const int n = r < rows ? max(0, min(16, m + cols * SIZE - c * 16)) : 0;
+      copy16(ptx::smem_addr(dst), n ? row - m + c * 16 : src - ((uintptr_t)src & 15), n);
+    };
+    for (int i = threadIdx.x; i < kTile * kChunks; i += kQThreads) {
+      const int r = i / kChunks, c = i % kChunks;
+      piece(place<SIZE, NOISE>(tile, r, c), r, c);
+    }
+    if (threadIdx.x < kTile) piece(extra + threadIdx.x * 16, threadIdx.x, kChunks);
+  }
+}
+
+// A warp has whole rows: every chunk is read before one is written.
+template <int SIZE, bool NOISE>
+__device__ __forceinline__ void realign(uint8_t* tile, const uint8_t* extra, const uint8_t* src, int64_t pitch, int rows) {
+  constexpr int kChunks = kTile * SIZE / 16, kRows = 32 / kChunks;  // rows a warp has at a time
+  const int lane = threadIdx.x & 31, c = lane % kChunks;
+#pragma unroll 2
+  for (int r = (threadIdx.x >> 5) * kRows + lane / kChunks; r < kTile; r += kQThreads / 32 * kRows) {
+    const uint32_t m = r < rows ? (uint32_t)(uintptr_t)(src + r * pitch) & 15u : 0u;
+    uint8_t* dst = place<SIZE, NOISE>(tile, r, c);
+    const uint4 a = *reinterpret_cast<const uint4*>(dst);
+    const uint4 b = *reinterpret_cast<const uint4*>(c + 1 < kChunks ? place<SIZE, NOISE>(tile, r, c + 1) : extra + r * 16);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (m & 3) * 8);
+    __syncwarp();
+    *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
@@ -385,10 +400,20 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) mx_quant_ke
   const int64_t tr = blockIdx.x / ct, tc = blockIdx.x % ct;
   const int64_t row0 = tr * kTile, col0 = tc * kTile;
   const int rows = (int)min((int64_t)kTile, a.rows - row0), cols = (int)min((int64_t)kTile, a.cols - col0);
-  load_tile<S, false>(tile, (const uint8_t*)a.src + (row0 * a.ld + col0) * S, a.ld * S, rows, cols, a.vec);
-  if constexpr (NOISE) load_tile<1, true>(noise, a.noise + row0 * a.noise_ld + col0, a.noise_ld, rows, cols, a.noise_vec);
+  const uint8_t* src = (const uint8_t*)a.src + (row0 * a.ld + col0) * S;
+  const uint8_t* src_noise = NOISE ? a.noise + row0 * a.noise_ld + col0 : nullptr;
+  uint8_t *extra = noise + (NOISE ? kTile * kTile : 0), *extra_noise = extra + kTile * 16;
+  load_tile<S, false>(tile, extra, src, a.ld * S, rows, cols, a.vec);
+  if constexpr (NOISE) load_tile<1, true>(noise, extra_noise, src_noise, a.noise_ld, rows, cols, a.noise_vec);
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncthreads();
+  if ((S < 4 && !a.vec) || (NOISE && !a.noise_vec)) {
+    if constexpr (S < 4)
+      if (!a.vec) realign<S, false>(tile, extra, src, a.ld * S, rows);
+    if constexpr (NOISE)
+      if (!a.noise_vec) realign<1, true>(noise, extra_noise, src_noise, a.noise_ld, rows);
+    __syncthreads();
+  }
   if (a.row_data) row_phase<T, NOISE>(a, tile, noise, scales, row0, col0, rows, cols);
   if (a.col_data) col_phase<T, NOISE>(a, tile, noise, scales + kMxScaleTile, row0, col0, rows, cols);
   __syncthreads();
@@ -526,7 +551,8 @@ __global__ void __launch_bounds__(256) mx_dequant_any_kernel(const MxDequantArgs
 template <typename T, bool NOISE>
 cudaError_t launch_quant_one(const MxQuantArgs& a, cudaStream_t s) {
   const int64_t tiles = (a.rows + kTile - 1) / kTile * ((a.cols + kTile - 1) / kTile);
-  const int smem = 2 * kMxScaleTile + kTile * kTile * ((int)sizeof(T) + (NOISE ? 1 : 0));
+  const bool whole = (sizeof(T) == 4 || a.vec) && (!NOISE || a.noise_vec);
+  const int smem = 2 * kMxScaleTile + kTile * kTile * ((int)sizeof(T) + (NOISE ? 1 : 0)) + (whole ? 0 : 2 * kTile * 16);
   const cudaError_t e = cudaFuncSetAttribute(mx_quant_kernel<T, NOISE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   mx_quant_kernel<T, NOISE><<<(unsigned)tiles, kQThreads, smem, s>>>(a);
