@@ -12,6 +12,7 @@
 #include "../../include/dmuon.h"
 #include "block_norm.cuh"
 #include "bounded_wait.cuh"
+#include "pieces.cuh"
 #include "ptx.cuh"
 
 namespace dmuon {
@@ -312,76 +313,15 @@ __device__ __forceinline__ void store_chunk(T* row, const RowUnit& u, int v, con
   }
 }
 
-// Bytes of `row` past a 16-byte boundary.
-template <typename T>
-__device__ __forceinline__ uint32_t past16(const T* row) { return (uint32_t)(uintptr_t)row & 15u; }
-
-// out[i] = the word at byte 4 i + m of w (m even, below 16; N words).
-template <int N>
-__device__ __forceinline__ void shift_out(uint32_t (&out)[N], const uint32_t (&w)[N + 4], uint32_t m) {
-  const uint32_t sh = (m & 2) * 8;
-  auto from = [&](auto k) {
-    constexpr int K = decltype(k)::value;
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = __funnelshift_r(w[K + i], w[K + i + 1], sh);
-  };
-  switch (m >> 2) {
-    case 0: from(std::integral_constant<int, 0>()); break;
-    case 1: from(std::integral_constant<int, 1>()); break;
-    case 2: from(std::integral_constant<int, 2>()); break;
-    default: from(std::integral_constant<int, 3>()); break;
-  }
-}
-
-// Sixteen values of 2 bytes a thread at any even address, by the aligned
-// 16-byte pieces that they begin in: a thread's first piece takes the last
-// words of the thread before.  Where that is another warp's (or another unit's)
-// either side stores its own bytes.  All lanes of a warp call it.
+// Sixteen values of 2 bytes a thread.  All lanes of a warp call it.
 template <typename T>
 __device__ __forceinline__ void store_shifted(T* row, const RowUnit& u, const f2 (&val)[V][4], bool live) {
-  uint32_t w[16];  // the thread before's last four words, this one's eight, and room
+  uint32_t w[16];
 #pragma unroll
   for (int v = 0; v < V; ++v) pack4<T>(val[v], w + 4 + 4 * v);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    w[i] = __shfl_up_sync(0xffffffffu, w[8 + i], 1);
-    w[12 + i] = 0;
-  }
   const int lane = threadIdx.x & 31, c = u.t * 8 * V;
-  if (!live || c >= u.cols) return;
-  const uint32_t m = past16(row);
-  T* own = row + c;
-  if (c + 16 > u.cols) {  // the row's last columns
-#pragma unroll
-    for (int e = 0; e < 15; ++e)
-      if (c + e < u.cols) reinterpret_cast<uint16_t*>(own)[e] = (uint16_t)(w[4 + e / 2] >> (16 * (e & 1)));
-    return;
-  }
-  uint32_t o[12];  // words of the pieces from this thread's first on
-  if (m == 0) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = w[4 + i];
-  } else {
-    shift_out<12>(o, w, 16 - m);
-  }
-  uint32_t* piece = reinterpret_cast<uint32_t*>(reinterpret_cast<uint8_t*>(own) - m);
-  if (m == 0 || (lane > 0 && u.t > 0)) {
-    *reinterpret_cast<uint4*>(piece) = make_uint4(o[0], o[1], o[2], o[3]);
-  } else {  // from byte m on
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * i >= (int)m) piece[i] = o[i];
-      else if (4 * i + 2 == (int)m) reinterpret_cast<uint16_t*>(piece)[2 * i + 1] = (uint16_t)(o[i] >> 16);
-    }
-  }
-  *reinterpret_cast<uint4*>(piece + 4) = make_uint4(o[4], o[5], o[6], o[7]);
-  if (m && (lane == 31 || u.t + 1 == u.tpr || c + 32 > u.cols)) {  // the last m bytes
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (4 * i + 4 <= (int)m) piece[8 + i] = o[8 + i];
-      else if (4 * i + 2 == (int)m) reinterpret_cast<uint16_t*>(piece + 8)[2 * i] = (uint16_t)o[8 + i];
-    }
-  }
+  store_pieces<2>(reinterpret_cast<uint8_t*>(row + c), w, (u.cols - c) * 2, lane == 0 || u.t == 0,
+                  lane == 31 || u.t + 1 == u.tpr || c + 32 > u.cols, live);
 }
 
 // Eight fp32 values of a parameter (its first column is column 0 of the row);

@@ -23,6 +23,7 @@
 
 #include "../../include/dmuon.h"
 #include "mxfp4.cuh"
+#include "pieces.cuh"
 #include "ptx.cuh"
 
 namespace dmuon {
@@ -450,8 +451,10 @@ template <>
 __device__ __forceinline__ __half narrow<__half>(float f) { return __float2half_rn(f); }
 
 // A lane reads the codes of 32 bytes of output (16 or 8 elements, all of one
-// block) and stores them whole, four rows 8 apart in flight.
-constexpr int kDqRows = 32;  // per CTA: 8 warps x 4 rows
+// block) and stores them whole, four rows 8 apart in flight.  ANY: rows of dst on
+// any element, by aligned pieces (8191 x 8191 bf16 40 us, fp32 56; two elements
+// a lane, stored side by side, took 71 and 68).  Short rows share a warp.
+constexpr int kDqRows = 32;  // per CTA: 8 warps x 4 rows, 32 / lanes times as many short ones
 template <typename T>
 constexpr int dq_cols() { return 32 * 32 / (int)sizeof(T); }
 
@@ -462,20 +465,21 @@ __device__ __forceinline__ uint32_t value_word(uint32_t codes, float s) {  // th
   return (uint32_t)*reinterpret_cast<const uint16_t*>(&lo) | ((uint32_t)*reinterpret_cast<const uint16_t*>(&hi) << 16);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(256) mx_dequant_kernel(const MxDequantArgs a) {
+template <typename T, bool ANY>
+__global__ void __launch_bounds__(256) mx_dequant_kernel(const MxDequantArgs a, int lanes) {  // lanes of a row: a power of two
   constexpr int kPer = 32 / (int)sizeof(T);  // elements a lane
   const int64_t ct = (a.k + dq_cols<T>() - 1) / dq_cols<T>();
-  const int64_t row0 = (int64_t)(blockIdx.x / ct) * kDqRows + (threadIdx.x >> 5);
-  const int64_t col = (int64_t)(blockIdx.x % ct) * dq_cols<T>() + (threadIdx.x & 31) * kPer;
-  if (col >= a.k) return;
+  const int at_once = 256 / lanes, lane = threadIdx.x & (lanes - 1);
+  const int64_t row0 = (int64_t)(blockIdx.x / ct) * 4 * at_once + threadIdx.x / lanes;
+  const int64_t col = (int64_t)(blockIdx.x % ct) * dq_cols<T>() + lane * kPer;
+  if (!ANY && col >= a.k) return;
   const int64_t pitch = mx_pitch(a.k), blk = col / kMxBlock, sc = mx_scale_cols(a.k);
-  uint32_t q[4][kPer / 8];
-  uint32_t byte[4];
+  uint32_t q[4][kPer / 8] = {};
+  uint32_t byte[4] = {};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t r = row0 + 8 * i;
-    if (r >= a.rows) continue;
+    const int64_t r = row0 + at_once * i;
+    if (r >= a.rows || (ANY && col >= a.k)) continue;
     const uint32_t* src = reinterpret_cast<const uint32_t*>(a.data + r * pitch + col / 2);
     if constexpr (kPer == 16) {
       const uint2 v = *reinterpret_cast<const uint2*>(src);
@@ -488,62 +492,25 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const MxDequantArgs a) 
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t r = row0 + 8 * i;
-    if (r >= a.rows) continue;
+    const int64_t r = row0 + at_once * i;
+    if (!ANY && r >= a.rows) continue;
     const float s = scale_value(byte[i]);
-    uint32_t w[8];
+    uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = value_word<T>(q[i][kPer == 16 ? j / 4 : 0] >> (kPer == 16 ? 8 * (j & 3) : 4 * j), s);
+    for (int j = 0; j < 8; ++j) w[4 + j] = value_word<T>(q[i][kPer == 16 ? j / 4 : 0] >> (kPer == 16 ? 8 * (j & 3) : 4 * j), s);
     T* dst = (T*)a.dst + r * a.ld + col;
-    if (col + kPer <= a.k) {
-      ptx::st_global_v8(dst, w);
+    const int64_t left = (a.k - col) * (int64_t)sizeof(T);
+    if constexpr (ANY) {
+      store_pieces<sizeof(T)>(reinterpret_cast<uint8_t*>(dst), w, left, lane == 0, lane == lanes - 1 || left < 64, r < a.rows);
+    } else if (left >= 32) {
+      ptx::st_global_v8(dst, *reinterpret_cast<uint32_t(*)[8]>(w + 4));
     } else {
 #pragma unroll
-      for (int j = 0; j < kPer; ++j)
+      for (int j = 0; j < kPer - 1; ++j)
         if (col + j < a.k) {
-          if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(dst)[j] = w[j];
-          else reinterpret_cast<uint16_t*>(dst)[j] = (uint16_t)(w[j / 2] >> (16 * (j & 1)));
+          if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(dst)[j] = w[4 + j];
+          else reinterpret_cast<uint16_t*>(dst)[j] = (uint16_t)(w[4 + j / 2] >> (16 * (j & 1)));
         }
-    }
-  }
-}
-
-// Rows of dst that are not 32-byte aligned: a lane takes one byte of codes (two
-// elements), so that the stores of a warp are consecutive whatever their
-// alignment; four bytes 32 apart in flight.  With 32 bytes a lane stored
-// element by element, 8191 x 8191 bf16 took 350 us.
-constexpr int kDqAnyCols = 256;  // a warp's columns: 32 lanes x 2 x 4
-template <typename T>
-__global__ void __launch_bounds__(256) mx_dequant_any_kernel(const MxDequantArgs a) {
-  const int64_t ct = (a.k + kDqAnyCols - 1) / kDqAnyCols;
-  const int64_t row = (int64_t)(blockIdx.x / ct) * 8 + (threadIdx.x >> 5);
-  const int64_t col0 = (int64_t)(blockIdx.x % ct) * kDqAnyCols + (threadIdx.x & 31) * 2;
-  if (row >= a.rows) return;
-  const uint8_t* src = a.data + row * mx_pitch(a.k) + col0 / 2;
-  const uint8_t* scales = a.scales + (row >> 7) * mx_scale_cols(a.k) * kMxScaleTile + (row & 31) * 16 + ((row >> 5) & 3) * 4;
-  T* dst = (T*)a.dst + row * a.ld + col0;
-  const bool pairs = ((uintptr_t)dst & (2 * sizeof(T) - 1)) == 0;
-  uint32_t q[4], byte[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t col = col0 + 64 * j, blk = col / kMxBlock;
-    if (col >= a.k) continue;
-    q[j] = src[32 * j];
-    byte[j] = scales[(blk >> 2) * kMxScaleTile + (blk & 3)];
-  }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int64_t col = col0 + 64 * j;
-    if (col >= a.k) continue;
-    const float s = scale_value(byte[j]);
-    const T v[2] = {narrow<T>(code_value(q[j], s)), narrow<T>(code_value(q[j] >> 4, s))};
-    if (pairs && col + 1 < a.k) {
-      if constexpr (sizeof(T) == 4) *reinterpret_cast<float2*>(dst + 64 * j) = make_float2(v[0], v[1]);
-      else *reinterpret_cast<uint32_t*>(dst + 64 * j) =
-          (uint32_t)*reinterpret_cast<const uint16_t*>(v) | ((uint32_t)*reinterpret_cast<const uint16_t*>(v + 1) << 16);
-    } else {
-      dst[64 * j] = v[0];
-      if (col + 1 < a.k) dst[64 * j + 1] = v[1];
     }
   }
 }
@@ -565,13 +532,12 @@ cudaError_t launch_quant(const MxQuantArgs& a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_dequant(const MxDequantArgs& a, cudaStream_t s) {
-  if (!a.vec) {
-    const int64_t ctas = (a.rows + 7) / 8 * ((a.k + kDqAnyCols - 1) / kDqAnyCols);
-    mx_dequant_any_kernel<T><<<(unsigned)ctas, 256, 0, s>>>(a);
-    return cudaGetLastError();
-  }
-  const int64_t tiles = (a.rows + kDqRows - 1) / kDqRows * ((a.k + dq_cols<T>() - 1) / dq_cols<T>());
-  mx_dequant_kernel<T><<<(unsigned)tiles, 256, 0, s>>>(a);
+  int lanes = 1;
+  while (lanes < 32 && lanes * 32 / (int)sizeof(T) < a.k) lanes *= 2;
+  const int64_t rows = kDqRows * (32 / lanes);
+  const int64_t tiles = (a.rows + rows - 1) / rows * ((a.k + dq_cols<T>() - 1) / dq_cols<T>());
+  if (a.vec) mx_dequant_kernel<T, false><<<(unsigned)tiles, 256, 0, s>>>(a, lanes);
+  else mx_dequant_kernel<T, true><<<(unsigned)tiles, 256, 0, s>>>(a, lanes);
   return cudaGetLastError();
 }
 
