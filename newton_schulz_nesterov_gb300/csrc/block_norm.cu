@@ -1026,15 +1026,49 @@ __global__ void __launch_bounds__(kThreads) norm_bwd_kernel(const NormBwdArgs a)
   }
 }
 
+__device__ __forceinline__ void add4(float4& s, const float4& v) {
+  s.x += v.x;
+  s.y += v.y;
+  s.z += v.z;
+  s.w += v.w;
+}
+
 // Column sums over the units' partial rows (blockIdx.y: 0 pre, 1 post, 2 res)
 // and, from 3 on, over the chunks of gate group blockIdx.y - 3: 32 columns a
 // block, four a thread (the rows' pitch is whole 16 bytes), 32 rows at a time,
-// eight loads in flight, then the 32 in a fixed order.  Launched while the rows
-// kernel runs: what it reads is there after the wait.  (Eight rows at a time,
-// launched after it: 1.1 us more at 1000 x 1111.)
+// eight loads in flight, then the 32 in a fixed order.  Groups of few chunks
+// have a warp each and 128 columns: 30000 x 100 fp32, 1875 groups of two, 53 us
+// in all where a block each took 67; 60000 x 64, 60 of 81 chunks, 43 with warps
+// and 26 with blocks.  Launched while the rows kernel runs: what it reads is
+// there after the wait (launched after it, eight rows at a time, 1.1 us more at
+// 1000 x 1111).
+__host__ __device__ __forceinline__ bool warp_a_group(const NormBwdArgs& a) { return a.chunks_per_group <= 16; }
 __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a) {
   __shared__ float red[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, turn = threadIdx.x >> 3;
+  // The last group may be short: its chunks past the rows are not written.
+  auto chunks = [&](int64_t g) { return (int)((min(a.per_gate, a.rows - g * a.per_gate) + a.chunk_rows - 1) / a.chunk_rows); };
+  if (blockIdx.y >= 3 && warp_a_group(a)) {
+    const int64_t g = (int64_t)(blockIdx.y - 3) * 8 + warp, c = (int64_t)blockIdx.x * 128 + lane * 4;
+    if (g >= a.groups || c >= a.cols) return;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int n = chunks(g);
+    const float* src = a.part_gate + g * a.chunks_per_group * a.part_ld + c;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i = 0; i < n; i += 8) {
+      float4 v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        v[k] = i + k < n ? *reinterpret_cast<const float4*>(src + (i + k) * a.part_ld) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) add4(s, v[k]);
+    }
+    const float t[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + k < a.cols) a.d_gate[g * a.cols + c + k] = t[k] * a.post_w[c + k];
+    return;
+  }
   const int64_t c0 = (int64_t)blockIdx.x * 32;
   const float* src;
   float* dst;
@@ -1045,8 +1079,7 @@ __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a)
   else if (blockIdx.y == 2) { src = a.part_res; dst = a.d_res; }
   else {
     const int64_t g = blockIdx.y - 3;
-    // The last group may be short: its chunks past the rows are not written.
-    n = (int)((min(a.per_gate, a.rows - g * a.per_gate) + a.chunk_rows - 1) / a.chunk_rows);
+    n = chunks(g);
     step = a.part_ld;
     src = a.part_gate + g * a.chunks_per_group * a.part_ld;
     dst = a.d_gate + g * a.cols;
@@ -1063,12 +1096,7 @@ __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a)
       for (int k = 0; k < 8; ++k)
         v[k] = i + 32 * k < n ? *reinterpret_cast<const float4*>(src + (i + 32 * k) * step) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        s.x += v[k].x;
-        s.y += v[k].y;
-        s.z += v[k].z;
-        s.w += v[k].w;
-      }
+      for (int k = 0; k < 8; ++k) add4(s, v[k]);
     }
   }
   float* mine = red[turn] + (threadIdx.x & 7) * 4;
@@ -1209,7 +1237,7 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
     e = a.vec ? pick(std::true_type()) : pick(std::false_type());
   }
   if (e != cudaSuccess) return e;
-  const unsigned ys = 3 + (a.d_gate && a.chunks_per_group > 1 ? (unsigned)a.groups : 0u);
+  const unsigned ys = 3 + (a.d_gate && a.chunks_per_group > 1 ? (unsigned)(warp_a_group(a) ? (a.groups + 7) / 8 : a.groups) : 0u);
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
