@@ -434,14 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
   const uint32_t tmem = *tmem_slot;
   const uint32_t full0 = ptx::smem_addr(full), empty0 = ptx::smem_addr(empty), stage0 = ptx::smem_addr(stages);
 
-  bool have = true;  // epilogue warps: the accumulator may be read
+  bool have = true;     // epilogue warps: the accumulator may be read
+  uint32_t issued = 0;  // warp 0: stages that are being loaded; warp 1: being multiplied
+  const bool elected = elect_one();
   if (warp == 0) {
-    const bool elected = elect_one();
     uint32_t s = 0, ph = 0;
-    int it = 0;
-    bool ok = true;
-    for (; it < kbn; ++it) {
-      if (!bounded_wait_warp(empty0 + s * 8, ph ^ 1u, abort_flag, a.err, tmo)) { ok = false; break; }
+    for (int it = 0; it < kbn; ++it) {
+      if (!bounded_wait_warp(empty0 + s * 8, ph ^ 1u, abort_flag, a.err, tmo)) break;
       if (elected) {
         const uint32_t fb = full0 + s * 8, st = stage0 + s * C::kStage;
         const int kb = kb0 + it;
@@ -451,21 +450,15 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
         tma_load_3d(st + kPBytes + C::kQBytes, &a.p_scales, 0, kb * 2, p0 / 128, fb);
         tma_load_3d(st + kPBytes + C::kQBytes + kScaleBytes, &a.q_scales, 0, kb * 2, q0 / 128, fb);
       }
+      ++issued;
       if (++s == (uint32_t)C::kN) { s = 0; ph ^= 1u; }
-    }
-    if (!ok || *abort_flag) {  // no copy may land after the CTA has gone
-      const int out = it < C::kN ? it : C::kN;
-      for (int i = it - out; i < it; ++i)
-        bounded_wait_slow(full0 + i % C::kN * 8, (i / C::kN) & 1u, abort_flag, a.err, false, kWaitNs);
     }
   } else if (warp == 1) {
     // A tile of NT < 128 is Q's only one, so every tile starts on a scale tile.
-    const bool elected = elect_one();
     const int last_parts = (int)((a.k - (int64_t)(total - 1) * kStageK + 63) / 64);  // K = 64 products of the last stage
     uint32_t s = 0, ph = 0;
-    bool ok = true, issued = false;
     for (int it = 0; it < kbn; ++it) {
-      if (!bounded_wait_warp(full0 + s * 8, ph, abort_flag, a.err, tmo)) { ok = false; break; }
+      if (!bounded_wait_warp(full0 + s * 8, ph, abort_flag, a.err, tmo)) break;
       ptx::tc_fence_after();
       if (elected) {
         const uint32_t st = stage0 + s * C::kStage, sc = st + kPBytes + C::kQBytes;
@@ -484,12 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
         ptx::mma_commit(empty0 + s * 8);
         if (it + 1 == kbn) ptx::mma_commit(ptx::smem_addr(done));
       }
-      issued = true;
+      ++issued;
       if (++s == (uint32_t)C::kN) { s = 0; ph ^= 1u; }
-    }
-    if (issued && (!ok || *abort_flag)) {
-      if (elected) ptx::mma_commit(ptx::smem_addr(drain));
-      bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
     }
   } else {
     have = bounded_wait_warp(ptx::smem_addr(done), 0, abort_flag, a.err, tmo);
@@ -534,11 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
       const uint32_t bytes = (uint32_t)(rows * pitch) * 4;
       const float* theirs = reinterpret_cast<const float*>(scratch);  // [rank][rows][pitch]
       const int t = threadIdx.x - 64;
-      if (have && t < split && t != rank)
+      // A rank that gave up sends too (what its stages hold: the status says
+      // that the product is not to be used), so that every rank's shares land.
+      if (t < split && t != rank)
         send(ptx::mapa_shared(ptx::smem_addr(scratch) + rank * bytes, t), ptx::smem_addr(mine) + t * bytes, bytes,
              ptx::mapa_shared(ptx::smem_addr(shares), t));
+      if (have) have = bounded_wait_warp(ptx::smem_addr(shares), 0, abort_flag, a.err, tmo);
       if (!have) bounded_wait_slow(ptx::smem_addr(shares), 0, abort_flag, a.err, false, kWaitNs);  // what is on its way lands
-      else have = bounded_wait_warp(ptx::smem_addr(shares), 0, abort_flag, a.err, tmo);
       if (have) {
         const int pr0 = p0 + rank * rows, r_here = min(rows, (int)a.p_rows - pr0);
         mine += rank * rows * pitch;
@@ -547,11 +538,20 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
         else add_shares<8, T>(a, mine, theirs, rank, pitch, r_here, q_here, pr0, q0, t);
       }
     }
+    __syncwarp();
     ptx::cluster_sync();  // no rank leaves while its shares are being read or written
   }
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (*abort_flag) {  // neither copies nor products may outlive the CTA
+    if (warp == 0 && lane == 0) drain_stages(full0, C::kN, issued, abort_flag, a.err);
+    if (warp == 1 && issued) {
+      if (elected) ptx::mma_commit(ptx::smem_addr(drain));
+      bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
+      __syncwarp();
+    }
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem, C::kTmem);
@@ -638,6 +638,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   uint64_t* drain = sready + kPairN;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile uint32_t* peer_gave_up = tmem_slot + 2;  // the peer stores both before the roles' last barrier
+  volatile uint32_t* peer_issued = tmem_slot + 3;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t tmo = a.timeout_ns ? a.timeout_ns : kWaitNs;
@@ -662,6 +664,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
     for (int i = 0; i < kPairSets; ++i) ptx::mbar_init(ptx::smem_addr(sfull + i), 8);  // 4 scale warps x 2 ranks
     ptx::mbar_init(ptx::smem_addr(drain), 1);
     *abort_flag = 0;
+    *peer_gave_up = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -673,13 +676,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   ptx::cluster_sync();  // both ranks' barriers exist before any remote signal
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  uint32_t issued = 0;  // warp 0: stages that are being loaded; warp 1: being multiplied
+  const bool elected = elect_one();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
-    const bool elected = elect_one();
     const uint32_t full0 = ptx::smem_addr(full), remote = ptx::mapa_shared(full0, 0), ready0 = ptx::smem_addr(sready);
     const uint32_t empty0 = ptx::smem_addr(empty), stage0 = ptx::smem_addr(stages);
-    uint32_t s = 0, ph = 0, issued = 0;
+    uint32_t s = 0, ph = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += npairs) {
       int mt, nt;
@@ -700,21 +704,14 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
         if (++s == kPairN) { s = 0; ph ^= 1u; }
       }
     }
-    if (!ok || *abort_flag) {  // every copy lands before exit: both ranks' codes on the leader, scales on each rank
-      const uint32_t out = issued < (uint32_t)kPairN ? issued : (uint32_t)kPairN;
-      for (uint32_t i = issued - out; i < issued; ++i) {
-        bounded_wait_slow(ready0 + i % kPairN * 8, (i / kPairN) & 1u, abort_flag, a.err, false, kWaitNs);
-        if (leader) bounded_wait_slow(full0 + i % kPairN * 8, (i / kPairN) & 1u, abort_flag, a.err, false, kWaitNs);
-      }
-    }
+    if (!leader && lane == 0) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(tmem_slot + 3), 0), issued);
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (leader) {
-      const bool elected = elect_one();
       const uint32_t full0 = ptx::smem_addr(full), empty0 = ptx::smem_addr(empty), sfull0 = ptx::smem_addr(sfull);
       const uint32_t desc0 = desc_lo(ptx::smem_addr(stages));
       uint32_t s = 0, ph = 0, set = 0, sph = 0, tc = 0;
-      bool ok = true, issued = false;
+      bool ok = true;
       for (int t = pair; ok && t < tiles; t += npairs, ++tc) {
         const uint32_t acc = tc & 1u;
         if (!bounded_wait_warp(ptx::smem_addr(tempty + acc), ((tc >> 1) & 1u) ^ 1u, abort_flag, a.err, tmo) ||
@@ -736,14 +733,10 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
             ptx::mma_commit_multicast(empty0 + s * 8, 0x3);
             if (kb + 1 == kbn) ptx::mma_commit_multicast(ptx::smem_addr(tfull + acc), 0x3);
           }
-          issued = true;
+          ++issued;
           if (++s == kPairN) { s = 0; ph ^= 1u; }
           if (++set == kPairSets) { set = 0; sph ^= 1u; }
         }
-      }
-      if (issued && (!ok || *abort_flag)) {
-        if (elected) ptx::mma_commit_pair(ptx::smem_addr(drain));
-        bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
       }
     }
   } else if (warp >= 6) {
@@ -820,7 +813,22 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *abort_flag) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(tmem_slot + 2), rank ^ 1u), 1);
+  __syncwarp();
   ptx::cluster_sync();  // no rank frees tensor memory or exits while its pair is busy
+  if (*abort_flag || *peer_gave_up) {  // nor while its copies or products are in flight
+    if (warp == 0 && lane == 0) {
+      drain_stages(ptx::smem_addr(sready), kPairN, issued, abort_flag, a.err);
+      if (leader)
+        drain_pair_stages(ptx::smem_addr(full), kPairN, issued, *peer_issued, 2 * kPBytes, abort_flag, a.err);
+    }
+    if (warp == 1 && issued) {
+      if (elected) ptx::mma_commit_pair(ptx::smem_addr(drain));
+      bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
+    }
+    __syncthreads();
+    ptx::cluster_sync();
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem, 512);
