@@ -30,8 +30,9 @@
 //
 // Every mbarrier wait is bounded (GemmArgs::timeout_ns, default 4 s without
 // progress); on timeout the CTA records
-// bit 0 of *err, stops issuing, drains its own copies and MMAs with bounded
-// waits, frees TMEM and returns.
+// bit 0 of *err, stops issuing, waits (bounded) after every role has ended for
+// its copies and MMAs in flight, frees TMEM and returns.
+#include "bounded_wait.cuh"
 #include "common.cuh"
 #include "ptx.cuh"
 
@@ -509,6 +510,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
   ptx::tc_fence_after();
   const uint32_t tmem_base = *sm.tmem_slot;
 
+  uint32_t issued = 0;  // lane 0 of warp 0: stages that are being loaded; of warp 1: being multiplied
+
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------------- producer
@@ -559,14 +562,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
           }
         }
       }
-      if (!ok || *sm.abort_flag) {
-        // Drain: wait (bounded, ignoring the abort flag) for the copies of
-        // the last issued stages so none lands after the CTA exits.
-        const uint32_t n_out = it < (uint32_t)kS ? it : (uint32_t)kS;
-        for (uint32_t i = it - n_out; i < it; ++i)
-          wait_slow(ptx::smem_addr(full + (i % kS)), (i / kS) & 1u, sm.abort_flag,
-                    a.err, false, kDrainTimeoutNs);
-      }
+      issued = it;
     }
   } else if (warp == 1) {
     if (lane == 0) {
@@ -575,7 +571,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
       constexpr uint32_t bdesc_sym = ptx::idesc_bf16(kBM, BN, 0), bdesc_app = ptx::idesc_bf16(kBM, BN, 1);
       uint32_t it = 0, tc = 0;
       bool ok = true;
-      bool issued = false;
       ItemCursor<PHASE> cur(a, (int)blockIdx.x, (int)gridDim.x);
       int4 item;
       ItemInfo inf;
@@ -601,16 +596,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
                                    : ptx::desc_sw128(sb + kk * 32, 16, 1024);
             ptx::mma_f16(dt, ad, bd, idesc, (kb | kk) != 0);
           }
-          issued = true;
           ptx::mma_commit(ptx::smem_addr(empty + s));
         }
         if (!ok) break;
         ptx::mma_commit(ptx::smem_addr(tfull + acc));
       }
-      if (issued && (!ok || *sm.abort_flag)) {
-        ptx::mma_commit(ptx::smem_addr(drain));
-        wait_slow(ptx::smem_addr(drain), 0, sm.abort_flag, a.err, false, kDrainTimeoutNs);
-      }
+      issued = it;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -634,6 +625,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_kernel(const __grid_c
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (*sm.abort_flag) {  // neither copies nor MMAs may outlive the CTA
+    if (warp == 0 && lane == 0) drain_stages(ptx::smem_addr(full), kS, issued, sm.abort_flag, a.err);
+    if (warp == 1 && issued) {
+      ptx::mma_commit(ptx::smem_addr(drain));
+      wait_slow(ptx::smem_addr(drain), 0, sm.abort_flag, a.err, false, kDrainTimeoutNs);
+    }
+    __syncwarp();
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc(tmem_base, C::kTmem);
@@ -657,6 +656,7 @@ struct PairSmem {
   uint64_t* bars;      // full[6], empty[6], tfull[2], tempty[2], drain
   uint32_t* tmem_slot;
   volatile int* abort_flag;
+  uint32_t* from_peer;  // the peer gave up; stages it issued: stored by the peer before the roles' last barrier
   uint32_t* tile_done;  // fused launches: epilogue warps done per accumulator slot
 };
 
@@ -670,6 +670,7 @@ __device__ __forceinline__ PairSmem carve_pair(uint8_t* raw) {
   s.bars = reinterpret_cast<uint64_t*>(after + 4 * kEpiWords * 4);
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.bars + 2 * kPairStages + 5);
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem_slot + 1);
+  s.from_peer = s.tmem_slot + 4;
   s.tile_done = s.tmem_slot + 2;
   return s;
 }
@@ -703,6 +704,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_pair_kernel(const __g
     }
     ptx::mbar_init(ptx::smem_addr(drain), 1);
     *sm.abort_flag = 0;
+    sm.from_peer[0] = 0;
     sm.tile_done[0] = sm.tile_done[1] = 0;
     ptx::fence_mbar_init();
   }
@@ -715,6 +717,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_pair_kernel(const __g
   ptx::cluster_sync();  // both ranks' barriers exist before any remote signal
   ptx::tc_fence_after();
   const uint32_t tmem_base = *sm.tmem_slot;
+  uint32_t issued = 0;  // lane 0 of warp 0: stages that are being loaded; of warp 1: being multiplied
 
   if (warp == 0) {
     if (lane == 0) {
@@ -767,14 +770,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_pair_kernel(const __g
           }
         }
       }
-      if (leader && (!ok || *sm.abort_flag)) {
-        // Drain: the last issued stages' bytes (both ranks') must land before
-        // exit; bounded, ignoring the abort flag.
-        const uint32_t n_out = it < (uint32_t)kPairStages ? it : (uint32_t)kPairStages;
-        for (uint32_t i = it - n_out; i < it; ++i)
-          wait_slow(ptx::smem_addr(full + (i % kPairStages)), (i / kPairStages) & 1u, sm.abort_flag,
-                    a.err, false, kDrainTimeoutNs);
-      }
+      issued = it;
+      if (!leader) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(sm.from_peer + 1), 0), issued);
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
@@ -783,7 +780,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_pair_kernel(const __g
       constexpr uint32_t bdesc_sym = ptx::idesc_bf16(256, kBN, 0), bdesc_app = ptx::idesc_bf16(256, kBN, 1);
       uint32_t it = 0, tc = 0;
       bool ok = true;
-      bool issued = false;
       ItemCursor<PHASE> cur(a, pair, npairs);
       int4 item;
       ItemInfo inf;
@@ -809,16 +805,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_pair_kernel(const __g
                                    : ptx::desc_sw128(sb + kk * 32, 16, 1024);
             ptx::mma_f16_pair(dt, ad, bd, idesc, (kb | kk) != 0);
           }
-          issued = true;
           ptx::mma_commit_multicast(ptx::smem_addr(empty + s), 0x3);
         }
         if (!ok) break;
         ptx::mma_commit_multicast(ptx::smem_addr(tfull + acc), 0x3);
       }
-      if (issued && (!ok || *sm.abort_flag)) {
-        ptx::mma_commit_pair(ptx::smem_addr(drain));
-        wait_slow(ptx::smem_addr(drain), 0, sm.abort_flag, a.err, false, kDrainTimeoutNs);
-      }
+      issued = it;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -843,7 +835,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gemm_pair_kernel(const __g
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *sm.abort_flag) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(sm.from_peer), rank ^ 1u), 1);
+  __syncwarp();
   ptx::cluster_sync();  // no rank frees TMEM or exits while its pair is busy
+  if (*sm.abort_flag || *(volatile uint32_t*)sm.from_peer) {  // nor while its copies or MMAs are in flight
+    if (warp == 0 && lane == 0 && leader)
+      drain_pair_stages(ptx::smem_addr(full), kPairStages, issued, sm.from_peer[1], kPairStageBytes, sm.abort_flag, a.err);
+    if (warp == 1 && issued) {
+      ptx::mma_commit_pair(ptx::smem_addr(drain));
+      wait_slow(ptx::smem_addr(drain), 0, sm.abort_flag, a.err, false, kDrainTimeoutNs);
+    }
+    __syncthreads();
+    ptx::cluster_sync();
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, kTmemCols);

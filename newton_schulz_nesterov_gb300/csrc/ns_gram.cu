@@ -21,8 +21,10 @@
 // barrier; warp 1 of rank 0 issues tcgen05.mma (M = 256, N = 256, K = 16;
 // fp16 in, fp32 accumulate) into one of two TMEM accumulators;
 // warps 2-5 of both CTAs run the epilogue of their 128 rows.  Every wait is
-// bounded; on expiry the CTA records bit 0 of *err, drains its own copies
-// and MMAs (bounded), frees TMEM and returns.
+// bounded; on expiry the CTA records bit 0 of *err, waits (bounded) after
+// every role has ended for its copies and MMAs in flight, frees TMEM and
+// returns.
+#include "bounded_wait.cuh"
 #include "common.cuh"
 #include "gram.cuh"
 #include "ptx.cuh"
@@ -237,6 +239,7 @@ struct PairSmem {
   uint64_t* bars;      // full[6], empty[6], tfull[2], tempty[2], drain
   uint32_t* tmem_slot;
   volatile int* abort_flag;
+  uint32_t* from_peer;  // the peer gave up; stages it issued: stored by the peer before the roles' last barrier
 };
 
 __device__ __forceinline__ PairSmem carve_pair(uint8_t* raw) {
@@ -249,6 +252,7 @@ __device__ __forceinline__ PairSmem carve_pair(uint8_t* raw) {
   s.bars = reinterpret_cast<uint64_t*>(after + 4 * kEpiWords * 4);
   s.tmem_slot = reinterpret_cast<uint32_t*>(s.bars + 2 * kPairStages + 5);
   s.abort_flag = reinterpret_cast<volatile int*>(s.tmem_slot + 1);
+  s.from_peer = s.tmem_slot + 4;
   return s;
 }
 
@@ -283,6 +287,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_pair_kernel(const __g
     }
     ptx::mbar_init(ptx::smem_addr(drain), 1);
     *sm.abort_flag = 0;
+    sm.from_peer[0] = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 1) {  // one warp of each rank allocates the pair's TMEM together
@@ -294,6 +299,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_pair_kernel(const __g
   ptx::cluster_sync();  // both ranks' barriers exist before any remote signal
   ptx::tc_fence_after();
   const uint32_t tmem_base = *sm.tmem_slot;
+  uint32_t issued = 0;  // lane 0 of warp 0: stages that are being loaded; of warp 1: being multiplied
 
   if (warp == 0) {
     if (lane == 0) {
@@ -329,14 +335,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_pair_kernel(const __g
           ptx::tma_load_2d_pair(sb + kBoxBytes, mapB, k0, rowB + kBox, fb);
         }
       }
-      if (leader && (!ok || *sm.abort_flag)) {
-        // Drain: the last issued stages' bytes (both ranks') must land before
-        // exit; bounded, ignoring the abort flag.
-        const uint32_t n_out = it < (uint32_t)kPairStages ? it : (uint32_t)kPairStages;
-        for (uint32_t i = it - n_out; i < it; ++i)
-          wait_slow(ptx::smem_addr(full + (i % kPairStages)), (i / kPairStages) & 1u, sm.abort_flag, a.err, false,
-                    kDrainTimeoutNs);
-      }
+      issued = it;
+      if (!leader) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(sm.from_peer + 1), 0), issued);
     }
   } else if (warp == 1) {
     if (lane == 0 && leader) {
@@ -344,7 +344,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_pair_kernel(const __g
       constexpr uint32_t idesc = ptx::idesc_f16(256, kBN, 0);
       uint32_t it = 0, tc = 0;
       bool ok = true;
-      bool issued = false;
       for (int w = wr.w0; ok && w < wr.w1; w += wr.step, ++tc) {
         const int4 item = a.items[w];
         const uint32_t acc = tc & 1u;
@@ -367,16 +366,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_pair_kernel(const __g
             const uint64_t bd = ptx::desc_sw128(sb + kk * 32, 16, 1024);
             ptx::mma_f16_pair(dt, ad, bd, idesc, (kb | kk) != 0);
           }
-          issued = true;
           ptx::mma_commit_multicast(ptx::smem_addr(empty + s), 0x3);
         }
         if (!ok) break;
         ptx::mma_commit_multicast(ptx::smem_addr(tfull + acc), 0x3);
       }
-      if (issued && (!ok || *sm.abort_flag)) {
-        ptx::mma_commit_pair(ptx::smem_addr(drain));
-        wait_slow(ptx::smem_addr(drain), 0, sm.abort_flag, a.err, false, kDrainTimeoutNs);
-      }
+      issued = it;
     }
   } else {
     // ------------------------------------------------------------ epilogue
@@ -398,7 +393,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1) ns_gram_pair_kernel(const __g
 
   ptx::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x == 0 && *sm.abort_flag) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(sm.from_peer), rank ^ 1u), 1);
+  __syncwarp();
   ptx::cluster_sync();  // no rank frees TMEM or exits while its pair is busy
+  if (*sm.abort_flag || *(volatile uint32_t*)sm.from_peer) {  // nor while its copies or MMAs are in flight
+    if (warp == 0 && lane == 0 && leader)
+      drain_pair_stages(ptx::smem_addr(full), kPairStages, issued, sm.from_peer[1], kPairStageBytes, sm.abort_flag, a.err);
+    if (warp == 1 && issued) {
+      ptx::mma_commit_pair(ptx::smem_addr(drain));
+      wait_slow(ptx::smem_addr(drain), 0, sm.abort_flag, a.err, false, kDrainTimeoutNs);
+    }
+    __syncthreads();
+    ptx::cluster_sync();
+  }
   if (warp == 1) {
     ptx::tc_fence_after();
     ptx::tmem_dealloc_pair(tmem_base, kTmemCols);
