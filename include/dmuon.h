@@ -444,7 +444,11 @@ const char* dmuon_last_error(dmuon_handle_t h);
  * tensor memory, returns, and dmuon_get_status reports DMUON_ERR_TIMEOUT.
  * ns == 0 restores the default (4 s).  Applies to later launches of the
  * handle; a tiny value makes the first non-immediate wait give up, which
- * is how the failure path is exercised without faulting the GPU. */
+ * is how the failure path is exercised without faulting the GPU.  The block
+ * norms wait too where a row is held by several CTAs (forward beyond 8192
+ * columns, backward beyond 4096): a wait past the limit is reported the same
+ * way, its sums then have 4 s more to come, and results are complete if they
+ * do. */
 int dmuon_set_wait_timeout(dmuon_handle_t h, uint64_t ns);
 
 /* Tensor-core tiling of later plans: 0 = automatic (the default: CTA pairs when

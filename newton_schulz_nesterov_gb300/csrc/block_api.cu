@@ -258,6 +258,7 @@ int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p, void
   a.per_gate = p->rows_per_gate;
   a.eps = p->eps;
   a.err = h->d_op_err;
+  a.timeout_ns = h->wait_timeout_ns;
   a.vec = cols % 8 == 0 && rows_aligned(p->x, p->ldx, p->dtype) && rows_aligned(p->f, p->ldf, p->dtype) &&
           rows_aligned(p->y, p->ldy, p->dtype) && rows_aligned(p->h, p->ldh, p->dtype) && aligned(p->post_w, 16) &&
           aligned(p->pre_w, 16) && aligned(p->gate, 16) && aligned(p->res_scale, 16);
@@ -333,6 +334,7 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   a.units = norm_bwd_units(rows, cols, h->num_sms, h->norm_places);
   a.cta_units = norm_bwd_cta_units(cols, a.units);
   a.err = h->d_op_err;
+  a.timeout_ns = h->wait_timeout_ns;
   // Chunks lie inside a group; no more of them than units where that can be,
   // so that no unit has two while another has one.
   a.chunks_per_group = std::max<int64_t>(1, std::min(a.per_gate, a.units / std::max<int64_t>(1, a.groups)));

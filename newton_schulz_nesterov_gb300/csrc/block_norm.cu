@@ -112,13 +112,15 @@ struct RowSums {
   int clusters, units;
   uint32_t calls;
   int* err;
-  __device__ __forceinline__ void init(float* r, uint64_t* b, int cl, int un, int* e) {
+  uint64_t limit_ns;
+  __device__ __forceinline__ void init(float* r, uint64_t* b, int cl, int un, int* e, uint64_t limit) {
     red = r;
     bars = ptx::smem_addr(b);
     clusters = cl;
     units = un;
     calls = 0;
     err = e;
+    limit_ns = limit;
     if (cl > 1 || blockDim.x / un > 32)
       for (int i = threadIdx.x; i < 2 * un * 3 * kRedRow; i += blockDim.x) r[i] = 0.f;
     if (cl > 1 && threadIdx.x == 0) {
@@ -129,27 +131,46 @@ struct RowSums {
   }
 };
 
-// A wait of row_sum in a cluster that does not end in kWaitNs sets *err; the
-// kernel goes on with what is there, so that it ends.
-__device__ __forceinline__ void wait_sums(uint32_t bar, uint32_t parity, int* err) {
-  if (ptx::mbar_try(bar, parity)) return;
-  const uint64_t t0 = ptx::globaltimer();
-  while (!ptx::mbar_try(bar, parity)) {
-    if (ptx::globaltimer() - t0 > kWaitNs || *(volatile int*)err) {
-      atomicOr(err, 1);
-      return;
+// A wait of row_sum in a cluster, with the same answer for a whole warp.  One
+// that passes the handle's limit sets *err; its sums then have kWaitNs more to
+// come, and if they do the kernel goes on with them, its barriers in step.
+// False: they do not come.  Nothing but this wait decides: *err may hold what
+// an earlier call of the handle left there.
+__device__ __forceinline__ bool wait_sums(uint32_t bar, uint32_t parity, int* err, uint64_t limit_ns) {
+  if (__all_sync(0xffffffffu, ptx::mbar_try(bar, parity))) return true;
+  const uint64_t limit = limit_ns ? limit_ns : kWaitNs;
+  uint64_t t0 = ptx::globaltimer();
+  bool late = false;
+  while (!__all_sync(0xffffffffu, ptx::mbar_try(bar, parity))) {
+    if (!__any_sync(0xffffffffu, ptx::globaltimer() - t0 > (late ? kWaitNs : limit))) continue;
+    if (late) return false;
+    late = true;
+    if ((threadIdx.x & 31) == 0) atomicOr(err, 1);
+    t0 = ptx::globaltimer();
+  }
+  return true;
+}
+
+// After a wait that returned false and the cluster barrier behind which no CTA
+// sends any more: what was sent to this CTA lands before it exits.  Peers are at
+// most one call ahead, since they wait for this CTA's sums too.
+__device__ __forceinline__ void land_sums(const RowSums& s) {
+  for (uint32_t c = s.calls; c < s.calls + 2; ++c) {
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try(s.bars + 8 * (c & 1), (c >> 1) & 1) && ptx::globaltimer() - t0 < kWaitNs) {
     }
   }
 }
 
+// False only in a cluster, one of whose CTAs does not come: the kernel leaves its rows.
 template <int N, int KIND>
-__device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, RowSums& s) {
+__device__ __forceinline__ bool row_sum(float (&v)[N], const RowUnit& u, RowSums& s) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
     if (KIND != kSub || o < u.tpr)
 #pragma unroll
       for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
-  if (KIND == kSub || (KIND == kCta && u.warps == 1)) return;
+  if (KIND == kSub || (KIND == kCta && u.warps == 1)) return true;
   const int lane = threadIdx.x & 31, warp = u.t >> 5, half = s.calls & 1;
   float* mine = s.red + (half * s.units + u.unit) * 3 * kRedRow;
   int n = u.warps;
@@ -171,8 +192,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, RowSums
                      "r"(__float_as_uint(v[k])), "r"(there)
                      : "memory");
     }
-    wait_sums(bar, (s.calls >> 1) & 1, s.err);
-    __syncwarp();
+    if (!wait_sums(bar, (s.calls >> 1) & 1, s.err, s.limit_ns)) return false;
   }
   ++s.calls;
   if (KIND == kCta && n <= 8) {  // what no warp writes is zero
@@ -181,7 +201,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, RowSums
       const float4 p = *reinterpret_cast<const float4*>(mine + k * kRedRow), q = *reinterpret_cast<const float4*>(mine + k * kRedRow + 4);
       v[k] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
     }
-    return;
+    return true;
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
@@ -192,6 +212,7 @@ __device__ __forceinline__ void row_sum(float (&v)[N], const RowUnit& u, RowSums
   for (int o = 16; o > 0; o >>= 1)
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  return true;
 }
 
 // Two fp32 values in one 64-bit register, for the packed fp32 instructions.
@@ -463,7 +484,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
   const int units = blockDim.x / tpr;
   uint8_t* after = smem + red_bytes(units, tpr);
   RowSums sums;
-  sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err);
+  sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err, a.timeout_ns);
   const Ring<T, 2, kHow> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   const int64_t per = (a.rows + all - 1) / all;
@@ -501,6 +522,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
   }
   int group_end = a.gate ? row0 : INT_MAX;  // first row past the gate row in gw
   int slot = 0;
+  bool lost = false;
   const int last = KIND == kSub ? row0 + (int)per : row1;  // as often for every unit of a warp
   for (int row = row0; row < last; ++row) {
     const bool live = KIND != kSub || row < row1;
@@ -544,7 +566,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
 #pragma unroll
       for (int i = 0; i < 4; ++i) q = fma2(fr[v].pair(i), fr[v].pair(i), q);
     float s[1] = {add_up(q)};
-    row_sum<1, KIND>(s, u, sums);
+    if (!row_sum<1, KIND>(s, u, sums)) { lost = true; break; }
     const float r1 = rsqrtf(fmaf(s[0], inv, a.eps));
     const f2 rr1 = both(r1);
     f2 y[V][4];
@@ -563,7 +585,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
       if (++slot == kRing) slot = 0;
     }
     s[0] = add_up(q);
-    row_sum<1, KIND>(s, u, sums);
+    if (!row_sum<1, KIND>(s, u, sums)) { lost = true; break; }
     const float r2 = rsqrtf(fmaf(s[0], inv, a.eps));
     const f2 rr2 = both(r2);
 #pragma unroll
@@ -579,7 +601,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1) norm_fwd_rows_kernel(const Nor
       a.rstd[a.rows + row] = r2;
     }
   }
-  if constexpr (KIND == kCluster) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
+  if constexpr (KIND == kCluster) {
+    if (lost) wait_group<0>();
+    __syncwarp();
+    ptx::cluster_sync();  // a peer may still send to this CTA's shared memory
+    if (lost) land_sums(sums);
+  }
 }
 
 // The rows of a unit, chunk after chunk (rows and chunks fit 31 bits).
@@ -632,7 +659,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
   const int units = blockDim.x / tpr;
   uint8_t* after = smem + red_bytes(units, tpr);
   RowSums sums;
-  sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err);
+  sums.init(reinterpret_cast<float*>(smem), reinterpret_cast<uint64_t*>(after - 128), clusters, units, a.err, a.timeout_ns);
   const Ring<T, 5, kHow> ring{ptx::smem_addr(after) + threadIdx.x * 16, blockDim.x * 16};
   const int64_t all = (int64_t)gridDim.x / clusters * units, id = (int64_t)(blockIdx.x / clusters) * units + u.unit;
   ChunkRows at{(int)all, (int)id, 0, 0};
@@ -725,6 +752,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
     }
     post_written = true;
   };
+  bool lost = false;
   float n1 = 0.f, n2 = 0.f;
   if (!at.done()) {
     n1 = a.rstd[at.row];
@@ -833,7 +861,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       }
     }
     float s[3] = {add_up(s0), add_up(s1), add_up(s2)};
-    row_sum<3, KIND>(s, u, sums);
+    if (!row_sum<3, KIND>(s, u, sums)) { lost = true; break; }
     if constexpr (kHasRing) {
       fetch(slot);  // this thread has taken its slot
       if (++slot == kRing) slot = 0;
@@ -893,7 +921,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) norm_bwd_rows_kernel(const Nor
       (k == 0 ? a.part_pre : k == 1 ? a.part_post : a.part_res)[first + col] = sum;
     }
   }
-  if constexpr (KIND == kCluster) ptx::cluster_sync();  // a peer may still read this CTA's shared memory
+  if constexpr (KIND == kCluster) {
+    if (lost) wait_group<0>();
+    __syncwarp();
+    ptx::cluster_sync();  // a peer may still send to this CTA's shared memory
+    if (lost) land_sums(sums);
+  }
 }
 
 // ------------------------------------------------------------ longer rows

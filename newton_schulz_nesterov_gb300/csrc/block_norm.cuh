@@ -25,6 +25,7 @@ struct NormFwdArgs {
   int64_t rows, cols, ldx, ldf, ldy, ldh, per_gate;
   float eps;
   int* err;                                   // a wait inside a cluster ran out
+  unsigned long long timeout_ns;              // its limit, 0: kWaitNs
   int vec;                                    // rows and parameters 16-byte aligned, columns a multiple of 8
 };
 
@@ -41,6 +42,7 @@ struct NormBwdArgs {
   int64_t part_ld;                            // pitch of the partial arrays: columns to a multiple of 4
   int cta_units;                              // units whose sums one CTA has added up in its first's row
   int* err;
+  unsigned long long timeout_ns;
   int vec;
   float *part_pre, *part_post, *part_res;     // [units][cols]
   float* part_gate;                           // [groups * chunks_per_group][cols] (several chunks a group)
