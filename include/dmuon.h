@@ -41,6 +41,7 @@
  * Threading/streams: a handle is not thread-safe.  Calls on one handle are
  * asynchronous on the given stream and must be issued on one stream (or be
  * ordered by the caller), because they share the handle's workspace.
+ * Handles share nothing: host threads with a handle each run side by side.
  *
  * Return codes: 0 on success, a negative DMUON_ERR_* otherwise.  Every
  * argument check happens on the host before anything is launched, so an

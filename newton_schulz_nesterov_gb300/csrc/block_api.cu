@@ -42,6 +42,16 @@ int check_packed(dmuon_ctx* h, const void* data, const void* scales, const char*
   return DMUON_OK;
 }
 
+// The kernels' limits of shared memory, set by a handle's first call (loading
+// the norms' kernels takes 15 ms, which a handle without norms does not pay).
+int ready(dmuon_ctx* h, bool& done, cudaError_t (*configure)(), const char* what) {
+  if (done) return DMUON_OK;
+  const cudaError_t e = configure();
+  if (e != cudaSuccess) return fail(h, cuda_err(e), what, e);
+  done = true;
+  return DMUON_OK;
+}
+
 bool encode(CUtensorMap* map, CUtensorMapDataType type, int dims, void* base, const cuuint64_t* size,
             const cuuint64_t* stride, const cuuint32_t* box, CUtensorMapSwizzle swizzle) {
   const cuuint32_t one[3] = {1, 1, 1};
@@ -100,6 +110,7 @@ int dmuon_mxfp4_quantize(dmuon_handle_t h, const void* src, int dtype, int64_t r
   if (((rows + 127) / 128) * ((cols + 127) / 128) > INT32_MAX)
     return fail(h, DMUON_ERR_ARG, "mxfp4_quantize: too many tiles");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
+  if ((rc = ready(h, h->quant_ready, mx_quant_configure, "mxfp4_quantize: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   MxQuantArgs a{};
   a.src = src;
@@ -238,6 +249,7 @@ int dmuon_block_norm_forward(dmuon_handle_t h, const dmuon_block_norm_t* p, void
   if (p->y == p->h || p->y == p->x || p->y == p->f || p->h == p->x || p->h == p->f)
     return fail(h, DMUON_ERR_ARG, "block_norm_forward: outputs overlap");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
+  if ((rc = ready(h, h->norm_ready, block_norm_configure, "block_norm_forward: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   NormFwdArgs a{};
   a.x = p->x;
@@ -302,6 +314,7 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p, con
   }
   if (q->d_post_w == q->d_pre_w) return fail(h, DMUON_ERR_ARG, "block_norm_backward: outputs overlap");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
+  if ((rc = ready(h, h->norm_ready, block_norm_configure, "block_norm_backward: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   NormBwdArgs a{};
   a.dy = q->dy;

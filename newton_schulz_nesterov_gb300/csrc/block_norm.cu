@@ -1174,8 +1174,6 @@ static_assert(kMaxCluster * kBwdThreads * V * 8 >= kHeld && kMaxCluster * kFwdTh
 
 template <typename K, typename A>
 cudaError_t launch_rows(K kernel, const A& a, const RowShape& r, int64_t ctas, int smem, cudaStream_t s) {
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1194,6 +1192,15 @@ cudaError_t launch_rows(K kernel, const A& a, const RowShape& r, int64_t ctas, i
 template <typename T>
 int ring_bytes(const RowShape& r, int arrays, Access how) {
   return red_bytes(r.units, r.tpr) + (how == kSingles ? 0 : ring_depth<T>(how) * arrays * row_parts<T>(how) * r.tpr * r.units * 16);
+}
+
+// Shared memory of a CTA: the ring, and in the backward where the ring was the
+// sums of the CTA's units.
+template <typename T, bool VEC>
+int fwd_bytes(const RowShape& r) { return ring_bytes<T>(r, 2, VEC ? kChunks : kSingles); }
+template <typename T, bool VEC>
+int bwd_bytes(const RowShape& r, int64_t cols, bool fold) {
+  return std::max(ring_bytes<T>(r, 5, bwd_access<T, VEC>()), red_bytes(r.units, r.tpr) + (fold ? 3 * r.units * (int)cols * 4 : 0));
 }
 
 // CTAs (clusters) of rows that are resident together.  How many clusters of
@@ -1216,9 +1223,7 @@ int places(const RowShape& r, int sms, int* kept, bool backward) {
     const RowShape full{(int)cfg.blockDim.x, r.clusters, 1, 1};
     auto ask = [&](auto kernel, int arrays) {
       cfg.dynamicSmemBytes = ring_bytes<__nv_bfloat16>(full, arrays, kChunks);
-      if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cfg.dynamicSmemBytes) == cudaSuccess)
-        return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
-      return cudaErrorInvalidValue;
+      return cudaOccupancyMaxActiveClusters(&n, kernel, &cfg);
     };
     const cudaError_t e = backward ? ask(norm_bwd_rows_kernel<__nv_bfloat16, true, kCluster, 4>, 5)
                                    : ask(norm_fwd_rows_kernel<__nv_bfloat16, true, kCluster>, 2);
@@ -1239,7 +1244,7 @@ cudaError_t fwd(const NormFwdArgs& a, int sms, int* kept, cudaStream_t s) {
   }
   const RowShape r = fwd_shape(a.cols);
   const int64_t ctas = std::min((a.rows + r.units - 1) / r.units, (int64_t)places(r, sms, kept, false));
-  const int smem = ring_bytes<T>(r, 2, a.vec ? kChunks : kSingles);
+  const int smem = a.vec ? fwd_bytes<T, true>(r) : fwd_bytes<T, false>(r);
   auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
   if (r.tpr < 32) return a.vec ? go(norm_fwd_rows_kernel<T, true, kSub>) : go(norm_fwd_rows_kernel<T, false, kSub>);
   if (r.clusters > 1) return a.vec ? go(norm_fwd_rows_kernel<T, true, kCluster>) : go(norm_fwd_rows_kernel<T, false, kCluster>);
@@ -1255,9 +1260,8 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
   } else {
     const RowShape r = bwd_shape(a.cols);
     const int64_t ctas = a.units / r.units;
-    // Ring, and then the sums of a CTA's units.
-    const int fold = a.cta_units > 1 ? 3 * r.units * (int)a.cols * 4 : 0;
-    const int smem = std::max(ring_bytes<T>(r, 5, a.vec ? bwd_access<T, true>() : bwd_access<T, false>()), red_bytes(r.units, r.tpr) + fold);
+    const bool fold = a.cta_units > 1;
+    const int smem = a.vec ? bwd_bytes<T, true>(r, a.cols, fold) : bwd_bytes<T, false>(r, a.cols, fold);
     auto go = [&](auto kernel) { return launch_rows(kernel, a, r, ctas, smem, s); };
     const bool dy = a.dy != nullptr, x = a.d_res != nullptr;
     auto pick = [&](auto vec) {
@@ -1283,7 +1287,43 @@ cudaError_t bwd(const NormBwdArgs& a, cudaStream_t s) {
   return cudaLaunchKernelEx(&cfg, norm_bwd_sums_kernel, a);
 }
 
+// The limit of dynamic shared memory belongs to the kernel on its device and not
+// to a call or a handle: it is set once, to the most that any width of rows
+// takes (widths of one shape end on a multiple of 16).
+template <typename T, bool VEC>
+cudaError_t configure() {
+  int fwd_most = 0, bwd_most = 0;
+  for (int64_t cols = 16; cols <= kHeld; cols += 16) {
+    fwd_most = std::max(fwd_most, fwd_bytes<T, VEC>(fwd_shape(cols)));
+    const RowShape r = bwd_shape(cols);
+    bwd_most = std::max(bwd_most, bwd_bytes<T, VEC>(r, cols, r.units > 1));
+  }
+  cudaError_t e = cudaSuccess;
+  auto set = [&](auto kernel, int bytes) {
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  };
+  set(norm_fwd_rows_kernel<T, VEC, kSub>, fwd_most);
+  set(norm_fwd_rows_kernel<T, VEC, kCta>, fwd_most);
+  set(norm_fwd_rows_kernel<T, VEC, kCluster>, fwd_most);
+  set(norm_bwd_rows_kernel<T, VEC, kSub, 4>, bwd_most);
+  set(norm_bwd_rows_kernel<T, VEC, kCta, 0>, bwd_most);
+  set(norm_bwd_rows_kernel<T, VEC, kCta, 1>, bwd_most);
+  set(norm_bwd_rows_kernel<T, VEC, kCta, 2>, bwd_most);
+  set(norm_bwd_rows_kernel<T, VEC, kCta, 3>, bwd_most);
+  set(norm_bwd_rows_kernel<T, VEC, kCluster, 4>, bwd_most);
+  return e;
+}
+
 }  // namespace
+
+cudaError_t block_norm_configure() {
+  for (auto one : {configure<float, true>, configure<float, false>, configure<__nv_bfloat16, true>, configure<__nv_bfloat16, false>,
+                   configure<__half, true>, configure<__half, false>}) {
+    const cudaError_t e = one();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 // Units whose sums a CTA adds up itself: its own where there are many units in
 // all (fewer are added up sooner by norm_bwd_sums_kernel alone: 3 us at two a CTA).

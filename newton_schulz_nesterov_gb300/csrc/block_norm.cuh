@@ -48,6 +48,8 @@ struct NormBwdArgs {
   float* part_gate;                           // [groups * chunks_per_group][cols] (several chunks a group)
 };
 
+// Before the launches.
+cudaError_t block_norm_configure();
 // kept: what is asked of the device once, eight integers of the handle, 0 at first.
 cudaError_t launch_norm_fwd(const NormFwdArgs& a, int dtype, int sms, int* kept, cudaStream_t s);
 cudaError_t launch_norm_bwd(const NormBwdArgs& a, int dtype, cudaStream_t s);

@@ -131,6 +131,7 @@ struct dmuon_ctx {
   void* op_ws = nullptr;
   size_t op_ws_cap = 0;
   int norm_places[8] = {};
+  bool quant_ready = false, norm_ready = false;  // the kernels' limits of shared memory are set
   bool op_ws_captured = false;         // a graph holds op_ws: it stays until the handle goes
   std::vector<void*> op_ws_kept;
 };

@@ -64,6 +64,8 @@ struct MxGemmArgs {
 
 cudaError_t launch_mx_quant(const MxQuantArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_mx_dequant(const MxDequantArgs& a, int dtype, cudaStream_t s);
+// Before the launches.
+cudaError_t mx_quant_configure();
 cudaError_t mx_gemm_configure();
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, int nt, int split, cudaStream_t s);
 cudaError_t launch_mx_gemm_pair(const MxGemmArgs& a, int pairs, cudaStream_t s);

@@ -515,13 +515,21 @@ __global__ void __launch_bounds__(256) mx_dequant_kernel(const MxDequantArgs a, 
   }
 }
 
+// whole: rows are loaded by whole chunks, without the last pieces around them.
+template <typename T, bool NOISE>
+constexpr int quant_bytes(bool whole) {
+  return 2 * kMxScaleTile + kTile * kTile * ((int)sizeof(T) + (NOISE ? 1 : 0)) + (whole ? 0 : 2 * kTile * 16);
+}
+// The limit belongs to the kernel on its device, not to a call: set once, to the larger.
+template <typename T, bool NOISE>
+cudaError_t configure_quant() {
+  return cudaFuncSetAttribute(mx_quant_kernel<T, NOISE>, cudaFuncAttributeMaxDynamicSharedMemorySize, quant_bytes<T, NOISE>(false));
+}
+
 template <typename T, bool NOISE>
 cudaError_t launch_quant_one(const MxQuantArgs& a, cudaStream_t s) {
   const int64_t tiles = (a.rows + kTile - 1) / kTile * ((a.cols + kTile - 1) / kTile);
-  const bool whole = (sizeof(T) == 4 || a.vec) && (!NOISE || a.noise_vec);
-  const int smem = 2 * kMxScaleTile + kTile * kTile * ((int)sizeof(T) + (NOISE ? 1 : 0)) + (whole ? 0 : 2 * kTile * 16);
-  const cudaError_t e = cudaFuncSetAttribute(mx_quant_kernel<T, NOISE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
+  const int smem = quant_bytes<T, NOISE>((sizeof(T) == 4 || a.vec) && (!NOISE || a.noise_vec));
   mx_quant_kernel<T, NOISE><<<(unsigned)tiles, kQThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
@@ -542,6 +550,15 @@ cudaError_t launch_dequant(const MxDequantArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+cudaError_t mx_quant_configure() {
+  for (auto one : {configure_quant<float, true>, configure_quant<float, false>, configure_quant<__nv_bfloat16, true>,
+                   configure_quant<__nv_bfloat16, false>, configure_quant<__half, true>, configure_quant<__half, false>}) {
+    const cudaError_t e = one();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
 
 cudaError_t launch_mx_quant(const MxQuantArgs& a, int dtype, cudaStream_t s) {
   if (dtype == DMUON_BF16) return launch_quant<__nv_bfloat16>(a, s);
