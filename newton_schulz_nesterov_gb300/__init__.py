@@ -255,9 +255,14 @@ def dmuon_error_string(code):
     return load().dmuon_error_string(int(code)).decode()
 
 
+class _RawHandle(ctypes.c_void_p):
+    """A dmuon handle that knows its device."""
+
+
 def dmuon_create(device=0):
-    h = ctypes.c_void_p()
+    h = _RawHandle()
     _check(load().dmuon_create(ctypes.byref(h), int(device)), "dmuon_create")
+    h.device = int(device)
     return h
 
 
@@ -469,13 +474,23 @@ def dmuon_clip_grad_norm(h, grads, max_norm, buckets=None, n_buckets=None, stats
 
 # ------------------------------------------- 4-bit projections and their norms
 
-def _matrix(t, name, dtype=None, shape=None):
-    """(pointer, leading dimension, type code, shape) of a 2-D CUDA tensor whose
-    rows are contiguous; ``dtype`` and ``shape``, where given, have to match."""
+def _device(h, t, name):
+    """Index of the handle's device, on which every tensor of a call has to be
+    (the first tensor's, for a handle that does not tell)."""
+    index = t.get_device()
+    if index < 0 or getattr(h, "device", index) != index:
+        raise ValueError("%s: a CUDA tensor on the handle's device is wanted" % name)
+    return index
+
+
+def _matrix(t, name, index, dtype=None, shape=None):
+    """(pointer, leading dimension, type code, shape) of a 2-D tensor on the
+    device ``index`` whose rows are contiguous; ``dtype`` and ``shape``, where
+    given, have to match."""
     code = (_TYPES or _types()).get(t.dtype, 3)
     size = t.shape
-    if code > 2 or not t.is_cuda or len(size) != 2 or (dtype is not None and code != dtype):
-        raise ValueError("%s: a 2-D CUDA tensor of float32, bfloat16 or float16%s is wanted"
+    if code > 2 or t.get_device() != index or len(size) != 2 or (dtype is not None and code != dtype):
+        raise ValueError("%s: a 2-D tensor of float32, bfloat16 or float16%s on the handle's device is wanted"
                          % (name, "" if dtype is None else " (the type of the others)"))
     if shape is not None and size != shape:
         raise ValueError("%s: shape %s, %s wanted" % (name, tuple(size), tuple(shape)))
@@ -491,34 +506,34 @@ def _pitch(t, size, name):
 
 
 def _like(t, name, first):
-    """(pointer, leading dimension) of a matrix of the type, type code and shape
-    ``first``; None gives (0, 0)."""
+    """(pointer, leading dimension) of a matrix of the device, type, type code
+    and shape ``first``; None gives (0, 0)."""
     if t is None:
         return 0, 0
-    dtype, code, size = first
-    if t.dtype is dtype and t.shape == size and t.is_cuda and t.is_contiguous():
+    index, dtype, code, size = first
+    if t.dtype is dtype and t.shape == size and t.get_device() == index and t.is_contiguous():
         return t.data_ptr(), size[1]
-    return _matrix(t, name, code, size)[:2]
+    return _matrix(t, name, index, code, size)[:2]
 
 
-def _floats(t, name, shape):
-    """Pointer of a contiguous fp32 CUDA tensor of ``shape``; None gives 0."""
+def _floats(t, name, index, shape):
+    """Pointer of a contiguous fp32 tensor of ``shape`` on the device; None gives 0."""
     if t is None:
         return 0
-    if (_TYPES or _types()).get(t.dtype) != 0 or not t.is_cuda or t.shape != shape or not t.is_contiguous():
-        raise ValueError("%s: a contiguous float32 CUDA tensor of shape %s is wanted" % (name, tuple(shape)))
+    if (_TYPES or _types()).get(t.dtype) != 0 or t.get_device() != index or t.shape != shape or not t.is_contiguous():
+        raise ValueError("%s: a contiguous float32 tensor of shape %s on the handle's device is wanted" % (name, tuple(shape)))
     return t.data_ptr()
 
 
-def _mxfp4(q, name, rows, k):
+def _mxfp4(q, name, index, rows, k):
     """(data pointer, scales pointer) of an MXFP4 matrix (data, scales)."""
     data, scales = q
     nb = -(-k // 32)
     types = _TYPES or _types()
     if (types.get(data.dtype) != 3 or types.get(scales.dtype) != 3 or data.numel() != rows * nb * 16 or
-            scales.numel() != -(-rows // 128) * -(-nb // 4) * 512 or not data.is_cuda or not scales.is_cuda or
+            scales.numel() != -(-rows // 128) * -(-nb // 4) * 512 or data.get_device() != index or scales.get_device() != index or
             not data.is_contiguous() or not scales.is_contiguous()):
-        raise ValueError("%s: contiguous uint8 CUDA tensors of the sizes dmuon_mxfp4_empty(%d, %d) gives are wanted"
+        raise ValueError("%s: contiguous uint8 tensors of the sizes dmuon_mxfp4_empty(%d, %d) gives on the handle's device are wanted"
                          % (name, rows, k))
     return data.data_ptr(), scales.data_ptr()
 
@@ -526,8 +541,8 @@ def _mxfp4(q, name, rows, k):
 _raw_stream = None  # torch's current stream of a device as an integer
 
 
-def _stream_of(stream, t):
-    """Handle of ``stream``, or of the current stream of t's device."""
+def _stream_of(stream, index):
+    """Handle of ``stream``, or of the device's current stream."""
     global _raw_stream
     if stream is not None:
         return _stream_handle(stream)
@@ -535,7 +550,7 @@ def _stream_of(stream, t):
         import torch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda index: torch.cuda.current_stream(index).cuda_stream)
-    return _raw_stream(t.get_device())
+    return _raw_stream(index)
 
 
 def dmuon_mxfp4_bytes(rows, k):
@@ -557,30 +572,32 @@ def dmuon_mxfp4_quantize(h, src, by_rows=None, by_cols=None, noise=None, scale="
     """Quantise the matrix ``src`` [r, c] along its rows into ``by_rows`` (an
     r x c MXFP4 matrix) and / or along its columns into ``by_cols`` (c x r).
     ``noise``: uint8 [r, c] of random bytes for stochastic rounding."""
-    ptr, ld, code, size = _matrix(src, "src")
+    index = _device(h, src, "src")
+    ptr, ld, code, size = _matrix(src, "src", index)
     r, c = size
     nptr, nld = None, 0
     if noise is not None:
-        if not noise.is_cuda or (_TYPES or _types()).get(noise.dtype) != 3 or noise.shape != size:
-            raise ValueError("noise: a uint8 CUDA tensor of src's shape is wanted")
+        if noise.get_device() != index or (_TYPES or _types()).get(noise.dtype) != 3 or noise.shape != size:
+            raise ValueError("noise: a uint8 tensor of src's shape on the handle's device is wanted")
         nptr, nld = noise.data_ptr(), _pitch(noise, size, "noise")
-    rd, rs = (None, None) if by_rows is None else _mxfp4(by_rows, "by_rows", r, c)
-    cd, cs = (None, None) if by_cols is None else _mxfp4(by_cols, "by_cols", c, r)
+    rd, rs = (None, None) if by_rows is None else _mxfp4(by_rows, "by_rows", index, r, c)
+    cd, cs = (None, None) if by_cols is None else _mxfp4(by_cols, "by_cols", index, c, r)
     mode = SCALE_MODES[scale]
     if r == 0 or c == 0:
         return
-    rc = load().dmuon_mxfp4_quantize(h, ptr, code, r, c, ld, mode, nptr, nld, rd, rs, cd, cs, _stream_of(stream, src))
+    rc = load().dmuon_mxfp4_quantize(h, ptr, code, r, c, ld, mode, nptr, nld, rd, rs, cd, cs, _stream_of(stream, index))
     if rc:
         _check(rc, "dmuon_mxfp4_quantize", h)
 
 
 def dmuon_mxfp4_dequantize(h, q, out, stream=None):
     """The values of the MXFP4 matrix ``q`` into ``out`` [rows, k]."""
-    ptr, ld, code, (r, k) = _matrix(out, "out")
-    d, s = _mxfp4(q, "q", r, k)
+    index = _device(h, out, "out")
+    ptr, ld, code, (r, k) = _matrix(out, "out", index)
+    d, s = _mxfp4(q, "q", index, r, k)
     if r == 0 or k == 0:
         return
-    rc = load().dmuon_mxfp4_dequantize(h, d, s, r, k, ptr, code, ld, _stream_of(stream, out))
+    rc = load().dmuon_mxfp4_dequantize(h, d, s, r, k, ptr, code, ld, _stream_of(stream, index))
     if rc:
         _check(rc, "dmuon_mxfp4_dequantize", h)
 
@@ -588,21 +605,23 @@ def dmuon_mxfp4_dequantize(h, q, out, stream=None):
 def dmuon_mxfp4_gemm(h, a, b, out, k, alpha=1.0, beta=0.0, stream=None):
     """out = alpha * a b^T + beta * out of MXFP4 matrices a [m, k] and
     b [n, k]; out is [m, n] in float32, bfloat16 or float16."""
-    ptr, ld, code, (m, n) = _matrix(out, "out")
-    ad, as_ = _mxfp4(a, "a", m, k)
-    bd, bs = _mxfp4(b, "b", n, k)
+    index = _device(h, out, "out")
+    ptr, ld, code, (m, n) = _matrix(out, "out", index)
+    ad, as_ = _mxfp4(a, "a", index, m, k)
+    bd, bs = _mxfp4(b, "b", index, n, k)
     if m == 0 or n == 0:
         return
-    rc = load().dmuon_mxfp4_gemm(h, ad, as_, bd, bs, m, n, k, ptr, code, ld, alpha, beta, _stream_of(stream, out))
+    rc = load().dmuon_mxfp4_gemm(h, ad, as_, bd, bs, m, n, k, ptr, code, ld, alpha, beta, _stream_of(stream, index))
     if rc:
         _check(rc, "dmuon_mxfp4_gemm", h)
 
 
-def _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, eps, out):
+def _block_norm(h, x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, eps, out):
     """The fields that forward and backward share; x and out may be None."""
-    fp, ldf, code, shape = _matrix(f, "f")
+    index = _device(h, f, "f")
+    fp, ldf, code, shape = _matrix(f, "f", index)
     rows, cols = shape
-    first = f.dtype, code, shape
+    first = index, f.dtype, code, shape
     xp, ldx = _like(x, "x", first)
     yp, ldy = _like(y, "y", first)
     hp, ldh = _like(out, "out", first)
@@ -610,9 +629,9 @@ def _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, ep
     if per < 1:
         raise ValueError("rows_per_gate must be at least 1")
     line = (cols,)
-    packed = _NORM.pack(rows, cols, code, eps, xp, ldx, fp, ldf, _floats(post_w, "post_w", line), _floats(pre_w, "pre_w", line),
-                        _floats(gate, "gate", (-(-rows // per), cols)), per, _floats(res_scale, "res_scale", line), yp, ldy,
-                        hp, ldh, _floats(rstd, "rstd", (2, rows)))
+    packed = _NORM.pack(rows, cols, code, eps, xp, ldx, fp, ldf, _floats(post_w, "post_w", index, line),
+                        _floats(pre_w, "pre_w", index, line), _floats(gate, "gate", index, (-(-rows // per), cols)), per,
+                        _floats(res_scale, "res_scale", index, line), yp, ldy, hp, ldh, _floats(rstd, "rstd", index, (2, rows)))
     return BlockNorm.from_buffer_copy(packed), first
 
 
@@ -621,8 +640,8 @@ def dmuon_block_norm_forward(h, x, f, post_w, pre_w, y, out, rstd, gate=None, ro
     """y = res_scale * x + gate * rms(f) * post_w and out = rms(y) * pre_w over
     the rows of x and f [rows, cols]; rstd [2, rows] is what the backward needs.
     ``gate`` [ceil(rows / rows_per_gate), cols] (rows_per_gate None: one row for all)."""
-    p, _ = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, eps, out)
-    rc = load().dmuon_block_norm_forward(h, p, _stream_of(stream, f))
+    p, first = _block_norm(h, x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, eps, out)
+    rc = load().dmuon_block_norm_forward(h, p, _stream_of(stream, first[0]))
     if rc:
         _check(rc, "dmuon_block_norm_forward", h)
 
@@ -631,15 +650,15 @@ def dmuon_block_norm_backward(h, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d
                               d_gate=None, rows_per_gate=None, res_scale=None, d_res_scale=None, stream=None):
     """Gradients of dmuon_block_norm_forward from dh (of its out) and dy (of y,
     None = 0).  x may be None unless d_res_scale is wanted."""
-    p, first = _block_norm(x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, 0.0, None)
+    p, first = _block_norm(h, x, f, y, post_w, pre_w, rstd, gate, rows_per_gate, res_scale, 0.0, None)
     if d_gate is not None and gate is None:
         raise ValueError("d_gate without a gate")
-    line = (first[2][1],)
+    index, line = first[0], (first[3][1],)
     q = BlockNormGrad.from_buffer_copy(_NORM_GRAD.pack(
         *_like(dy, "dy", first), *_like(dh, "dh", first), *_like(dx, "dx", first), *_like(df, "df", first),
-        _floats(d_post_w, "d_post_w", line), _floats(d_pre_w, "d_pre_w", line),
-        0 if d_gate is None else _floats(d_gate, "d_gate", gate.shape), _floats(d_res_scale, "d_res_scale", line)))
-    rc = load().dmuon_block_norm_backward(h, p, q, _stream_of(stream, f))
+        _floats(d_post_w, "d_post_w", index, line), _floats(d_pre_w, "d_pre_w", index, line),
+        0 if d_gate is None else _floats(d_gate, "d_gate", index, gate.shape), _floats(d_res_scale, "d_res_scale", index, line)))
+    rc = load().dmuon_block_norm_backward(h, p, q, _stream_of(stream, first[0]))
     if rc:
         _check(rc, "dmuon_block_norm_backward", h)
 
