@@ -359,7 +359,8 @@ int dmuon_mxfp4_dequantize(dmuon_handle_t h, const void* data,
  * m x n of `dtype`, leading dimension ldd >= n elements.  fp32 accumulation,
  * one rounding at the store; beta == 0 does not read D.  DMUON_F32 with
  * beta = 1 accumulates a weight gradient that dmuon_step takes as G.  Any
- * m, n >= 0 (0 returns DMUON_OK), k >= 1.  The same inputs give the same bits.
+ * m, n >= 0 (0 returns DMUON_OK), k >= 1 (a sum over no rows, beta D, is the
+ * product of zero matrices with k = 32).  The same inputs give the same bits.
  * A wait that runs out inside the kernel is reported by dmuon_get_status as
  * DMUON_ERR_TIMEOUT.
  */

@@ -602,16 +602,34 @@ def dmuon_mxfp4_dequantize(h, q, out, stream=None):
         _check(rc, "dmuon_mxfp4_dequantize", h)
 
 
+def _zero_block(rows, stream, index):
+    """A zero MXFP4 matrix of one block of columns: buffers of the stream (raw
+    handle), which an empty sum is taken over since the library wants k >= 1."""
+    import contextlib
+    import torch
+    d, s = dmuon_mxfp4_bytes(rows, 32)
+    here = torch.cuda.current_stream(index)
+    on = contextlib.nullcontext() if here.cuda_stream == stream else torch.cuda.stream(torch.cuda.ExternalStream(stream, index))
+    with on:
+        buf = torch.zeros(d + s, dtype=torch.uint8, device="cuda:%d" % index)
+    return buf, buf.data_ptr(), buf.data_ptr() + d
+
+
 def dmuon_mxfp4_gemm(h, a, b, out, k, alpha=1.0, beta=0.0, stream=None):
     """out = alpha * a b^T + beta * out of MXFP4 matrices a [m, k] and
-    b [n, k]; out is [m, n] in float32, bfloat16 or float16."""
+    b [n, k]; out is [m, n] in float32, bfloat16 or float16.  k = 0, a sum over
+    no rows, gives beta * out."""
     index = _device(h, out, "out")
     ptr, ld, code, (m, n) = _matrix(out, "out", index)
     ad, as_ = _mxfp4(a, "a", index, m, k)
     bd, bs = _mxfp4(b, "b", index, n, k)
     if m == 0 or n == 0:
         return
-    rc = load().dmuon_mxfp4_gemm(h, ad, as_, bd, bs, m, n, k, ptr, code, ld, alpha, beta, _stream_of(stream, index))
+    stream = _stream_of(stream, index)
+    if k == 0:
+        zeros, ad, as_ = _zero_block(max(m, n), stream, index)
+        bd, bs, k = ad, as_, 32
+    rc = load().dmuon_mxfp4_gemm(h, ad, as_, bd, bs, m, n, k, ptr, code, ld, alpha, beta, stream)
     if rc:
         _check(rc, "dmuon_mxfp4_gemm", h)
 
