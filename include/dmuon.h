@@ -348,8 +348,11 @@ int dmuon_mxfp4_quantize(dmuon_handle_t h, const void* src, int dtype,
                          void* col_data, void* col_scales, void* stream);
 
 /* The values of a rows x k MXFP4 matrix into dst (device, `dtype`, leading
- * dimension ld >= k elements): exact in fp32 and bf16, rounded to nearest in
- * fp16 where 2^e is outside its range. */
+ * dimension ld >= k elements): exact in fp32 and bf16 up to these types' range
+ * and rounded to nearest in fp16.  A value past a type's range reads as Inf: in
+ * fp32 and bf16 magnitudes of 4 or 6 under byte 253 and of 2 or more under byte
+ * 254, which the format allows (the quantiser writes 253 in CEIL mode, for a
+ * block whose largest magnitude is above 1.5 * 2^127). */
 int dmuon_mxfp4_dequantize(dmuon_handle_t h, const void* data,
                            const void* scales, int64_t rows, int64_t k,
                            void* dst, int dtype, int64_t ld, void* stream);

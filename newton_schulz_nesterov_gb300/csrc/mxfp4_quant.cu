@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(kQThreads, sizeof(T) == 4 ? 2 : 4) mx_quant_ke
 
 // A code as fp32 is sign, two exponent bits and one mantissa bit moved to
 // fp32's places and scaled by 2^126 (code 1, 0.5, is then a subnormal times
-// 2^126); the product with the block's 2^e is exact.
+// 2^126); the product with the block's 2^e is exact, or Inf past fp32's range
+// (4 or 6 times 2^126, 2 or more times 2^127).
 __device__ __forceinline__ float code_value(uint32_t code, float scale) {
   const float v = __uint_as_float(((code & 8u) << 28) | ((code & 7u) << 22)) * 8.507059173023462e37f;
   return v * scale;
