@@ -475,11 +475,14 @@ def dmuon_clip_grad_norm(h, grads, max_norm, buckets=None, n_buckets=None, stats
 # ------------------------------------------- 4-bit projections and their norms
 
 def _device(h, t, name):
-    """Index of the handle's device, on which every tensor of a call has to be
-    (the first tensor's, for a handle that does not tell)."""
-    index = t.get_device()
-    if index < 0 or getattr(h, "device", index) != index:
-        raise ValueError("%s: a CUDA tensor on the handle's device is wanted" % name)
+    """Index of the handle's device, on which every tensor of a call has to be;
+    that of ``t``, the first one, for a handle that does not tell."""
+    try:
+        return h.device
+    except AttributeError:
+        index = t.get_device()
+    if index < 0:
+        raise ValueError("%s: a CUDA tensor is wanted" % name)
     return index
 
 
