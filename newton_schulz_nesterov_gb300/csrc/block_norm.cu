@@ -62,6 +62,8 @@ __device__ __forceinline__ __half narrow<__half>(float v) { return __float2half_
 // (16384 x 4095 bf16 backward 290 us one by one, 232 so; 65535 x 255 182 and
 // 84).  The forward is no faster that way (16384 x 4095 bf16 134 us
 // against 128, and 4.4 against 3.3 at 300 x 501).
+// Rows on any element cost registers: 12 of their 27 instances spill, the worst
+// (fp32 backward of rows that share a warp) 208 bytes of stores and 304 of loads.
 constexpr int V = 2;                             // chunks of eight columns a thread
 constexpr int kFwdThreads = 512, kBwdThreads = 256;  // of an SM: 128 and 255 registers a thread
 constexpr int kMaxCluster = 8;
@@ -1072,9 +1074,10 @@ __device__ __forceinline__ void add4(float4& s, const float4& v) {
 // eight loads in flight, then the 32 in a fixed order.  Groups of few chunks
 // have a warp each and 128 columns: 30000 x 100 fp32, 1875 groups of two, 53 us
 // in all where a block each took 67; 60000 x 64, 60 of 81 chunks, 43 with warps
-// and 26 with blocks.  Launched while the rows kernel runs: what it reads is
-// there after the wait (launched after it, eight rows at a time, 1.1 us more at
-// 1000 x 1111).
+// and 26 with blocks.  Launched as a programmatic dependent of the rows kernel,
+// whose end is what starts it (nothing triggers it earlier): the gap between two
+// launches is saved, and what it reads is there after the wait (an ordinary
+// launch, eight rows at a time, 1.1 us more at 1000 x 1111).
 __host__ __device__ __forceinline__ bool warp_a_group(const NormBwdArgs& a) { return a.chunks_per_group <= 16; }
 __global__ void __launch_bounds__(256) norm_bwd_sums_kernel(const NormBwdArgs a) {
   __shared__ float red[32][33];

@@ -1,4 +1,5 @@
-// Bounded mbarrier waits of the MXFP4 product kernels: a wait without
+// Bounded mbarrier waits of the MXFP4 product kernels (the Newton-Schulz
+// kernels have their own, and take the drains): a wait without
 // progress for `limit_ns` sets the CTA's abort flag, records bit 0 of *err and
 // gives up; the other roles of the CTA see the flag in their own waits.
 //

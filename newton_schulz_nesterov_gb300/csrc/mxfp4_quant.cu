@@ -16,8 +16,8 @@
 // one block of two adjacent columns), and each direction's scale bytes of the
 // tile are exactly one 512-byte scale tile.  Both directions write 64
 // contiguous bytes per row.  Bound by HBM without noise (14336 x 4096 fp32 in
-// both directions 54 us, 5.5 TB/s; 16384 x 14336 bf16 136 us, 5.3 TB/s), by
-// the ALU pipe with it (220 us, 4.3 TB/s).
+// both directions 54 us, 5.5 TB/s; 16384 x 14336 bf16 134 us, 5.4 TB/s), by
+// the ALU pipe with it (214 us, 4.5 TB/s).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -71,7 +71,10 @@ __device__ __forceinline__ uint32_t codes_nearest(const float (&f)[8]) {
 // Scaling rounds up: a value that is not representable stays on its side of
 // every threshold.  In float arithmetic (nineteen instructions an element)
 // quantising 16384 x 14336 bf16 in both directions with noise took 403 us,
-// this 220; byte permutes and logic then fill 82 % of the ALU pipe's slots.
+// this 214; byte permutes and logic then fill 77 % of the ALU pipe's slots.
+// cvt.rs.satfinite.e2m1x4.f32 takes four elements and a word of random bits; its
+// rule for these bits would take the place of the header's byte an element, and
+// it has not been measured.
 constexpr float kTiny = 1.1754943508222875e-38f;  // 2^-126
 
 // 4 bits - threshold of an element: its code is the top byte (8 only for a
