@@ -640,6 +640,11 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile uint32_t* peer_gave_up = tmem_slot + 2;  // the peer stores both before the roles' last barrier
   volatile uint32_t* peer_issued = tmem_slot + 3;
+  // Stages that warp 0 loads and warp 1 multiplies, for the drains only: kept
+  // here, since two more registers live through the kernel cost its epilogue
+  // 1 to 2 % (16384 x 8191 x 512 bf16 with beta = 1 466 -> 472 us).
+  volatile uint32_t* loaded = tmem_slot + 4;
+  volatile uint32_t* multiplied = tmem_slot + 5;
 
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint64_t tmo = a.timeout_ns ? a.timeout_ns : kWaitNs;
@@ -665,6 +670,8 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
     ptx::mbar_init(ptx::smem_addr(drain), 1);
     *abort_flag = 0;
     *peer_gave_up = 0;
+    *loaded = 0;
+    *multiplied = 0;
     ptx::fence_mbar_init();
   }
   if (warp == 1) {
@@ -676,14 +683,13 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   ptx::cluster_sync();  // both ranks' barriers exist before any remote signal
   ptx::tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  uint32_t issued = 0;  // warp 0: stages that are being loaded; warp 1: being multiplied
-  const bool elected = elect_one();
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
+    const bool elected = elect_one();
     const uint32_t full0 = ptx::smem_addr(full), remote = ptx::mapa_shared(full0, 0), ready0 = ptx::smem_addr(sready);
     const uint32_t empty0 = ptx::smem_addr(empty), stage0 = ptx::smem_addr(stages);
-    uint32_t s = 0, ph = 0;
+    uint32_t s = 0, ph = 0, issued = 0;
     bool ok = true;
     for (int t = pair; ok && t < tiles; t += npairs) {
       int mt, nt;
@@ -704,13 +710,17 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
         if (++s == kPairN) { s = 0; ph ^= 1u; }
       }
     }
-    if (!leader && lane == 0) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(tmem_slot + 3), 0), issued);
+    if (lane == 0) {
+      *loaded = issued;
+      if (!leader) ptx::st_cluster(ptx::mapa_shared(ptx::smem_addr(tmem_slot + 3), 0), issued);
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
     if (leader) {
+      const bool elected = elect_one();
       const uint32_t full0 = ptx::smem_addr(full), empty0 = ptx::smem_addr(empty), sfull0 = ptx::smem_addr(sfull);
       const uint32_t desc0 = desc_lo(ptx::smem_addr(stages));
-      uint32_t s = 0, ph = 0, set = 0, sph = 0, tc = 0;
+      uint32_t s = 0, ph = 0, set = 0, sph = 0, tc = 0, issued = 0;
       bool ok = true;
       for (int t = pair; ok && t < tiles; t += npairs, ++tc) {
         const uint32_t acc = tc & 1u;
@@ -738,6 +748,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
           if (++set == kPairSets) { set = 0; sph ^= 1u; }
         }
       }
+      if (lane == 0) *multiplied = issued;
     }
   } else if (warp >= 6) {
     // ------------------------------------------------------------ scales
@@ -818,12 +829,12 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
   ptx::cluster_sync();  // no rank frees tensor memory or exits while its pair is busy
   if (*abort_flag || *peer_gave_up) {  // nor while its copies or products are in flight
     if (warp == 0 && lane == 0) {
-      drain_stages(ptx::smem_addr(sready), kPairN, issued, abort_flag, a.err);
+      drain_stages(ptx::smem_addr(sready), kPairN, *loaded, abort_flag, a.err);
       if (leader)
-        drain_pair_stages(ptx::smem_addr(full), kPairN, issued, *peer_issued, 2 * kPBytes, abort_flag, a.err);
+        drain_pair_stages(ptx::smem_addr(full), kPairN, *loaded, *peer_issued, 2 * kPBytes, abort_flag, a.err);
     }
-    if (warp == 1 && issued) {
-      if (elected) ptx::mma_commit_pair(ptx::smem_addr(drain));
+    if (warp == 1 && *multiplied) {
+      if (elect_one()) ptx::mma_commit_pair(ptx::smem_addr(drain));
       bounded_wait_slow(ptx::smem_addr(drain), 0, abort_flag, a.err, false, kWaitNs);
     }
     __syncthreads();
