@@ -431,12 +431,152 @@ int dmuon_block_norm_backward(dmuon_handle_t h, const dmuon_block_norm_t* p,
                               const dmuon_block_norm_grad_t* q, void* stream);
 
 /*
+ * MXFP8 matrices: as the MXFP4 ones above with E4M3 elements (largest 448), a
+ * byte each: data of pitch 32 * ceil(k / 32) bytes, elements past k zero; scales
+ * laid out alike.  dmuon_mxfp8_quantize is dmuon_mxfp4_quantize without noise, to
+ * the nearest code, ties to the even one; scale modes: FLOOR floor(log2 amax) - 8
+ * (values above 448 * 2^e saturate), CEIL the least e with amax <= 448 * 2^e.
+ * Reading back is exact in fp32 and bf16 up to these types' range and rounds to
+ * nearest in fp16.
+ */
+int dmuon_mxfp8_bytes(int64_t rows, int64_t k, size_t* data_bytes,
+                      size_t* scale_bytes);
+int dmuon_mxfp8_quantize(dmuon_handle_t h, const void* src, int dtype,
+                         int64_t rows, int64_t cols, int64_t ld,
+                         int scale_mode, void* row_data, void* row_scales,
+                         void* col_data, void* col_scales, void* stream);
+int dmuon_mxfp8_dequantize(dmuon_handle_t h, const void* data,
+                           const void* scales, int64_t rows, int64_t k,
+                           void* dst, int dtype, int64_t ld, void* stream);
+
+/* Activations of a projection's epilogue. */
+#define DMUON_ACT_NONE      0
+#define DMUON_ACT_RELU      1  /* slope 0 at 0; where z <= 0 a gradient is 0
+                                * even if it was Inf or NaN                   */
+#define DMUON_ACT_SILU      2  /* z / (1 + exp(-z))                           */
+#define DMUON_ACT_GELU      3  /* z * Phi(z), Phi the normal distribution     */
+#define DMUON_ACT_GELU_TANH 4  /* z/2 (1 + tanh(sqrt(2/pi)(z + 0.044715 z^3)))*/
+
+/*
+ * A projection with its epilogue:
+ *   z = alpha * A B^T + bias,   D = act(z) + beta * C,   pre = z
+ * A m x k and B n x k in MXFP4 or MXFP8 (bits: of both), D, C and pre m x n of
+ * `dtype`.  Everything is fp32 up to one rounding at each store; D comes from z
+ * before it is rounded.  Sizes, leading dimensions, determinism and waits as in
+ * dmuon_mxfp4_gemm.
+ */
+typedef struct {
+    int64_t m, n, k;
+    int     bits;            /* 4 or 8                                     */
+    int     dtype;           /* of D, C and pre                            */
+    const void *a_data, *a_scales, *b_data, *b_scales;
+    float   alpha, beta;
+    const float* bias;       /* n, or NULL (0)                             */
+    int     act;             /* DMUON_ACT_*                                */
+    const void* c;   int64_t ldc;   /* or NULL (0); may be d, with its ldd */
+    void*       pre; int64_t ldpre; /* or NULL: what dmuon_act_backward
+                                     * needs                               */
+    void*       d;   int64_t ldd;
+} dmuon_mx_linear_t;
+
+int dmuon_mx_linear(dmuon_handle_t h, const dmuon_mx_linear_t* p, void* stream);
+
+/*
+ * Backward of the bias and activation: dz = dout * act'(pre), rounded once to
+ * `dtype` into dz and / or quantised (from fp32) to MXFP8 by rows and / or
+ * columns for the two gradient products, and its column sums, the bias's
+ * gradient.  NULL for what is not wanted.  Column sums run in a fixed order: the
+ * same inputs give the same bits.  rows == 0 writes a zero d_bias.  Workspace for
+ * d_bias as in dmuon_block_norm_backward.
+ */
+typedef struct {
+    int64_t rows, cols;
+    int     dtype;           /* of dout, pre and dz                        */
+    int     act;             /* DMUON_ACT_*                                */
+    const void* dout; int64_t lddout;
+    const void* pre;  int64_t ldpre;  /* not read for DMUON_ACT_NONE       */
+    void*   dz;       int64_t lddz;
+    float*  d_bias;          /* cols; written, not added                   */
+    int     scale_mode;      /* DMUON_MXFP4_SCALE_*                        */
+    void *row_data, *row_scales, *col_data, *col_scales;
+} dmuon_act_backward_t;
+
+int dmuon_act_backward(dmuon_handle_t h, const dmuon_act_backward_t* p,
+                       void* stream);
+
+/*
+ * Dropout is a function of (p, seed, offset, row, column): no mask is stored, and
+ * the same call on a gradient is the backward pass.  An element stays when its 16
+ * random bits are at least cut = round(65536 p), and is then multiplied by
+ * 65536 / (65536 - cut); else it is 0.  p in [0, 1) with cut < 65536; p below
+ * 2^-17 keeps everything.  The bits are those of Philox4x32-10 with key `seed` and
+ * counter (column / 8, row, low and high word of offset): column 8 g + 2 j has the
+ * low, 8 g + 2 j + 1 the high half of word j.  Callers give each use of one seed
+ * an offset of its own.
+ *
+ *   out = dropout(x) (+ residual)     rows x cols of `dtype`
+ *
+ * residual NULL: 0.  out may be x or residual, with its leading dimension.
+ */
+int dmuon_dropout(dmuon_handle_t h, const void* x, int dtype, int64_t rows,
+                  int64_t cols, int64_t ldx, const void* residual,
+                  int64_t ldres, void* out, int64_t ldout, float p,
+                  uint64_t seed, uint64_t offset, void* stream);
+
+/*
+ * The norm of a residual stream to which a block's output is added through
+ * dropout.  Per row:
+ *   y = x + dropout(f),   h = rms(y) * w,   rms(v) = v / sqrt(mean(v^2) + eps)
+ * y (the next residual stream) is rounded once to `dtype`; h comes from y before
+ * its rounding and goes to `dtype` (h) and / or, from fp32, to MXFP8 by rows (q),
+ * which the next projection takes.  Matrices as in dmuon_block_norm_forward.
+ */
+typedef struct {
+    int64_t rows, cols;
+    int     dtype;           /* of x, f, y, h and their gradients          */
+    float   eps;
+    const void* x;  int64_t ldx;    /* or NULL (0)                         */
+    const void* f;  int64_t ldf;
+    const float* w;                 /* cols                                */
+    void* y;        int64_t ldy;
+    void* h;        int64_t ldh;    /* or NULL                             */
+    void *q_data, *q_scales;        /* or NULLs                            */
+    int   scale_mode;               /* of q: DMUON_MXFP4_SCALE_*           */
+    float p;                        /* of dropout                          */
+    uint64_t seed, offset;
+    float* rstd;                    /* rows: 1 / sqrt(mean(y^2) + eps),
+                                     * what the backward needs             */
+} dmuon_add_norm_t;
+
+int dmuon_add_norm_forward(dmuon_handle_t h, const dmuon_add_norm_t* p,
+                           void* stream);
+
+/*
+ * Its backward: from dh (gradient of h; of the values before their quantisation
+ * where h went to MXFP8) and dy (gradient of y from its other uses, NULL = 0) the
+ * gradients of x, of f and, in fp32, of w (written, not added; in a fixed order).
+ * Takes p's y, w, rstd, p, seed and offset.  dx NULL: not wanted (without dropout
+ * it is df).  rows == 0 writes a zero d_w.  Workspace as in
+ * dmuon_block_norm_backward.
+ */
+typedef struct {
+    const void* dy; int64_t lddy;
+    const void* dh; int64_t lddh;
+    void* dx;       int64_t lddx;
+    void* df;       int64_t lddf;
+    float* d_w;
+} dmuon_add_norm_grad_t;
+
+int dmuon_add_norm_backward(dmuon_handle_t h, const dmuon_add_norm_t* p,
+                            const dmuon_add_norm_grad_t* q, void* stream);
+
+/*
  * Wait for the handle's stream work to finish and report what the kernels
  * recorded since the previous call of this function: per-matrix flags of
  * the last planned list (bit 0: non-finite input) are copied to
  * flags[0..min(n_flags, n_mats)) when flags != NULL, then cleared.
  * Returns DMUON_ERR_TIMEOUT if a kernel's bounded wait ran out (those of
- * dmuon_mxfp4_gemm and of the block norms too), DMUON_ERR_NONFINITE if any flag is set, DMUON_OK otherwise.
+ * dmuon_mxfp4_gemm, dmuon_mx_linear and of the block norms too), DMUON_ERR_NONFINITE if any flag is set, DMUON_OK otherwise.
  */
 int dmuon_get_status(dmuon_handle_t h, int* flags, int n_flags);
 
@@ -566,7 +706,11 @@ int64_t dmuon_launch_count(dmuon_handle_t h);
 #define DMUON_KIND_MX_GEMM       14
 #define DMUON_KIND_NORM_FWD      15
 #define DMUON_KIND_NORM_BWD      16  /* both launches                      */
-#define DMUON_NUM_KINDS     17
+#define DMUON_KIND_ACT_BWD       17  /* with its column sums               */
+#define DMUON_KIND_ADD_NORM_FWD  18
+#define DMUON_KIND_ADD_NORM_BWD  19  /* both launches                      */
+#define DMUON_KIND_DROPOUT       20
+#define DMUON_NUM_KINDS     21
 int dmuon_profile_enable(dmuon_handle_t h, int on);
 int dmuon_profile_read(dmuon_handle_t h, double* ms, int64_t* count,
                        int n_kinds);

@@ -23,6 +23,8 @@ __all__ = [
     "dmuon_plan_preview",
     "dmuon_mxfp4_bytes", "dmuon_mxfp4_empty", "dmuon_mxfp4_quantize", "dmuon_mxfp4_dequantize", "dmuon_mxfp4_gemm",
     "dmuon_block_norm_forward", "dmuon_block_norm_backward",
+    "dmuon_mxfp8_bytes", "dmuon_mxfp8_empty", "dmuon_mxfp8_quantize", "dmuon_mxfp8_dequantize", "dmuon_mx_linear",
+    "dmuon_act_backward", "dmuon_add_norm_forward", "dmuon_add_norm_backward", "dmuon_dropout", "ACTIVATIONS",
     "dmuon_launch_count", "dmuon_last_error", "dmuon_profile_enable", "dmuon_profile_read",
     "dmuon_plan_summary", "dmuon_error_string", "dmuon_version", "Handle",
     "KIND_NAMES", "STATUS",
@@ -38,7 +40,8 @@ STATUS = {
     -7: "DMUON_ERR_UNSUPPORTED",
 }
 KIND_NAMES = ("momentum", "finalize", "gram", "gram2", "apply", "update0", "adamw", "clip", "small",
-              "gs_gram", "gs_prod", "ns_fused", "mx_quantize", "mx_dequantize", "mx_gemm", "norm_fwd", "norm_bwd")
+              "gs_gram", "gs_prod", "ns_fused", "mx_quantize", "mx_dequantize", "mx_gemm", "norm_fwd", "norm_bwd",
+              "act_bwd", "add_norm_fwd", "add_norm_bwd", "dropout")
 
 
 class DmuonError(RuntimeError):
@@ -77,14 +80,51 @@ class BlockNormGrad(ctypes.Structure):
                 ("d_res_scale", ctypes.c_void_p)]
 
 
+class MxLinear(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64), ("bits", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("a_data", ctypes.c_void_p), ("a_scales", ctypes.c_void_p), ("b_data", ctypes.c_void_p), ("b_scales", ctypes.c_void_p),
+                ("alpha", ctypes.c_float), ("beta", ctypes.c_float), ("bias", ctypes.c_void_p), ("act", ctypes.c_int),
+                ("c", ctypes.c_void_p), ("ldc", ctypes.c_int64), ("pre", ctypes.c_void_p), ("ldpre", ctypes.c_int64),
+                ("d", ctypes.c_void_p), ("ldd", ctypes.c_int64)]
+
+
+class ActBackward(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int), ("act", ctypes.c_int),
+                ("dout", ctypes.c_void_p), ("lddout", ctypes.c_int64), ("pre", ctypes.c_void_p), ("ldpre", ctypes.c_int64),
+                ("dz", ctypes.c_void_p), ("lddz", ctypes.c_int64), ("d_bias", ctypes.c_void_p), ("scale_mode", ctypes.c_int),
+                ("row_data", ctypes.c_void_p), ("row_scales", ctypes.c_void_p), ("col_data", ctypes.c_void_p),
+                ("col_scales", ctypes.c_void_p)]
+
+
+class AddNorm(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("dtype", ctypes.c_int), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("f", ctypes.c_void_p), ("ldf", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("h", ctypes.c_void_p), ("ldh", ctypes.c_int64),
+                ("q_data", ctypes.c_void_p), ("q_scales", ctypes.c_void_p), ("scale_mode", ctypes.c_int), ("p", ctypes.c_float),
+                ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64), ("rstd", ctypes.c_void_p)]
+
+
+class AddNormGrad(ctypes.Structure):
+    _fields_ = [("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("dh", ctypes.c_void_p), ("lddh", ctypes.c_int64),
+                ("dx", ctypes.c_void_p), ("lddx", ctypes.c_int64), ("df", ctypes.c_void_p), ("lddf", ctypes.c_int64),
+                ("d_w", ctypes.c_void_p)]
+
+
 # The same fields for struct.pack, which fills them in half the time.
 _NORM = struct.Struct("qqifPqPqPPPqPPqPqP")
 _NORM_GRAD = struct.Struct("PqPqPqPqPPPP")
+_LINEAR = struct.Struct("qqqiiPPPPffPiPqPqPq")
+_ACT_BACKWARD = struct.Struct("qqiiPqPqPqPiPPPP")
+_ADD_NORM = struct.Struct("qqifPqPqPPqPqPPifQQP")
+_ADD_NORM_GRAD = struct.Struct("PqPqPqPqP")
 assert _NORM.size == ctypes.sizeof(BlockNorm) and _NORM_GRAD.size == ctypes.sizeof(BlockNormGrad)
+assert _LINEAR.size == ctypes.sizeof(MxLinear) and _ACT_BACKWARD.size == ctypes.sizeof(ActBackward)
+assert _ADD_NORM.size == ctypes.sizeof(AddNorm) and _ADD_NORM_GRAD.size == ctypes.sizeof(AddNormGrad)
 
 
 BACKENDS = {"direct": 0, "gram": 1}
 SCALE_MODES = {"floor": 0, "ceil": 1}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 _TYPES = {}  # torch dtype -> type code of include/dmuon.h, filled with the first tensor
 
 
@@ -194,6 +234,22 @@ def load(path=None):
     L.dmuon_block_norm_forward.restype = i32
     L.dmuon_block_norm_backward.argtypes = [vp, ctypes.POINTER(BlockNorm), ctypes.POINTER(BlockNormGrad), vp]
     L.dmuon_block_norm_backward.restype = i32
+    L.dmuon_mxfp8_bytes.argtypes = [i64, i64, sz, sz]
+    L.dmuon_mxfp8_bytes.restype = i32
+    L.dmuon_mxfp8_quantize.argtypes = [vp, vp, i32, i64, i64, i64, i32, vp, vp, vp, vp, vp]
+    L.dmuon_mxfp8_quantize.restype = i32
+    L.dmuon_mxfp8_dequantize.argtypes = [vp, vp, vp, i64, i64, vp, i32, i64, vp]
+    L.dmuon_mxfp8_dequantize.restype = i32
+    L.dmuon_mx_linear.argtypes = [vp, ctypes.POINTER(MxLinear), vp]
+    L.dmuon_mx_linear.restype = i32
+    L.dmuon_act_backward.argtypes = [vp, ctypes.POINTER(ActBackward), vp]
+    L.dmuon_act_backward.restype = i32
+    L.dmuon_add_norm_forward.argtypes = [vp, ctypes.POINTER(AddNorm), vp]
+    L.dmuon_add_norm_forward.restype = i32
+    L.dmuon_add_norm_backward.argtypes = [vp, ctypes.POINTER(AddNorm), ctypes.POINTER(AddNormGrad), vp]
+    L.dmuon_add_norm_backward.restype = i32
+    L.dmuon_dropout.argtypes = [vp, vp, i32, i64, i64, i64, vp, i64, vp, i64, f32, ctypes.c_uint64, ctypes.c_uint64, vp]
+    L.dmuon_dropout.restype = i32
     _lib = L
     return L
 
@@ -472,7 +528,7 @@ def dmuon_clip_grad_norm(h, grads, max_norm, buckets=None, n_buckets=None, stats
     return norms, coefs
 
 
-# ------------------------------------------- 4-bit projections and their norms
+# ------------------------------------ 4- and 8-bit projections and their norms
 
 def _device(h, t, name):
     """Index of the handle's device, on which every tensor of a call has to be;
@@ -528,17 +584,26 @@ def _floats(t, name, index, shape):
     return t.data_ptr()
 
 
-def _mxfp4(q, name, index, rows, k):
-    """(data pointer, scales pointer) of an MXFP4 matrix (data, scales)."""
+def _mx(q, name, index, rows, k, bits):
+    """(data pointer, scales pointer) of an MXFP4 or MXFP8 matrix (data, scales)."""
     data, scales = q
     nb = -(-k // 32)
     types = _TYPES or _types()
-    if (types.get(data.dtype) != 3 or types.get(scales.dtype) != 3 or data.numel() != rows * nb * 16 or
+    if (types.get(data.dtype) != 3 or types.get(scales.dtype) != 3 or data.numel() != rows * nb * 4 * bits or
             scales.numel() != -(-rows // 128) * -(-nb // 4) * 512 or data.get_device() != index or scales.get_device() != index or
             not data.is_contiguous() or not scales.is_contiguous()):
-        raise ValueError("%s: contiguous uint8 tensors of the sizes dmuon_mxfp4_empty(%d, %d) gives on the handle's device are wanted"
-                         % (name, rows, k))
+        raise ValueError("%s: contiguous uint8 tensors of the sizes dmuon_mxfp%d_empty(%d, %d) gives on the handle's device are wanted"
+                         % (name, bits, rows, k))
     return data.data_ptr(), scales.data_ptr()
+
+
+def _mxfp4(q, name, index, rows, k):
+    return _mx(q, name, index, rows, k, 4)
+
+
+def _mxfp8(q, name, index, rows, k):
+    """The same of an MXFP8 matrix; None gives (None, None)."""
+    return (None, None) if q is None else _mx(q, name, index, rows, k, 8)
 
 
 _raw_stream = None  # torch's current stream of a device as an integer
@@ -605,12 +670,12 @@ def dmuon_mxfp4_dequantize(h, q, out, stream=None):
         _check(rc, "dmuon_mxfp4_dequantize", h)
 
 
-def _zero_block(rows, stream, index):
-    """A zero MXFP4 matrix of one block of columns: buffers of the stream (raw
-    handle), which an empty sum is taken over since the library wants k >= 1."""
+def _zero_block(rows, stream, index, bits=4):
+    """A zero matrix of one block of columns: buffers of the stream (raw handle),
+    which an empty sum is taken over since the library wants k >= 1."""
     import contextlib
     import torch
-    d, s = dmuon_mxfp4_bytes(rows, 32)
+    d, s = dmuon_mxfp4_bytes(rows, 32) if bits == 4 else dmuon_mxfp8_bytes(rows, 32)
     here = torch.cuda.current_stream(index)
     on = contextlib.nullcontext() if here.cuda_stream == stream else torch.cuda.stream(torch.cuda.ExternalStream(stream, index))
     with on:
@@ -682,6 +747,161 @@ def dmuon_block_norm_backward(h, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d
     rc = load().dmuon_block_norm_backward(h, p, q, _stream_of(stream, first[0]))
     if rc:
         _check(rc, "dmuon_block_norm_backward", h)
+
+
+def dmuon_mxfp8_bytes(rows, k):
+    """(data bytes, scale bytes) of a rows x k MXFP8 matrix (host only)."""
+    d, s = ctypes.c_size_t(0), ctypes.c_size_t(0)
+    _check(load().dmuon_mxfp8_bytes(int(rows), int(k), ctypes.byref(d), ctypes.byref(s)), "dmuon_mxfp8_bytes")
+    return d.value, s.value
+
+
+def dmuon_mxfp8_empty(rows, k, device="cuda"):
+    """Uninitialised buffers (data, scales) of a rows x k MXFP8 matrix."""
+    import torch
+    d, s = dmuon_mxfp8_bytes(rows, k)
+    return (torch.empty((rows, d // max(1, rows)), dtype=torch.uint8, device=device),
+            torch.empty(s, dtype=torch.uint8, device=device))
+
+
+def dmuon_mxfp8_quantize(h, src, by_rows=None, by_cols=None, scale="floor", stream=None):
+    """Quantise the matrix ``src`` [r, c] along its rows into ``by_rows`` (an
+    r x c MXFP8 matrix) and / or along its columns into ``by_cols`` (c x r)."""
+    index = _device(h, src, "src")
+    ptr, ld, code, (r, c) = _matrix(src, "src", index)
+    rd, rs = _mxfp8(by_rows, "by_rows", index, r, c)
+    cd, cs = _mxfp8(by_cols, "by_cols", index, c, r)
+    mode = SCALE_MODES[scale]
+    if r == 0 or c == 0:
+        return
+    rc = load().dmuon_mxfp8_quantize(h, ptr, code, r, c, ld, mode, rd, rs, cd, cs, _stream_of(stream, index))
+    if rc:
+        _check(rc, "dmuon_mxfp8_quantize", h)
+
+
+def dmuon_mxfp8_dequantize(h, q, out, stream=None):
+    """The values of the MXFP8 matrix ``q`` into ``out`` [rows, k]."""
+    index = _device(h, out, "out")
+    ptr, ld, code, (r, k) = _matrix(out, "out", index)
+    d, s = _mx(q, "q", index, r, k, 8)
+    if r == 0 or k == 0:
+        return
+    rc = load().dmuon_mxfp8_dequantize(h, d, s, r, k, ptr, code, ld, _stream_of(stream, index))
+    if rc:
+        _check(rc, "dmuon_mxfp8_dequantize", h)
+
+
+def dmuon_mx_linear(h, a, b, out, k, bias=None, act="none", pre=None, residual=None, alpha=1.0, beta=1.0, bits=8, stream=None):
+    """z = alpha * a b^T + bias, out = act(z) + beta * residual, pre = z of
+    MXFP8 (bits=4: MXFP4) matrices a [m, k] and b [n, k]; out, pre and residual
+    (which may be out) are [m, n] of one type, bias [n] float32.  k = 0, a sum over
+    no rows, gives z = bias."""
+    index = _device(h, out, "out")
+    ptr, ld, code, size = _matrix(out, "out", index)
+    m, n = size
+    if bits not in (4, 8):
+        raise ValueError("bits must be 4 or 8")
+    ad, as_ = _mx(a, "a", index, m, k, bits)
+    bd, bs = _mx(b, "b", index, n, k, bits)
+    first = index, out.dtype, code, size
+    pp, ldp = _like(pre, "pre", first)
+    cp, ldc = _like(residual, "residual", first)
+    bp = _floats(bias, "bias", index, (n,))
+    kind = ACTIVATIONS[act]
+    if m == 0 or n == 0:
+        return
+    stream = _stream_of(stream, index)
+    if k == 0:
+        zeros, ad, as_ = _zero_block(max(m, n), stream, index, bits)
+        bd, bs, k = ad, as_, 32
+    p = MxLinear.from_buffer_copy(_LINEAR.pack(m, n, k, bits, code, ad, as_, bd, bs, alpha, beta, bp, kind, cp, ldc, pp, ldp, ptr, ld))
+    rc = load().dmuon_mx_linear(h, p, stream)
+    if rc:
+        _check(rc, "dmuon_mx_linear", h)
+
+
+def dmuon_act_backward(h, dout, pre, act, dz=None, d_bias=None, by_rows=None, by_cols=None, scale="floor", stream=None):
+    """dz = dout * act'(pre) of dout and pre [r, c] into ``dz``, by rows and / or
+    columns into the MXFP8 matrices ``by_rows`` (r x c) and ``by_cols`` (c x r),
+    and its column sums into ``d_bias`` [c] float32; None for what is not wanted.
+    ``pre`` may be None for act "none"."""
+    index = _device(h, dout, "dout")
+    ptr, ld, code, size = _matrix(dout, "dout", index)
+    r, c = size
+    kind = ACTIVATIONS[act]
+    if pre is None and kind != 0:
+        raise ValueError("pre is wanted for this activation")
+    first = index, dout.dtype, code, size
+    pp, ldp = _like(pre, "pre", first)
+    zp, ldz = _like(dz, "dz", first)
+    rd, rs = _mxfp8(by_rows, "by_rows", index, r, c)
+    cd, cs = _mxfp8(by_cols, "by_cols", index, c, r)
+    p = ActBackward.from_buffer_copy(_ACT_BACKWARD.pack(r, c, code, kind, ptr, ld, pp, ldp, zp, ldz, _floats(d_bias, "d_bias", index, (c,)),
+                                                        SCALE_MODES[scale], rd or 0, rs or 0, cd or 0, cs or 0))
+    if dz is None and d_bias is None and by_rows is None and by_cols is None:
+        raise ValueError("no output is given")
+    rc = load().dmuon_act_backward(h, p, _stream_of(stream, index))
+    if rc:
+        _check(rc, "dmuon_act_backward", h)
+
+
+def _add_norm(h, x, f, y, w, rstd, out, q, mode, p, seed, offset, eps, like):
+    """The fields that forward and backward share; ``like`` is f, or df."""
+    index = _device(h, like, "f")
+    fp, ldf, code, size = _matrix(like, "f", index)
+    rows, cols = size
+    first = index, like.dtype, code, size
+    xp, ldx = _like(x, "x", first)
+    yp, ldy = _like(y, "y", first)
+    hp, ldh = _like(out, "out", first)
+    qd, qs = _mxfp8(q, "q", index, rows, cols)
+    packed = _ADD_NORM.pack(rows, cols, code, eps, xp, ldx, fp, ldf, _floats(w, "w", index, (cols,)), yp, ldy, hp, ldh, qd or 0, qs or 0,
+                            SCALE_MODES[mode], p, seed, offset, _floats(rstd, "rstd", index, (rows,)))
+    return AddNorm.from_buffer_copy(packed), first
+
+
+def dmuon_add_norm_forward(h, x, f, w, y, rstd, out=None, q=None, p=0.0, seed=0, offset=0, eps=1e-6, scale="floor", stream=None):
+    """y = x + dropout(f) (x None: 0) and rms(y) * w over the rows of x and f
+    [rows, cols], into ``out`` (their type) and / or ``q`` (an MXFP8 matrix);
+    rstd [rows] is what the backward needs."""
+    if y is None or w is None or rstd is None or out is None and q is None:
+        raise ValueError("y, w, rstd and out or q are wanted")
+    s, first = _add_norm(h, x, f, y, w, rstd, out, q, scale, p, seed, offset, eps, f)
+    rc = load().dmuon_add_norm_forward(h, s, _stream_of(stream, first[0]))
+    if rc:
+        _check(rc, "dmuon_add_norm_forward", h)
+
+
+def dmuon_add_norm_backward(h, dy, dh, y, w, rstd, dx, df, d_w, p=0.0, seed=0, offset=0, stream=None):
+    """Gradients of dmuon_add_norm_forward from dh (of its normalised values) and
+    dy (of y, None = 0): dx (None: not wanted; without dropout it is df), df and
+    d_w [cols] float32.  y, rstd, p, seed and offset as in the forward."""
+    if dh is None or df is None or y is None or w is None or rstd is None or d_w is None:
+        raise ValueError("dh, y, w, rstd, df and d_w are wanted")
+    s, first = _add_norm(h, None, None, y, w, rstd, None, None, "floor", p, seed, offset, 0.0, df)
+    index, line = first[0], (first[3][1],)
+    g = AddNormGrad.from_buffer_copy(_ADD_NORM_GRAD.pack(*_like(dy, "dy", first), *_like(dh, "dh", first), *_like(dx, "dx", first),
+                                                         *_like(df, "df", first), _floats(d_w, "d_w", index, line)))
+    rc = load().dmuon_add_norm_backward(h, s, g, _stream_of(stream, index))
+    if rc:
+        _check(rc, "dmuon_add_norm_backward", h)
+
+
+def dmuon_dropout(h, x, out, p, seed, offset=0, residual=None, stream=None):
+    """out = dropout(x) (+ residual) over [rows, cols]: an element stays with
+    probability 1 - p, as (p, seed, offset, row, column) tell, and is then scaled
+    by 1 / (1 - p).  The same call on a gradient is the backward pass; out may be
+    x or residual."""
+    index = _device(h, x, "x")
+    ptr, ld, code, size = _matrix(x, "x", index)
+    first = index, x.dtype, code, size
+    if out is None:
+        raise ValueError("out is wanted")
+    op, ldo = _like(out, "out", first)
+    rp, ldr = _like(residual, "residual", first)
+    rc = load().dmuon_dropout(h, ptr, code, size[0], size[1], ld, rp or None, ldr, op, ldo, p, seed, offset, _stream_of(stream, index))
+    if rc:
+        _check(rc, "dmuon_dropout", h)
 
 
 def dmuon_get_status(h, n_flags=0):
@@ -815,3 +1035,24 @@ class Handle:
 
     def block_norm_backward(self, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d_post_w, d_pre_w, **kw):
         return dmuon_block_norm_backward(self.h, dy, dh, x, f, y, post_w, pre_w, rstd, dx, df, d_post_w, d_pre_w, **kw)
+
+    def mxfp8_quantize(self, src, by_rows=None, by_cols=None, scale="floor", stream=None):
+        return dmuon_mxfp8_quantize(self.h, src, by_rows, by_cols, scale, stream)
+
+    def mxfp8_dequantize(self, q, out, stream=None):
+        return dmuon_mxfp8_dequantize(self.h, q, out, stream)
+
+    def mx_linear(self, a, b, out, k, **kw):
+        return dmuon_mx_linear(self.h, a, b, out, k, **kw)
+
+    def act_backward(self, dout, pre, act, **kw):
+        return dmuon_act_backward(self.h, dout, pre, act, **kw)
+
+    def add_norm_forward(self, x, f, w, y, rstd, **kw):
+        return dmuon_add_norm_forward(self.h, x, f, w, y, rstd, **kw)
+
+    def add_norm_backward(self, dy, dh, y, w, rstd, dx, df, d_w, **kw):
+        return dmuon_add_norm_backward(self.h, dy, dh, y, w, rstd, dx, df, d_w, **kw)
+
+    def dropout(self, x, out, p, seed, offset=0, residual=None, stream=None):
+        return dmuon_dropout(self.h, x, out, p, seed, offset, residual, stream)

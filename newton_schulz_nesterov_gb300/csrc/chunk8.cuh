@@ -1,0 +1,135 @@
+// Eight consecutive elements of a row, loaded and stored by one thread, in rows
+// that are 16-byte aligned (VEC) or on any element.
+//
+// Loads take the aligned 16-byte pieces that hold one of the wanted elements
+// (such a piece lies in one allocation, whatever else is in it) and shift them
+// together: 8191 columns of bf16 cost two loads and fifteen selects for eight
+// elements, where single elements would cost eight loads that touch a line a
+// lane.  Stores of a warp whose lanes hold consecutive runs go by pieces.cuh.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include <type_traits>
+
+#include "pieces.cuh"
+
+namespace dmuon {
+
+template <typename T>
+constexpr int words8() { return (int)sizeof(T) * 2; }  // 32-bit words of eight elements
+
+// Pieces of a run of eight as they are loaded; `shift` puts them together.
+template <typename T, bool VEC>
+struct Raw8 {
+  static constexpr int kWords = words8<T>() + (VEC ? 0 : 4);
+  uint32_t w[kWords];
+};
+
+// n: elements of the row from p on; those past the eighth are not wanted.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load_raw8(Raw8<T, VEC>& r, const T* p, int n) {
+  const uint32_t m = VEC ? 0u : past16(p);
+  const uint4* piece = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(p) - m);
+  const int bytes = (int)m + min(n, 8) * (int)sizeof(T);
+#pragma unroll
+  for (int i = 0; i < Raw8<T, VEC>::kWords / 4; ++i) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (n > 0 && 16 * i < bytes) v = piece[i];
+    r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
+  }
+}
+
+// The elements as fp32, zero from the nth on.  p as in load_raw8.
+template <typename T, bool VEC>
+__device__ __forceinline__ void values8(float (&f)[8], Raw8<T, VEC> r, const T* p, int n) {
+  constexpr int W = words8<T>();
+  if constexpr (!VEC) {
+    const uint32_t m = past16(p);
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) r.w[i] = m & 8 ? r.w[i + 2] : r.w[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) r.w[i] = m & 4 ? r.w[i + 1] : r.w[i];
+    if constexpr (sizeof(T) == 2)
+#pragma unroll
+      for (int i = 0; i < W; ++i) r.w[i] = __funnelshift_r(r.w[i], r.w[i + 1], (m & 2) * 8);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if constexpr (sizeof(T) == 4) {
+      f[e] = __uint_as_float(r.w[e]);
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const __half2 h = *reinterpret_cast<const __half2*>(&r.w[e / 2]);
+      f[e] = e & 1 ? __high2float(h) : __low2float(h);
+    } else {
+      f[e] = __uint_as_float(e & 1 ? r.w[e / 2] & 0xFFFF0000u : r.w[e / 2] << 16);
+    }
+  }
+  if (n < 8)
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (e >= n) f[e] = 0.f;
+}
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(float (&f)[8], const T* p, int n) {
+  Raw8<T, VEC> r;
+  load_raw8<T, VEC>(r, p, n);
+  values8<T, VEC>(f, r, p, n);
+}
+
+// Eight values rounded to T, as words.
+template <typename T>
+__device__ __forceinline__ void pack8(uint32_t* w, const float (&f)[8]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(f[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (std::is_same<T, __half>::value) {
+        const __half2 h = __floats2half2_rn(f[2 * e], f[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * e], f[2 * e + 1]);
+        w[e] = *reinterpret_cast<const uint32_t*>(&h);
+      }
+    }
+  }
+}
+
+// The first n of eight values to p, 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&f)[8], int n) {
+  uint32_t w[words8<T>()];
+  pack8<T>(w, f);
+  if (n >= 8) {
+#pragma unroll
+    for (int i = 0; i < words8<T>(); i += 4) *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 7; ++e)
+    if (e < n) {
+      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[e] = w[e];
+      else reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+}
+
+// The same for a warp, whose lanes hold consecutive runs of eight; rows on any
+// element.  `first`, `last`, `live` as in store_pieces; n: of the row from p on.
+template <typename T, bool VEC>
+__device__ __forceinline__ void store8_warp(T* p, const float (&f)[8], int64_t n, bool first, bool last, bool live) {
+  if constexpr (VEC) {
+    if (live) store8<T>(p, f, (int)min((int64_t)8, n));
+  } else {
+    constexpr int W = words8<T>();
+    uint32_t w[W + 8];
+    pack8<T>(w + 4, f);
+    store_pieces<sizeof(T)>(reinterpret_cast<uint8_t*>(p), w, n * (int64_t)sizeof(T), first, last || n < 16, live);
+  }
+}
+
+}  // namespace dmuon

@@ -125,13 +125,14 @@ struct dmuon_ctx {
   size_t aux_host_cap = 0;
   cudaEvent_t aux_ev = nullptr;
   bool aux_pending = false;
-  // Operators of a 4-bit block: a wait that ran out (device word, allocated
-  // with the handle) and the norm backward's partial sums
+  // Operators around a 4- or 8-bit projection: a wait that ran out (device word,
+  // allocated with the handle) and the backward passes' partial sums
   int* d_op_err = nullptr;
   void* op_ws = nullptr;
   size_t op_ws_cap = 0;
   int norm_places[8] = {};
   bool quant_ready = false, norm_ready = false;  // the kernels' limits of shared memory are set
+  bool linear_ready[2] = {};           // of projections of 4 and 8 bits
   bool op_ws_captured = false;         // a graph holds op_ws: it stays until the handle goes
   std::vector<void*> op_ws_kept;
 };

@@ -33,7 +33,7 @@
 #include "common.cuh"
 #include "ctx.cuh"
 #include "gram.cuh"
-#include "mxfp4.cuh"
+#include "mx.cuh"
 #include "plan.cuh"
 #include "small.cuh"
 

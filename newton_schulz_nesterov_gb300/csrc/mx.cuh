@@ -1,9 +1,11 @@
-// MXFP4 matrices (OCP microscaling: blocks of 32 E2M1 elements along a row,
-// one E8M0 scale each): layout, kernel arguments and host launchers.
+// MXFP4 and MXFP8 matrices (OCP microscaling: blocks of 32 E2M1 or E4M3
+// elements along a row, one E8M0 scale each): layout, kernel arguments and host
+// launchers.
 //
 // A matrix of `rows` x `k`:
-//   data    row-major, pitch 16 * ceil(k / 32) bytes; element 2i in the low,
-//           2i + 1 in the high half of byte i; elements past k are zero
+//   data    row-major, elements past k are zero; MXFP4: pitch 16 * ceil(k / 32)
+//           bytes, element 2i in the low, 2i + 1 in the high half of byte i;
+//           MXFP8: pitch 32 * ceil(k / 32) bytes
 //   scales  one byte per block, in tiles of 128 rows x 4 blocks (512 bytes),
 //           tiles row-major: row r, block j of a tile at
 //           (r % 32) * 16 + (r / 32) * 4 + j; bytes past the matrix are zero
@@ -15,13 +17,15 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "act.cuh"
+
 namespace dmuon {
 
 constexpr int kMxBlock = 32;          // elements per scale
 constexpr int kMxScaleTile = 512;     // bytes: 128 rows x 4 blocks
 
 __host__ __device__ inline int64_t mx_blocks(int64_t k) { return (k + kMxBlock - 1) / kMxBlock; }
-__host__ __device__ inline int64_t mx_pitch(int64_t k) { return mx_blocks(k) * 16; }
+__host__ __device__ inline int64_t mx_pitch(int64_t k, int bits = 4) { return mx_blocks(k) * 4 * bits; }
 __host__ __device__ inline int64_t mx_scale_cols(int64_t k) { return (mx_blocks(k) + 3) / 4; }   // tiles per row of tiles
 __host__ __device__ inline int64_t mx_scale_bytes(int64_t rows, int64_t k) {
   return (rows + 127) / 128 * mx_scale_cols(k) * kMxScaleTile;
@@ -36,6 +40,23 @@ struct MxQuantArgs {
   uint8_t *col_data, *col_scales;   // cols x rows quantised along rows, or nullptr
   int ceil_scale;
   int vec, noise_vec;          // 16-byte aligned base and pitch
+};
+
+// An MXFP8 pass over a matrix: values (src, or dout * act'(pre)) to codes by rows
+// and / or by columns, to dz and to column sums.
+struct Mx8Args {
+  const void *src, *pre;            // pre: nullptr for a quantisation
+  int64_t rows, cols, ld, ldpre;
+  Act act;
+  uint8_t *row_data, *row_scales;   // or nullptr
+  uint8_t *col_data, *col_scales;   // or nullptr
+  void* dz;                         // rows x cols of src's type, or nullptr
+  int64_t lddz;
+  float* parts;                     // [chunks][part_ld] column sums, or nullptr
+  int64_t part_ld;
+  int64_t tiles;                    // tiles of 128 rows a CTA goes down
+  uint32_t round_up;                // added to a magnitude's bits ahead of taking its exponent
+  int vec;                          // every matrix's rows are 16-byte aligned
 };
 
 struct MxDequantArgs {
@@ -62,6 +83,16 @@ struct MxGemmArgs {
   unsigned long long timeout_ns;
 };
 
+// z = alpha A B^T + bias, D = act(z) + beta C, z to pre.
+struct MxLinearArgs : MxGemmArgs {
+  const void* c;               // as D, or nullptr
+  int64_t ldc;
+  const float* bias;           // columns of D, or nullptr
+  void* pre;                   // as D, or nullptr
+  int64_t ldpre;
+  Act act;
+};
+
 cudaError_t launch_mx_quant(const MxQuantArgs& a, int dtype, cudaStream_t s);
 cudaError_t launch_mx_dequant(const MxDequantArgs& a, int dtype, cudaStream_t s);
 // Before the launches.
@@ -69,5 +100,16 @@ cudaError_t mx_quant_configure();
 cudaError_t mx_gemm_configure();
 cudaError_t launch_mx_gemm(const MxGemmArgs& a, int nt, int split, cudaStream_t s);
 cudaError_t launch_mx_gemm_pair(const MxGemmArgs& a, int pairs, cudaStream_t s);
+cudaError_t mx_linear4_configure();
+cudaError_t launch_mx_linear4(const MxLinearArgs& a, int nt, int split, cudaStream_t s);
+cudaError_t launch_mx_linear4_pair(const MxLinearArgs& a, int pairs, cudaStream_t s);
+cudaError_t mx_linear8_configure();
+cudaError_t launch_mx_linear8(const MxLinearArgs& a, int nt, int split, cudaStream_t s);
+cudaError_t launch_mx_linear8_pair(const MxLinearArgs& a, int pairs, cudaStream_t s);
+// grad: dout * act'(pre) in place of src.
+cudaError_t launch_mx8_tiles(const Mx8Args& a, int dtype, bool grad, cudaStream_t s);
+cudaError_t launch_mx8_dequant(const MxDequantArgs& a, int dtype, cudaStream_t s);
+// out[c] = the sum over `n` rows of parts, in a fixed order.
+cudaError_t launch_column_sums(const float* parts, int64_t n, int64_t ld, int64_t cols, float* out, cudaStream_t s);
 
 }  // namespace dmuon

@@ -22,7 +22,7 @@
 #include <cuda_fp16.h>
 
 #include "../../include/dmuon.h"
-#include "mxfp4.cuh"
+#include "mx.cuh"
 #include "pieces.cuh"
 #include "ptx.cuh"
 

@@ -27,24 +27,26 @@ __device__ __forceinline__ void shift_out(uint32_t (&out)[N], const uint32_t (&w
   }
 }
 
-// 32 bytes a lane (w[4] .. w[11]; the rest is scratch) to `own`, on any element
+// B bytes a lane (w[4] .. w[B / 4 + 3]; the rest is scratch) to `own`, on any element
 // of SIZE (2 or 4) bytes: stored by the aligned pieces that they begin in, the
 // first of which takes the last words of the lane before.  `first`: the lane
-// before does not hold the 32 bytes before these; `last`: the lane after does
-// not hold 32 whole bytes after these; either side then stores its own bytes.
-// left: bytes of the row from `own` on (32 or more: all are stored).  All lanes
+// before does not hold the B bytes before these; `last`: the lane after does
+// not hold B whole bytes after these; either side then stores its own bytes.
+// left: bytes of the row from `own` on (B or more: all are stored).  All lanes
 // of a warp call it; one that is not live stores nothing.
-template <int SIZE>
-__device__ __forceinline__ void store_pieces(uint8_t* own, uint32_t (&w)[16], int64_t left, bool first, bool last, bool live) {
+template <int SIZE, int W>
+__device__ __forceinline__ void store_pieces(uint8_t* own, uint32_t (&w)[W], int64_t left, bool first, bool last, bool live) {
+  constexpr int N = W - 8, B = 4 * N;  // words and bytes a lane
+  static_assert(N == 4 || N == 8, "one or two pieces");
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w[i] = __shfl_up_sync(0xffffffffu, w[8 + i], 1);
-    w[12 + i] = 0;
+    w[i] = __shfl_up_sync(0xffffffffu, w[N + i], 1);
+    w[N + 4 + i] = 0;
   }
   if (!live || left <= 0) return;
-  if (left < 32) {  // the row's last elements
+  if (left < B) {  // the row's last elements
 #pragma unroll
-    for (int e = 0; e < 32 / SIZE - 1; ++e)
+    for (int e = 0; e < B / SIZE - 1; ++e)
       if (e * SIZE < left) {
         if constexpr (SIZE == 4) reinterpret_cast<uint32_t*>(own)[e] = w[4 + e];
         else reinterpret_cast<uint16_t*>(own)[e] = (uint16_t)(w[4 + e / 2] >> (16 * (e & 1)));
@@ -52,12 +54,12 @@ __device__ __forceinline__ void store_pieces(uint8_t* own, uint32_t (&w)[16], in
     return;
   }
   const uint32_t m = past16(own);
-  uint32_t o[12];  // words from this lane's first piece on
+  uint32_t o[N + 4];  // words from this lane's first piece on
   if (m == 0) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = w[4 + i];
+    for (int i = 0; i < N; ++i) o[i] = w[4 + i];
   } else {
-    shift_out<12>(o, w, 16 - m);
+    shift_out<N + 4>(o, w, 16 - m);
   }
   uint32_t* piece = reinterpret_cast<uint32_t*>(own - m);
   if (m == 0 || !first) {
@@ -69,12 +71,12 @@ __device__ __forceinline__ void store_pieces(uint8_t* own, uint32_t (&w)[16], in
       else if (SIZE == 2 && 4 * i + 2 == (int)m) reinterpret_cast<uint16_t*>(piece)[2 * i + 1] = (uint16_t)(o[i] >> 16);
     }
   }
-  *reinterpret_cast<uint4*>(piece + 4) = make_uint4(o[4], o[5], o[6], o[7]);
+  if constexpr (N == 8) *reinterpret_cast<uint4*>(piece + 4) = make_uint4(o[4], o[5], o[6], o[7]);
   if (m && last) {  // the last m bytes
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      if (4 * i + 4 <= (int)m) piece[8 + i] = o[8 + i];
-      else if (SIZE == 2 && 4 * i + 2 == (int)m) reinterpret_cast<uint16_t*>(piece + 8)[2 * i] = (uint16_t)o[8 + i];
+      if (4 * i + 4 <= (int)m) piece[N + i] = o[N + i];
+      else if (SIZE == 2 && 4 * i + 2 == (int)m) reinterpret_cast<uint16_t*>(piece + N)[2 * i] = (uint16_t)o[N + i];
     }
   }
 }
