@@ -1,8 +1,8 @@
 // Activations of a projection's epilogue and their slopes, in fp32.
 //
-// Five functions in three forms, chosen by uniform branches:
+// Five functions in three forms, chosen by uniform branches, two values at a time:
 //   clamp  z < a ? 0 : z                  none (a = -inf), relu (a = 0)
-//   gate   z / (1 + exp(-u)), u = z (a + b z^2)
+//   gate   z / (1 + exp(-u)), u = z (a + b z^2), kept as -log2(e) a and b
 //                                         silu (1, 0), gelu_tanh (2 sqrt(2/pi) (1, 0.044715),
 //                                         since 1 + tanh v = 2 / (1 + exp(-2 v)))
 //   erf    z Phi(z)                       gelu
@@ -13,6 +13,8 @@
 #pragma once
 
 #include <cuda_runtime.h>
+
+#include "f32x2.cuh"
 
 namespace dmuon {
 
@@ -27,9 +29,9 @@ inline Act act_of(int code) {
   const float lowest = -__builtin_huge_valf();
   switch (code) {
     case 1: return {kActClamp, 0.f, 0.f};
-    case 2: return {kActGate, 1.f, 0.f};
+    case 2: return {kActGate, -1.4426950408889634f, 0.f};
     case 3: return {kActErf, 0.f, 0.f};
-    case 4: return {kActGate, 1.5957691216057308f, 0.07135481282556f};
+    case 4: return {kActGate, -2.302208198144325f, -0.1029432395800235f};
     default: return {kActClamp, lowest, 0.f};
   }
 }
@@ -37,6 +39,10 @@ inline Act act_of(int code) {
 // Past +-1e4 every one of them is 0 or z to the last bit: what would overflow
 // there is taken at the border.
 __device__ __forceinline__ float act_inside(float z) { return z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z; }
+__device__ __forceinline__ f2 act_inside2(f2 z) {
+  const float2 p = unpack2(z);
+  return pack2(act_inside(p.x), act_inside(p.y));
+}
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float r;
@@ -48,68 +54,87 @@ __device__ __forceinline__ float rcp_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+__device__ __forceinline__ f2 exp2_fast2(f2 x) {
+  const float2 p = unpack2(x);
+  return pack2(exp2_fast(p.x), exp2_fast(p.y));
+}
+__device__ __forceinline__ f2 rcp_fast2(f2 x) {
+  const float2 p = unpack2(x);
+  return pack2(rcp_fast(p.x), rcp_fast(p.y));
+}
 
-constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
-// exp(-z^2/2) and Phi(z).
-__device__ __forceinline__ float normal_below(float z, float& bell) {
-  const float t = rcp_fast(fmaf(fabsf(z), 0.28284271f, 1.f));
-  float p = 0.05026565119624138f;
-  p = fmaf(p, t, -0.182915598154068f);
-  p = fmaf(p, t, 0.169108584523201f);
-  p = fmaf(p, t, -0.0056274873204529285f);
-  p = fmaf(p, t, 0.14144112169742584f);
-  p = fmaf(p, t, 0.16853934526443481f);
-  p = fmaf(p, t, 0.20784308016300201f);
-  p = fmaf(p, t, 0.22566957771778107f);
-  p = fmaf(p, t, 0.22567586600780487f);
-  bell = exp2_fast(z * z * (-0.5f * kLog2e));
-  const float below = 0.5f * (p * t) * bell;  // Phi(-|z|)
-  return z > 0.f ? 1.f - below : below;
+// exp(-z^2/2) and Phi(z) of two values.
+__device__ __forceinline__ f2 normal_below2(f2 z, f2& bell) {
+  const float2 p = unpack2(z);
+  const f2 t = rcp_fast2(fma2(pack2(fabsf(p.x), fabsf(p.y)), both(0.28284271f), both(1.f)));
+  f2 q = both(0.05026565119624138f);
+  q = fma2(q, t, both(-0.182915598154068f));
+  q = fma2(q, t, both(0.169108584523201f));
+  q = fma2(q, t, both(-0.0056274873204529285f));
+  q = fma2(q, t, both(0.14144112169742584f));
+  q = fma2(q, t, both(0.16853934526443481f));
+  q = fma2(q, t, both(0.20784308016300201f));
+  q = fma2(q, t, both(0.22566957771778107f));
+  q = fma2(q, t, both(0.22567586600780487f));
+  bell = exp2_fast2(mul2(mul2(z, z), both(-0.5f * kLog2e)));
+  const float2 below = unpack2(mul2(mul2(mul2(q, t), both(0.5f)), bell));  // Phi(-|z|)
+  return pack2(p.x > 0.f ? 1.f - below.x : below.x, p.y > 0.f ? 1.f - below.y : below.y);
 }
 
 // f[i] = act(f[i])
 template <int N>
-__device__ __forceinline__ void act_values(float (&f)[N], const Act& act) {
+__device__ __forceinline__ void act_values(f2 (&f)[N], const Act& act) {
   if (act.kind == kActClamp) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) f[i] = f[i] < act.a ? 0.f : f[i];
+    for (int i = 0; i < N; ++i) {
+      const float2 p = unpack2(f[i]);
+      f[i] = pack2(p.x < act.a ? 0.f : p.x, p.y < act.a ? 0.f : p.y);
+    }
   } else if (act.kind == kActGate) {
+    const f2 a = both(act.a), b = both(act.b);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float z = act_inside(f[i]);
-      f[i] *= rcp_fast(1.f + exp2_fast(-kLog2e * (z * fmaf(act.b * z, z, act.a))));
+      const f2 z = act_inside2(f[i]);
+      f[i] = mul2(f[i], rcp_fast2(add2(exp2_fast2(mul2(z, fma2(b, mul2(z, z), a))), both(1.f))));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      float bell;
-      f[i] *= normal_below(act_inside(f[i]), bell);
+      f2 bell;
+      f[i] = mul2(f[i], normal_below2(act_inside2(f[i]), bell));
     }
   }
 }
 
 // g[i] *= act'(z[i]); relu has slope 0 at 0, and where z is below it the
-// product is 0 whatever g is.
+// product is 0 whatever g is.  With s = 1 / (1 + exp(-u)) a gate's slope is
+// s + s (1 - s) z u'; u, u' come scaled by -log2 e, undone by -ln 2.
 template <int N>
-__device__ __forceinline__ void act_slopes(float (&g)[N], const float (&z)[N], const Act& act) {
+__device__ __forceinline__ void act_slopes(f2 (&g)[N], const f2 (&z)[N], const Act& act) {
   if (act.kind == kActClamp) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) g[i] = z[i] <= act.a ? 0.f : g[i];
+    for (int i = 0; i < N; ++i) {
+      const float2 p = unpack2(z[i]), q = unpack2(g[i]);
+      g[i] = pack2(p.x <= act.a ? 0.f : q.x, p.y <= act.a ? 0.f : q.y);
+    }
   } else if (act.kind == kActGate) {
+    const f2 a = both(act.a), b = both(act.b), b3 = both(3.f * act.b);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float v = act_inside(z[i]), bv2 = act.b * v * v;
-      const float s = rcp_fast(1.f + exp2_fast(-kLog2e * (v * (act.a + bv2))));
-      g[i] *= s * fmaf(v * (1.f - s), fmaf(3.f, bv2, act.a), 1.f);
+      const f2 v = act_inside2(z[i]), vv = mul2(v, v);
+      const f2 s = rcp_fast2(add2(exp2_fast2(mul2(v, fma2(b, vv, a))), both(1.f)));
+      const f2 m = mul2(mul2(v, fma2(b3, vv, a)), fma2(s, both(kLn2), both(-kLn2)));
+      g[i] = mul2(g[i], fma2(s, m, s));
     }
   } else {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const float v = act_inside(z[i]);
-      float bell;
-      const float below = normal_below(v, bell);
-      g[i] *= fmaf(v * 0.3989422804014327f, bell, below);
+      const f2 v = act_inside2(z[i]);
+      f2 bell;
+      const f2 below = normal_below2(v, bell);
+      g[i] = mul2(g[i], fma2(mul2(v, both(0.3989422804014327f)), bell, below));
     }
   }
 }

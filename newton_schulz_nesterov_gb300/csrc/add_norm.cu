@@ -76,11 +76,13 @@ __device__ __forceinline__ uint8_t* scale_at(uint8_t* scales, int64_t row, int64
 // Eight values of columns col .. of a row to codes; a warp's lanes together, four
 // consecutive ones a block.
 __device__ __forceinline__ void quantise8(const AddNormFwdArgs& a, const float (&h)[8], int64_t row, int64_t col, bool live) {
-  uint32_t byte = mx8::scale_byte(mx8::max_abs(h), a.round_up);
-  byte = max(byte, __shfl_xor_sync(0xffffffffu, byte, 1));
-  byte = max(byte, __shfl_xor_sync(0xffffffffu, byte, 2));
+  const float m = mx8::max_abs(h);
+  uint32_t key = mx8::keys2(m, m, a.rounding);
+  key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, 1));
+  key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, 2));
   if (!live || col >= mx_blocks(a.cols) * kMxBlock) return;
-  const float inv = mx8::inv_scale(byte);
+  const float inv = mx8::factor_of(mx8::exponent_of(key, 1));
+  const uint32_t byte = mx8::byte_of(key, 1, a.rounding);
   uint2 w = make_uint2(mx8::codes4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv), mx8::codes4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv));
   if (byte == 255u) w = make_uint2(0, 0);
   *reinterpret_cast<uint2*>(a.q + row * mx_pitch(a.cols, 8) + col) = w;

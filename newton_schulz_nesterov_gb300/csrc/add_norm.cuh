@@ -13,6 +13,7 @@
 #include <stdint.h>
 
 #include "dropout.cuh"
+#include "mx8.cuh"
 
 namespace dmuon {
 
@@ -25,7 +26,7 @@ struct AddNormFwdArgs {
   int64_t rows, cols, ldx, ldf, ldy, ldh;
   float eps;
   Drop drop;
-  uint32_t round_up;            // of the scale bytes (mx8.cuh)
+  mx8::Rounding rounding;       // of the scale bytes
   int vec;                      // rows and w 16-byte aligned
 };
 

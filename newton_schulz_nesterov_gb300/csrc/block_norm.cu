@@ -12,6 +12,7 @@
 #include "../../include/dmuon.h"
 #include "block_norm.cuh"
 #include "bounded_wait.cuh"
+#include "f32x2.cuh"
 #include "pieces.cuh"
 #include "ptx.cuh"
 
@@ -215,34 +216,6 @@ __device__ __forceinline__ bool row_sum(float (&v)[N], const RowUnit& u, RowSums
 #pragma unroll
     for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   return true;
-}
-
-// Two fp32 values in one 64-bit register, for the packed fp32 instructions.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 pack2(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ f2 both(float v) { return pack2(v, v); }
-__device__ __forceinline__ float2 unpack2(f2 v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float add_up(f2 v) {
-  const float2 p = unpack2(v);
-  return p.x + p.y;
 }
 
 // A chunk: eight values of one row in their type.

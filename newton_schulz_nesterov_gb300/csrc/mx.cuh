@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include "act.cuh"
+#include "mx8.cuh"
 
 namespace dmuon {
 
@@ -55,7 +56,7 @@ struct Mx8Args {
   float* parts;                     // [chunks][part_ld] column sums, or nullptr
   int64_t part_ld;
   int64_t tiles;                    // tiles of 128 rows a CTA goes down
-  uint32_t round_up;                // added to a magnitude's bits ahead of taking its exponent
+  mx8::Rounding rounding;
   int vec;                          // every matrix's rows are 16-byte aligned
 };
 
@@ -106,6 +107,7 @@ cudaError_t launch_mx_linear4_pair(const MxLinearArgs& a, int pairs, cudaStream_
 cudaError_t mx_linear8_configure();
 cudaError_t launch_mx_linear8(const MxLinearArgs& a, int nt, int split, cudaStream_t s);
 cudaError_t launch_mx_linear8_pair(const MxLinearArgs& a, int pairs, cudaStream_t s);
+cudaError_t mx8_configure();
 // grad: dout * act'(pre) in place of src.
 cudaError_t launch_mx8_tiles(const Mx8Args& a, int dtype, bool grad, cudaStream_t s);
 cudaError_t launch_mx8_dequant(const MxDequantArgs& a, int dtype, cudaStream_t s);

@@ -31,23 +31,33 @@ __device__ __forceinline__ float max_abs(const float (&v)[N]) {
   return m;
 }
 
-// Scale byte of a magnitude.  It does not fall as the magnitude grows, so that
-// the largest byte of a block's parts is the block's.
+// Exponents are found from the high halves of magnitudes' bits, which do not fall
+// as a magnitude grows: a block's parts are compared by them, two in a word.
 // amax = 1.m x 2^(ex-127): floor takes ex - 8; 448 = 1.75 x 2^8, so ceil takes
 // one more where 1.m > 1.75, which is where adding 0x1FFFFF to the bits carries
-// into the exponent.
-constexpr uint32_t kFloor = 0, kCeil = 0x1FFFFFu;
-__device__ __forceinline__ uint32_t scale_byte(float amax, uint32_t round_up) {
+// into the exponent.  What is not finite is then put above every finite one.
+struct Rounding {
+  uint32_t up;      // added to the bits: 0 (floor), 0x1FFFFF (ceil)
+  uint32_t not_finite;  // the least half of one that is not
+};
+__host__ __device__ constexpr Rounding rounding_of(bool ceil) { return ceil ? Rounding{0x1FFFFFu, 0xFFFFu} : Rounding{0u, 0x7F80u}; }
+__device__ __forceinline__ uint32_t key_bits(float amax, const Rounding& r) {
   const uint32_t bits = __float_as_uint(amax);
-  const uint32_t byte = max((bits + round_up) >> 23, 8u) - 8u;
-  return bits >= 0x7F800000u ? 255u : byte;
+  if (r.up == 0) return bits;
+  return bits >= 0x7F800000u ? 0xFFFF0000u : bits + r.up;
 }
-
-// 2^(127 - byte), by which a block's values are multiplied; 0 for byte 255.
-__device__ __forceinline__ float inv_scale(uint32_t byte) { return byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23); }
-
-// Larger halves of two words.
+// The keys of two magnitudes, the first in the low half.
+__device__ __forceinline__ uint32_t keys2(float a, float b, const Rounding& r) { return __byte_perm(key_bits(a, r), key_bits(b, r), 0x7632); }
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
+__device__ __forceinline__ bool any_not_finite(uint32_t two, const Rounding& r) { return (two & 0xFFFFu) >= r.not_finite || (two >> 16) >= r.not_finite; }
+
+// max(ex, 8) of a key; the scale byte is 8 less (255 where the key is not finite),
+// and 2^(127 - byte) the factor of the block's values.
+__device__ __forceinline__ uint32_t exponent_of(uint32_t two, int half) { return max(half ? two >> 23 : (two >> 7) & 0x1FFu, 8u); }
+__device__ __forceinline__ uint32_t byte_of(uint32_t two, int half, const Rounding& r) {
+  return (half ? two >> 16 : two & 0xFFFFu) >= r.not_finite ? 255u : exponent_of(two, half) - 8u;
+}
+__device__ __forceinline__ float factor_of(uint32_t exponent) { return __uint_as_float((262u - exponent) << 23); }
 
 // Four scaled values to four codes, the first in the low byte.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {

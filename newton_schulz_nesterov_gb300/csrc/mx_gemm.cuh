@@ -291,7 +291,16 @@ __device__ __forceinline__ void put(const MxLinearArgs& a, int64_t row, int64_t 
     for (int j = 0; j < N; ++j)
       if (j < n) pre[DOWN ? j * a.ldpre : j] = narrow<T>(f[j]);
   }
-  act_values(f, a.act);
+  f2 g[N / 2];
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) g[j] = pack2(f[2 * j], f[2 * j + 1]);
+  act_values(g, a.act);
+#pragma unroll
+  for (int j = 0; j < N / 2; ++j) {
+    const float2 p = unpack2(g[j]);
+    f[2 * j] = p.x;
+    f[2 * j + 1] = p.y;
+  }
   T* d = (T*)a.d + row * a.ldd + col;
 #pragma unroll
   for (int j = 0; j < N; ++j)
@@ -382,7 +391,16 @@ __device__ __forceinline__ void store_block(const A& a, int64_t row0, int64_t co
           if (live)
             *reinterpret_cast<uint4*>((T*)a.pre + (at_row + q * kRows) * a.ldpre + at_col) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        act_values(f, a.act);
+        f2 g[2 * kPer];
+#pragma unroll
+        for (int e = 0; e < 2 * kPer; ++e) g[e] = pack2(f[2 * e], f[2 * e + 1]);
+        act_values(g, a.act);
+#pragma unroll
+        for (int e = 0; e < 2 * kPer; ++e) {
+          const float2 p = unpack2(g[e]);
+          f[2 * e] = p.x;
+          f[2 * e + 1] = p.y;
+        }
         if (a.c) {
           const uint32_t o4[4] = {old[q].x, old[q].y, old[q].z, old[q].w};
 #pragma unroll

@@ -15,7 +15,7 @@ namespace {
 
 bool sizes_ok(int64_t rows, int64_t cols) { return rows >= 0 && cols >= 0 && rows <= kMaxSide && cols <= kMaxSide; }
 bool mode_ok(int mode) { return mode == DMUON_MXFP4_SCALE_FLOOR || mode == DMUON_MXFP4_SCALE_CEIL; }
-uint32_t round_up_of(int mode) { return mode == DMUON_MXFP4_SCALE_CEIL ? mx8::kCeil : mx8::kFloor; }
+mx8::Rounding rounding_of(int mode) { return mx8::rounding_of(mode == DMUON_MXFP4_SCALE_CEIL); }
 int64_t part_pitch(int64_t cols) { return (cols + 31) / 32 * 32; }
 
 // No pointer of `outs` is another's or one of `ins` (NULL: none).
@@ -33,6 +33,13 @@ bool apart(const void* const (&outs)[O], const void* const (&ins)[I]) {
 
 // The 128 x 128 tiles of a matrix are numbered by 31 bits.
 bool tiles_ok(int64_t rows, int64_t cols) { return ((rows + 127) / 128) * ((cols + 127) / 128) <= INT32_MAX; }
+
+// Tiles that a CTA goes down, one after the other: as many as fill its ring and
+// still leave six CTAs for each of two on an SM, so that their ends are spread.
+int64_t tiles_down(const dmuon_ctx* h, int64_t rows, int64_t cols) {
+  const int64_t rt = (rows + 127) / 128, ct = (cols + 127) / 128;
+  return std::max<int64_t>(1, std::min<int64_t>(16, rt * ct / (12 * h->num_sms)));
+}
 
 }  // namespace
 
@@ -61,6 +68,7 @@ int dmuon_mxfp8_quantize(dmuon_handle_t h, const void* src, int dtype, int64_t r
     return fail(h, DMUON_ERR_ARG, "mxfp8_quantize: an output is another or an input");
   if (!tiles_ok(rows, cols)) return fail(h, DMUON_ERR_ARG, "mxfp8_quantize: too many tiles");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
+  if ((rc = ready(h, h->quant8_ready, mx8_configure, "mxfp8_quantize: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   Mx8Args a{};
   a.src = src;
@@ -71,8 +79,8 @@ int dmuon_mxfp8_quantize(dmuon_handle_t h, const void* src, int dtype, int64_t r
   a.row_scales = (uint8_t*)row_scales;
   a.col_data = (uint8_t*)col_data;
   a.col_scales = (uint8_t*)col_scales;
-  a.tiles = 1;
-  a.round_up = round_up_of(scale_mode);
+  a.tiles = tiles_down(h, rows, cols);
+  a.rounding = rounding_of(scale_mode);
   a.vec = rows_aligned(src, ld, dtype);
   LaunchGuard g(h, stream, DMUON_KIND_MX_QUANTIZE);
   const cudaError_t e = launch_mx8_tiles(a, dtype, false, stream);
@@ -172,6 +180,7 @@ int dmuon_act_backward(dmuon_handle_t h, const dmuon_act_backward_t* p, void* st
   if (!aligned(p->d_bias, 4)) return fail(h, DMUON_ERR_ALIGN, "act_backward: d_bias");
   if (!tiles_ok(rows, cols)) return fail(h, DMUON_ERR_ARG, "act_backward: too many tiles");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
+  if ((rc = ready(h, h->quant8_ready, mx8_configure, "act_backward: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   Mx8Args a{};
   a.src = p->dout;
@@ -187,13 +196,11 @@ int dmuon_act_backward(dmuon_handle_t h, const dmuon_act_backward_t* p, void* st
   a.col_scales = (uint8_t*)p->col_scales;
   a.dz = p->dz;
   a.lddz = p->lddz;
-  a.round_up = round_up_of(p->scale_mode);
+  a.rounding = rounding_of(p->scale_mode);
   a.vec = rows_aligned(p->dout, p->lddout, p->dtype) && (!pre || rows_aligned(pre, p->ldpre, p->dtype)) &&
           (!p->dz || rows_aligned(p->dz, p->lddz, p->dtype));
-  // With column sums a CTA goes down several tiles, so that there are few rows
-  // of partial sums, but about six CTAs stay for each of two on an SM.
-  const int64_t rt = (rows + 127) / 128, ct = (cols + 127) / 128;
-  a.tiles = p->d_bias ? std::max<int64_t>(1, std::min<int64_t>(16, rt * ct / (12 * h->num_sms))) : 1;
+  const int64_t rt = (rows + 127) / 128;
+  a.tiles = tiles_down(h, rows, cols);
   const int64_t chunks = (rt + a.tiles - 1) / a.tiles;
   if (p->d_bias) {
     a.part_ld = part_pitch(cols);
@@ -254,7 +261,7 @@ int dmuon_add_norm_forward(dmuon_handle_t h, const dmuon_add_norm_t* p, void* st
   a.ldy = p->ldy;
   a.ldh = p->ldh;
   a.eps = p->eps;
-  a.round_up = round_up_of(p->scale_mode);
+  a.rounding = rounding_of(p->scale_mode);
   a.vec = aligned(p->w, 16) && rows_aligned(p->f, p->ldf, p->dtype) && rows_aligned(p->y, p->ldy, p->dtype) &&
           (!p->x || rows_aligned(p->x, p->ldx, p->dtype)) && (!p->h || rows_aligned(p->h, p->ldh, p->dtype));
   LaunchGuard g(h, stream, DMUON_KIND_ADD_NORM_FWD);
