@@ -38,7 +38,11 @@ inline Act act_of(int code) {
 
 // Past +-1e4 every one of them is 0 or z to the last bit: what would overflow
 // there is taken at the border.
-__device__ __forceinline__ float act_inside(float z) { return z > 1e4f ? 1e4f : z < -1e4f ? -1e4f : z; }
+__device__ __forceinline__ float act_inside(float z) {  // the smaller magnitude, with z's sign; NaN stays
+  float r;
+  asm("min.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(1e4f));
+  return r;
+}
 __device__ __forceinline__ f2 act_inside2(f2 z) {
   const float2 p = unpack2(z);
   return pack2(act_inside(p.x), act_inside(p.y));
@@ -111,26 +115,20 @@ __device__ __forceinline__ void act_values(f2 (&f)[N], const Act& act) {
 // g[i] *= act'(z[i]); relu has slope 0 at 0, and where z is below it the
 // product is 0 whatever g is.  With s = 1 / (1 + exp(-u)) a gate's slope is
 // s + s (1 - s) z u'; u, u' come scaled by -log2 e, undone by -ln 2.
-template <int N>
+template <int KIND, int N>
 __device__ __forceinline__ void act_slopes(f2 (&g)[N], const f2 (&z)[N], const Act& act) {
-  if (act.kind == kActClamp) {
+  const f2 a = both(act.a), b = both(act.b), b3 = both(3.f * act.b);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < N; ++i) {
+    if constexpr (KIND == kActClamp) {
       const float2 p = unpack2(z[i]), q = unpack2(g[i]);
       g[i] = pack2(p.x <= act.a ? 0.f : q.x, p.y <= act.a ? 0.f : q.y);
-    }
-  } else if (act.kind == kActGate) {
-    const f2 a = both(act.a), b = both(act.b), b3 = both(3.f * act.b);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
+    } else if constexpr (KIND == kActGate) {
       const f2 v = act_inside2(z[i]), vv = mul2(v, v);
       const f2 s = rcp_fast2(add2(exp2_fast2(mul2(v, fma2(b, vv, a))), both(1.f)));
       const f2 m = mul2(mul2(v, fma2(b3, vv, a)), fma2(s, both(kLn2), both(-kLn2)));
       g[i] = mul2(g[i], fma2(s, m, s));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
+    } else {
       const f2 v = act_inside2(z[i]);
       f2 bell;
       const f2 below = normal_below2(v, bell);

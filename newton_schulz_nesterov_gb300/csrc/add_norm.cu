@@ -77,16 +77,22 @@ __device__ __forceinline__ uint8_t* scale_at(uint8_t* scales, int64_t row, int64
 // consecutive ones a block.
 __device__ __forceinline__ void quantise8(const AddNormFwdArgs& a, const float (&h)[8], int64_t row, int64_t col, bool live) {
   const float m = mx8::max_abs(h);
-  uint32_t key = mx8::keys2(m, m, a.rounding);
+  uint32_t key = mx8::keys2(m, m, a.up);
   key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, 1));
   key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, 2));
+  uint32_t bad = 0;  // the block holds Inf or NaN
+  if (__any_sync(0xffffffffu, mx8::may_not_be_finite(key))) {
+    bad = mx8::not_finite(m);
+    bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
+    bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+  }
   if (!live || col >= mx_blocks(a.cols) * kMxBlock) return;
-  const float inv = mx8::factor_of(mx8::exponent_of(key, 1));
-  const uint32_t byte = mx8::byte_of(key, 1, a.rounding);
+  const uint32_t ex = mx8::exponents2(key);
+  const float inv = mx8::factors2(ex).y;
   uint2 w = make_uint2(mx8::codes4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv), mx8::codes4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv));
-  if (byte == 255u) w = make_uint2(0, 0);
+  if (bad) w = make_uint2(0, 0);
   *reinterpret_cast<uint2*>(a.q + row * mx_pitch(a.cols, 8) + col) = w;
-  if ((col & 31) == 0) *scale_at(a.q_scales, row, col >> 5, a.cols) = (uint8_t)byte;
+  if ((col & 31) == 0) *scale_at(a.q_scales, row, col >> 5, a.cols) = bad ? 255 : (uint8_t)mx8::byte_of(ex, 1);
 }
 __device__ __forceinline__ void zero_blocks_behind(const AddNormFwdArgs& a, int64_t row, int t, bool live) {
   const int64_t nb = mx_blocks(a.cols);

@@ -26,7 +26,7 @@ struct AddNormFwdArgs {
   int64_t rows, cols, ldx, ldf, ldy, ldh;
   float eps;
   Drop drop;
-  mx8::Rounding rounding;       // of the scale bytes
+  uint32_t up;                  // added to the bits of magnitudes (mx8.cuh)
   int vec;                      // rows and w 16-byte aligned
 };
 

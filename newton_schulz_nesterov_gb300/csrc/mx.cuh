@@ -56,7 +56,7 @@ struct Mx8Args {
   float* parts;                     // [chunks][part_ld] column sums, or nullptr
   int64_t part_ld;
   int64_t tiles;                    // tiles of 128 rows a CTA goes down
-  mx8::Rounding rounding;
+  uint32_t up;                      // added to the bits of magnitudes (mx8.cuh)
   int vec;                          // every matrix's rows are 16-byte aligned
 };
 
@@ -108,8 +108,10 @@ cudaError_t mx_linear8_configure();
 cudaError_t launch_mx_linear8(const MxLinearArgs& a, int nt, int split, cudaStream_t s);
 cudaError_t launch_mx_linear8_pair(const MxLinearArgs& a, int pairs, cudaStream_t s);
 cudaError_t mx8_configure();
-// grad: dout * act'(pre) in place of src.
-cudaError_t launch_mx8_tiles(const Mx8Args& a, int dtype, bool grad, cudaStream_t s);
+cudaError_t launch_mx8_tiles(const Mx8Args& a, int dtype, cudaStream_t s);
+// dout * act'(pre) in place of src.
+cudaError_t mx8_act_configure();
+cudaError_t launch_mx8_act(const Mx8Args& a, int dtype, cudaStream_t s);
 cudaError_t launch_mx8_dequant(const MxDequantArgs& a, int dtype, cudaStream_t s);
 // out[c] = the sum over `n` rows of parts, in a fixed order.
 cudaError_t launch_column_sums(const float* parts, int64_t n, int64_t ld, int64_t cols, float* out, cudaStream_t s);

@@ -31,33 +31,29 @@ __device__ __forceinline__ float max_abs(const float (&v)[N]) {
   return m;
 }
 
-// Exponents are found from the high halves of magnitudes' bits, which do not fall
-// as a magnitude grows: a block's parts are compared by them, two in a word.
-// amax = 1.m x 2^(ex-127): floor takes ex - 8; 448 = 1.75 x 2^8, so ceil takes
-// one more where 1.m > 1.75, which is where adding 0x1FFFFF to the bits carries
-// into the exponent.  What is not finite is then put above every finite one.
-struct Rounding {
-  uint32_t up;      // added to the bits: 0 (floor), 0x1FFFFF (ceil)
-  uint32_t not_finite;  // the least half of one that is not
-};
-__host__ __device__ constexpr Rounding rounding_of(bool ceil) { return ceil ? Rounding{0x1FFFFFu, 0xFFFFu} : Rounding{0u, 0x7F80u}; }
-__device__ __forceinline__ uint32_t key_bits(float amax, const Rounding& r) {
-  const uint32_t bits = __float_as_uint(amax);
-  if (r.up == 0) return bits;
-  return bits >= 0x7F800000u ? 0xFFFF0000u : bits + r.up;
+// Exponents are found from the high halves of magnitudes' bits ("keys"), which do
+// not fall as a magnitude grows: a block's parts are compared by them, two in a
+// word.  amax = 1.m x 2^(ex-127): floor takes ex - 8; 448 = 1.75 x 2^8, so ceil
+// takes one more where 1.m > 1.75, which is where adding 0x1FFFFF to the bits
+// carries into the exponent.  Keys of what is not finite are 0x7F80 or more, as
+// ceil's of magnitudes above 1.75 x 2^127 are: those are then looked at again.
+constexpr uint32_t kFloor = 0u, kCeil = 0x1FFFFFu;
+__device__ __forceinline__ uint32_t keys2(float a, float b, uint32_t up) {  // the first in the low half
+  return __byte_perm(__float_as_uint(a) + up, __float_as_uint(b) + up, 0x7632);
 }
-// The keys of two magnitudes, the first in the low half.
-__device__ __forceinline__ uint32_t keys2(float a, float b, const Rounding& r) { return __byte_perm(key_bits(a, r), key_bits(b, r), 0x7632); }
 __device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) { return __vmaxu2(a, b); }
-__device__ __forceinline__ bool any_not_finite(uint32_t two, const Rounding& r) { return (two & 0xFFFFu) >= r.not_finite || (two >> 16) >= r.not_finite; }
+__device__ __forceinline__ bool may_not_be_finite(uint32_t two) { return (two & 0xFFFFu) >= 0x7F80u || two >= 0x7F800000u; }
+__device__ __forceinline__ bool not_finite(float amax) { return __float_as_uint(amax) >= 0x7F800000u; }
 
-// max(ex, 8) of a key; the scale byte is 8 less (255 where the key is not finite),
-// and 2^(127 - byte) the factor of the block's values.
-__device__ __forceinline__ uint32_t exponent_of(uint32_t two, int half) { return max(half ? two >> 23 : (two >> 7) & 0x1FFu, 8u); }
-__device__ __forceinline__ uint32_t byte_of(uint32_t two, int half, const Rounding& r) {
-  return (half ? two >> 16 : two & 0xFFFFu) >= r.not_finite ? 255u : exponent_of(two, half) - 8u;
+// The exponents of two keys where they stand in an fp32's high half, not below 8:
+// the scale byte is 8 less (255 for a block that is not finite), 2^(127 - byte)
+// the factor of the block's values.
+__device__ __forceinline__ uint32_t exponents2(uint32_t two) { return __vmaxu2(two, 0x04000400u) & 0xFF80FF80u; }
+__device__ __forceinline__ uint32_t byte_of(uint32_t exponents, int half) { return (half ? exponents >> 23 : (exponents >> 7) & 0x1FFu) - 8u; }
+__device__ __forceinline__ float2 factors2(uint32_t exponents) {  // (262 - exponent) << 23
+  const uint32_t f = 0x83008300u - exponents;
+  return make_float2(__uint_as_float(f << 16), __uint_as_float(f & 0xFFFF0000u));
 }
-__device__ __forceinline__ float factor_of(uint32_t exponent) { return __uint_as_float((262u - exponent) << 23); }
 
 // Four scaled values to four codes, the first in the low byte.
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {

@@ -15,7 +15,7 @@ namespace {
 
 bool sizes_ok(int64_t rows, int64_t cols) { return rows >= 0 && cols >= 0 && rows <= kMaxSide && cols <= kMaxSide; }
 bool mode_ok(int mode) { return mode == DMUON_MXFP4_SCALE_FLOOR || mode == DMUON_MXFP4_SCALE_CEIL; }
-mx8::Rounding rounding_of(int mode) { return mx8::rounding_of(mode == DMUON_MXFP4_SCALE_CEIL); }
+uint32_t up_of(int mode) { return mode == DMUON_MXFP4_SCALE_CEIL ? mx8::kCeil : mx8::kFloor; }
 int64_t part_pitch(int64_t cols) { return (cols + 31) / 32 * 32; }
 
 // No pointer of `outs` is another's or one of `ins` (NULL: none).
@@ -80,10 +80,10 @@ int dmuon_mxfp8_quantize(dmuon_handle_t h, const void* src, int dtype, int64_t r
   a.col_data = (uint8_t*)col_data;
   a.col_scales = (uint8_t*)col_scales;
   a.tiles = tiles_down(h, rows, cols);
-  a.rounding = rounding_of(scale_mode);
+  a.up = up_of(scale_mode);
   a.vec = rows_aligned(src, ld, dtype);
   LaunchGuard g(h, stream, DMUON_KIND_MX_QUANTIZE);
-  const cudaError_t e = launch_mx8_tiles(a, dtype, false, stream);
+  const cudaError_t e = launch_mx8_tiles(a, dtype, stream);
   if (e != cudaSuccess) return fail(h, cuda_err(e), "mxfp8_quantize launch", e);
   h->last_stream = stream;
   return DMUON_OK;
@@ -180,7 +180,7 @@ int dmuon_act_backward(dmuon_handle_t h, const dmuon_act_backward_t* p, void* st
   if (!aligned(p->d_bias, 4)) return fail(h, DMUON_ERR_ALIGN, "act_backward: d_bias");
   if (!tiles_ok(rows, cols)) return fail(h, DMUON_ERR_ARG, "act_backward: too many tiles");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
-  if ((rc = ready(h, h->quant8_ready, mx8_configure, "act_backward: configure"))) return rc;
+  if ((rc = pre ? ready(h, h->act_ready, mx8_act_configure, "act_backward: configure") : ready(h, h->quant8_ready, mx8_configure, "act_backward: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   Mx8Args a{};
   a.src = p->dout;
@@ -196,7 +196,7 @@ int dmuon_act_backward(dmuon_handle_t h, const dmuon_act_backward_t* p, void* st
   a.col_scales = (uint8_t*)p->col_scales;
   a.dz = p->dz;
   a.lddz = p->lddz;
-  a.rounding = rounding_of(p->scale_mode);
+  a.up = up_of(p->scale_mode);
   a.vec = rows_aligned(p->dout, p->lddout, p->dtype) && (!pre || rows_aligned(pre, p->ldpre, p->dtype)) &&
           (!p->dz || rows_aligned(p->dz, p->lddz, p->dtype));
   const int64_t rt = (rows + 127) / 128;
@@ -213,7 +213,7 @@ int dmuon_act_backward(dmuon_handle_t h, const dmuon_act_backward_t* p, void* st
   }
   LaunchGuard g(h, stream, DMUON_KIND_ACT_BWD);
   cudaError_t e = cudaSuccess;
-  if (rows > 0) e = launch_mx8_tiles(a, p->dtype, true, stream);
+  if (rows > 0) e = pre ? launch_mx8_act(a, p->dtype, stream) : launch_mx8_tiles(a, p->dtype, stream);
   if (e == cudaSuccess && p->d_bias && chunks != 1) {
     if (rows > 0) ++h->launches;
     e = launch_column_sums(a.parts, chunks, a.part_ld, cols, p->d_bias, stream);
@@ -261,7 +261,7 @@ int dmuon_add_norm_forward(dmuon_handle_t h, const dmuon_add_norm_t* p, void* st
   a.ldy = p->ldy;
   a.ldh = p->ldh;
   a.eps = p->eps;
-  a.rounding = rounding_of(p->scale_mode);
+  a.up = up_of(p->scale_mode);
   a.vec = aligned(p->w, 16) && rows_aligned(p->f, p->ldf, p->dtype) && rows_aligned(p->y, p->ldy, p->dtype) &&
           (!p->x || rows_aligned(p->x, p->ldx, p->dtype)) && (!p->h || rows_aligned(p->h, p->ldh, p->dtype));
   LaunchGuard g(h, stream, DMUON_KIND_ADD_NORM_FWD);
