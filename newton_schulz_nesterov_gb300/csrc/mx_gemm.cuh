@@ -360,6 +360,9 @@ __device__ __forceinline__ void store_block(const A& a, int64_t row0, int64_t co
     const int64_t step = (int64_t)kRows * a.ldd;
     if constexpr (std::is_same<A, MxLinearArgs>::value) {
       const int64_t at_row = row0 + lr, at_col = col0 + lc * 4 * kPer;
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        *reinterpret_cast<uint4*>(scratch + lane * 36 + q * 4) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       uint4 old[kLanes];
       if (a.c) {
         const T* c = (const T*)a.c + at_row * a.ldc + at_col;
@@ -373,9 +376,6 @@ __device__ __forceinline__ void store_block(const A& a, int64_t row0, int64_t co
         const float4 b = a.bias ? *reinterpret_cast<const float4*>(a.bias + at_col + e) : make_float4(0.f, 0.f, 0.f, 0.f);
         bias[e] = b.x; bias[e + 1] = b.y; bias[e + 2] = b.z; bias[e + 3] = b.w;
       }
-#pragma unroll
-      for (int q = 0; q < 8; ++q)
-        *reinterpret_cast<uint4*>(scratch + lane * 36 + q * 4) = make_uint4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
       __syncwarp();
 #pragma unroll
       for (int q = 0; q < kLanes; ++q) {
@@ -744,13 +744,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 // 512): 16384 x 14336 x 4096 to bf16 265 us, 7.26 PFLOP/s.
 // ---------------------------------------------------------------------------
 constexpr int kPairN = 5;
-constexpr int kPairThreads = 320;
 constexpr int kPairSets = 4;
-template <int BITS>
+// A tile's products take 18000 clocks at K = 4096; its epilogue by four warps takes
+// about as many without, and 26000 with bias, GELU and two outputs (8192 x 14336 x
+// 4096 460 and 612 thousand clocks), so that one has eight warps.
+template <int BITS, bool EPI>
 struct Pair {
+  static constexpr int kEpiWarps = EPI ? 8 : 4;
+  static constexpr int kThreads = 32 * (2 + kEpiWarps + 4);
   static constexpr int kScales = Fmt<BITS>::kScaleBytes * 3;                       // A's 128 rows, B's 256
   static constexpr int kStage = (2 * kPBytes + kScales + 1023) / 1024 * 1024;      // 35 KB, 34 at 8 bits
-  static constexpr int kSmem = 1024 + kPairN * kStage + 4 * kScratch * 4 + 256;
+  static constexpr int kSmem = 1024 + kPairN * kStage + kEpiWarps * kScratch * 4 + 256;
   static constexpr int kSetCols = BITS == 4 ? 24 : 16;                             // A's words from 0, B's from 8
   static constexpr int kScaleCol = 512 - kPairSets * kSetCols;                     // 416, 448
   static constexpr int kAccStride = kScaleCol - 256;                               // 160, 192
@@ -806,13 +810,13 @@ __device__ __forceinline__ void tile_of(int t, int tm, int tn, int& m, int& n) {
 }
 
 template <int BITS, bool EPI, typename T>
-__global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __grid_constant__ GemmArgs<EPI> a) {
+__global__ void __launch_bounds__(Pair<BITS, EPI>::kThreads, 1) mx_gemm_pair_kernel(const __grid_constant__ GemmArgs<EPI> a) {
   using F = Fmt<BITS>;
-  using P = Pair<BITS>;
+  using P = Pair<BITS, EPI>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024u - (ptx::smem_addr(smem_raw) & 1023u)) & 1023u);
   uint32_t* scratch = reinterpret_cast<uint32_t*>(stages + kPairN * P::kStage);
-  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + 4 * kScratch);
+  uint64_t* full = reinterpret_cast<uint64_t*>(scratch + P::kEpiWarps * kScratch);
   uint64_t* empty = full + kPairN;
   uint64_t* tfull = empty + kPairN;     // [2] accumulator complete
   uint64_t* tempty = tfull + 2;         // [2] accumulator stored
@@ -847,9 +851,9 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_addr(tfull + i), 1);
-      ptx::mbar_init(ptx::smem_addr(tempty + i), 8);  // 4 epilogue warps x 2 ranks
+      ptx::mbar_init(ptx::smem_addr(tempty + i), 2 * P::kEpiWarps);  // of both ranks
     }
-    ptx::mbar_init(ptx::smem_addr(tshared), 8);
+    ptx::mbar_init(ptx::smem_addr(tshared), 2 * P::kEpiWarps);
     for (int i = 0; i < kPairSets; ++i) ptx::mbar_init(ptx::smem_addr(sfull + i), 8);  // 4 scale warps x 2 ranks
     ptx::mbar_init(ptx::smem_addr(drain), 1);
     *abort_flag = 0;
@@ -935,7 +939,7 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
       }
       if (lane == 0) *multiplied = issued;
     }
-  } else if (warp >= 6) {
+  } else if (warp >= 2 + P::kEpiWarps) {
     // ------------------------------------------------------------ scales
     const uint32_t ready0 = ptx::smem_addr(sready), empty0 = ptx::smem_addr(empty);
     const uint32_t sfull0 = ptx::mapa_shared(ptx::smem_addr(sfull), 0);
@@ -994,30 +998,59 @@ __global__ void __launch_bounds__(kPairThreads, 1) mx_gemm_pair_kernel(const __g
       if (!bounded_wait_warp(ptx::smem_addr(tfull + acc), (tc >> 1) & 1u, abort_flag, a.err, tmo)) break;
       ptx::tc_fence_after();
       const uint32_t tq = tmem + acc * P::kAccStride + ((uint32_t)(quad * 32) << 16);
-      {  // the shared columns first: the last 96 (8 bits: 64) of accumulator 0, the first of 1
-        const int c = acc ? 0 : P::kAccStride;
-        uint32_t v[P::kSharedCols];
-        if constexpr (BITS == 4) tmem_ld96(tq + c, v);
-        else tmem_ld64(tq + c, v);
+      constexpr int kShared = P::kSharedCols / 32, kRest = P::kAccStride / 32;
+      const int shared0 = acc ? 0 : P::kAccStride, rest0 = acc ? P::kSharedCols : 0;
+      // The shared columns first: the last 96 (8 bits: 64) of accumulator 0, the first of 1.
+      if constexpr (EPI) {
+        // Of the two warps of a quarter one has the shared blocks 0, 2 and the
+        // others 1, 3, .., one the shared block 1 and the others 0, 2, ..: four each.
+        const int h = (warp - 2) >> 2;
+        constexpr int kMine = (kShared + 1) / 2;
+        uint32_t v[kMine][32];
+#pragma unroll
+        for (int q = 0; q < kMine; ++q)
+          if (h + 2 * q < kShared) ptx::tmem_ld32(tq + shared0 + (h + 2 * q) * 32, v[q]);
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tshared), 0));
 #pragma unroll
-        for (int q = 0; q < P::kSharedCols / 32; ++q)
-          if (col0 + c + q * 32 < a.q_rows) store_block<T>(a, row0, col0 + c + q * 32, a.p_rows, a.q_rows, v + q * 32, mine, lane);
-      }
-      constexpr int kRest = P::kAccStride / 32;
+        for (int q = 0; q < kMine; ++q)
+          if (h + 2 * q < kShared && col0 + shared0 + (h + 2 * q) * 32 < a.q_rows)
+            store_block<T>(a, row0, col0 + shared0 + (h + 2 * q) * 32, a.p_rows, a.q_rows, v[q], mine, lane);
 #pragma unroll 1
-      for (int i = 0; i < kRest; ++i) {
-        const int c = (acc ? P::kSharedCols : 0) + i * 32;
-        uint32_t v[32];
-        ptx::tmem_ld32(tq + c, v);
-        if (i == kRest - 1) {
-          ptx::tc_fence_before();
-          __syncwarp();
-          if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tempty + acc), 0));
+        for (int i = 1 - h; i < kRest; i += 2) {
+          const int c = rest0 + i * 32;
+          ptx::tmem_ld32(tq + c, v[0]);
+          if (i + 2 >= kRest) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tempty + acc), 0));
+          }
+          if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, v[0], mine, lane);
         }
-        if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, v, mine, lane);
+      } else {
+        uint32_t v[P::kSharedCols];
+        if constexpr (BITS == 4) tmem_ld96(tq + shared0, v);
+        else tmem_ld64(tq + shared0, v);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tshared), 0));
+#pragma unroll
+        for (int q = 0; q < kShared; ++q)
+          if (col0 + shared0 + q * 32 < a.q_rows)
+            store_block<T>(a, row0, col0 + shared0 + q * 32, a.p_rows, a.q_rows, v + q * 32, mine, lane);
+#pragma unroll 1
+        for (int i = 0; i < kRest; ++i) {
+          const int c = rest0 + i * 32;
+          uint32_t w[32];
+          ptx::tmem_ld32(tq + c, w);
+          if (i == kRest - 1) {
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tempty + acc), 0));
+          }
+          if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, w, mine, lane);
+        }
       }
     }
   }
@@ -1057,7 +1090,7 @@ struct MxKernels {
     if ((e = f(mx_gemm_kernel<BITS, EPI, 32, T>, Cfg<BITS, 32>::kSmem)) != cudaSuccess) return e;
     if ((e = f(mx_gemm_kernel<BITS, EPI, 64, T>, Cfg<BITS, 64>::kSmem)) != cudaSuccess) return e;
     if ((e = f(mx_gemm_kernel<BITS, EPI, 128, T>, Cfg<BITS, 128>::kSmem)) != cudaSuccess) return e;
-    return f(mx_gemm_pair_kernel<BITS, EPI, T>, Pair<BITS>::kSmem);
+    return f(mx_gemm_pair_kernel<BITS, EPI, T>, Pair<BITS, EPI>::kSmem);
   }
 
   static cudaError_t configure() {
@@ -1101,7 +1134,7 @@ struct MxKernels {
   }
 
   static cudaError_t launch_pair(const Args& a, int pairs, cudaStream_t s) {
-    auto go = [&](auto kernel) { return start(kernel, a, 2 * (int64_t)pairs, 2, kPairThreads, Pair<BITS>::kSmem, s); };
+    auto go = [&](auto kernel) { return start(kernel, a, 2 * (int64_t)pairs, 2, Pair<BITS, EPI>::kThreads, Pair<BITS, EPI>::kSmem, s); };
     if (a.dtype == DMUON_BF16) return go(mx_gemm_pair_kernel<BITS, EPI, __nv_bfloat16>);
     if (a.dtype == DMUON_F16) return go(mx_gemm_pair_kernel<BITS, EPI, __half>);
     return go(mx_gemm_pair_kernel<BITS, EPI, float>);

@@ -57,7 +57,7 @@ def act_bar(z, act):
 
 
 # One CTA a tile with few rows of A; K split 2, 4 and 8 ways; 64 and 128 rows; CTA pairs.
-SIZES = [(1, 1, 1), (1, 4096, 333), (3, 129, 2061), (5, 600, 4096), (33, 257, 96), (50, 1111, 640), (77, 300, 31), (128, 128, 129),
+SIZES = [(1, 1, 1), (1, 4096, 333), (1, 300, 14336), (2, 1000, 4100), (3, 129, 2061), (4, 33, 6000), (5, 600, 4096), (8, 200, 2080), (9, 600, 4096), (33, 257, 96), (50, 1111, 640), (77, 300, 31), (128, 128, 129),
          (200, 130, 1024), (300, 264, 64), (257, 1000, 4097), (2100, 2600, 1300), (2560, 2304, 257)]
 
 
@@ -92,7 +92,7 @@ def test_whole_numbers_are_exact(handle, m, n, k, bits, odd):
     assert handle.status()[0] == 0
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 4096, 333), (3, 129, 2061), (50, 1111, 640), (200, 130, 1024), (257, 1000, 4097), (2100, 2600, 300)])
+@pytest.mark.parametrize("m,n,k", [(1, 4096, 333), (2, 100, 9000), (3, 129, 2061), (4, 700, 1024), (8, 55, 300), (9, 300, 3000), (50, 1111, 640), (200, 130, 1024), (257, 1000, 4097), (2100, 2600, 300)])
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("bits,act,with_bias,with_res,odd", [(8, "none", True, True, False), (8, "relu", False, False, True),
                                                              (8, "silu", True, True, True), (8, "gelu", True, False, False),
@@ -175,7 +175,7 @@ def test_refusals(handle):
     assert not out.any()
 
 
-@pytest.mark.parametrize("m,n,k", [(1, 30000, 4500), (300, 600, 600), (1, 4096, 4096), (2100, 2600, 650), (2100, 2600, 2500)])
+@pytest.mark.parametrize("m,n,k", [(9, 30000, 4500), (300, 600, 600), (9, 4096, 4096), (2100, 2600, 650), (2100, 2600, 2500)])
 def test_waits_that_run_out(handle, m, n, k):
     r = np.random.RandomState(1)
     a, b = dm.dmuon_mxfp8_empty(m, k), dm.dmuon_mxfp8_empty(n, k)
