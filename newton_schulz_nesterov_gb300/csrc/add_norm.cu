@@ -4,9 +4,11 @@
 //
 // A row is held by a unit of threads, V chunks of eight columns a thread, so that
 // it is read once: part of a warp up to 256 columns, a warp up to 512, a CTA up
-// to 16384.  A unit goes from row to row with its columns' weights (and, backward,
-// their sums) in registers, and loads the next row ahead of the present one's
-// sums.  Longer rows are read in two passes by one CTA (add_norm_long_*).
+// to 16384 (backward: 8192).  A unit goes from row to row with its columns' weights
+// (and, backward, their sums) in registers; the coming rows are on their way to a
+// ring in shared memory (cp.async: no registers), each warp's part its own, so that
+// only the row's sums meet at a barrier.  Longer rows are read in two passes by one
+// CTA (add_norm_long_*).
 // A block of 32 columns is four lanes, so its scale byte takes two exchanges.
 #include <algorithm>
 
@@ -15,6 +17,7 @@
 #include "chunk8.cuh"
 #include "mx.cuh"
 #include "mx8.cuh"
+#include "ptx.cuh"
 
 namespace dmuon {
 
@@ -42,7 +45,11 @@ struct Unit {
 
 // Sum over a unit, in a fixed order, to all of it.  Consecutive calls of a CTA
 // alternate between the halves of `red`: one is written again only after the
-// next call's barrier, when every thread has read it.
+// next call's barrier, when every thread has read it.  What no warp writes is zero
+// (clear_sums, ahead of a barrier or of the first call's).
+__device__ __forceinline__ void clear_sums(float (*red)[16]) {
+  if (threadIdx.x < 32 && threadIdx.x % 16 >= blockDim.x / 32) red[threadIdx.x / 16][threadIdx.x % 16] = 0.f;
+}
 template <bool MULTI>
 __device__ __forceinline__ float unit_sum(float v, const Unit& u, float (*red)[16], uint32_t& calls) {
 #pragma unroll
@@ -52,12 +59,14 @@ __device__ __forceinline__ float unit_sum(float v, const Unit& u, float (*red)[1
   float* mine = red[calls++ & 1];
   if (u.lane == 0) mine[u.warp] = v;
   __syncthreads();
-  const int n = blockDim.x >> 5;
-  v = 0.f;
-#pragma unroll
-  for (int i = 0; i < 16; ++i)
-    if (i < n) v += mine[i];
-  return v;
+  const float4* four = reinterpret_cast<const float4*>(mine);
+  float4 p = four[0], q = four[1];
+  if (blockDim.x > 256) {
+    const float4 r = four[2], t = four[3];
+    p.x += r.x; p.y += r.y; p.z += r.z; p.w += r.w;
+    q.x += t.x; q.y += t.y; q.z += t.z; q.w += t.w;
+  }
+  return ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
 }
 
 // Scale bytes past the matrix are zero: rows from `rows` to the tile's end, by
@@ -75,7 +84,7 @@ __device__ __forceinline__ uint8_t* scale_at(uint8_t* scales, int64_t row, int64
 
 // Eight values of columns col .. of a row to codes; a warp's lanes together, four
 // consecutive ones a block.
-__device__ __forceinline__ void quantise8(const AddNormFwdArgs& a, const float (&h)[8], int64_t row, int64_t col, bool live) {
+__device__ __forceinline__ void quantise8(const AddNormFwdArgs& a, const float (&h)[8], int64_t row, int col, bool live) {
   const float m = mx8::max_abs(h);
   uint32_t key = mx8::keys2(m, m, a.up);
   key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, 1));
@@ -86,7 +95,7 @@ __device__ __forceinline__ void quantise8(const AddNormFwdArgs& a, const float (
     bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
     bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
   }
-  if (!live || col >= mx_blocks(a.cols) * kMxBlock) return;
+  if (!live || col >= (int)mx_blocks(a.cols) * kMxBlock) return;
   const uint32_t ex = mx8::exponents2(key);
   const float inv = mx8::factors2(ex).y;
   uint2 w = make_uint2(mx8::codes4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv), mx8::codes4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv));
@@ -99,76 +108,195 @@ __device__ __forceinline__ void zero_blocks_behind(const AddNormFwdArgs& a, int6
   if (live && t < mx_scale_cols(a.cols) * 4 - nb) *scale_at(a.q_scales, row, nb + t, a.cols) = 0;
 }
 
-template <typename T, bool VEC, int V, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? 512 : 256) add_norm_fwd_kernel(const AddNormFwdArgs a, int tpr) {
-  __shared__ float red[2][16];
+// Rows on their way, as shared memory has room for them.
+template <typename T, int V>
+constexpr int depth() { return (sizeof(T) == 4 ? 2 : 3) - (V == 4 ? 1 : 0); }
+
+// The ring of a warp: DEPTH slots of ARRAYS x V runs.  A run is the 16-byte pieces
+// that the chunks of a unit's lanes of this warp lie in, one after the other (rows
+// on any element: one piece more), copied by those lanes piece by piece.
+template <typename T, bool VEC, int V, int ARRAYS, int DEPTH>
+struct Ring {
+  static constexpr int W = words8<T>() / 4;                      // pieces of a lane
+  static constexpr int kRun = (32 * W + (VEC ? 0 : 8)) * 16;     // bytes; up to eight units a warp
+  static constexpr int kSlot = ARRAYS * V * kRun;
+  static constexpr int kWarp = DEPTH * kSlot;
+  const uint8_t* mine;     // this lane's first piece in slot 0
+  uint32_t copies;         // where it copies its first piece to
+  int lanes, l;            // of its unit in this warp; its place among them
+  __device__ __forceinline__ Ring(uint8_t* smem, const Unit& u) {
+    lanes = u.tpr < 32 ? u.tpr : 32;
+    l = u.lane & (lanes - 1);
+    const int run = u.lane / lanes * (lanes * W + (VEC ? 0 : 1)) * 16;
+    uint8_t* warp = smem + u.warp * kWarp;
+    mine = warp + run + l * W * 16;
+    copies = ptx::smem_addr(warp + run + l * 16);
+  }
+  // Run (array, v) of the slot at `slot` bytes: p its first element (of the unit's
+  // first lane in this warp), left the elements of the row from there on (none:
+  // below 1), inside an address of the matrix.
+  __device__ __forceinline__ void fetch(int slot, int array, int v, const uint8_t* p, int left, const void* inside) const {
+    const uint32_t dst = copies + slot + (array * V + v) * kRun;
+    const uint32_t m = VEC ? 0u : past16(p);
+    const uint8_t* from = p - m + l * 16;
+    if (left >= lanes * 8) {
+#pragma unroll
+      for (int k = 0; k < W; ++k) copy16(dst + k * lanes * 16, from + k * lanes * 16);
+      if (!VEC && l == 0) copy16(dst + W * lanes * 16, m ? from + W * lanes * 16 : from, (int)m);
+      return;
+    }
+    const int bytes = left > 0 ? min(left, lanes * 8) * (int)sizeof(T) + (int)m : 0;
+    const uint8_t* other = reinterpret_cast<const uint8_t*>(inside) - past16(reinterpret_cast<const uint8_t*>(inside));
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const int at = (k * lanes + l) * 16, n = max(0, min(16, bytes - at));
+      copy16(dst + k * lanes * 16, n ? from + k * lanes * 16 : other, n);
+    }
+    if (!VEC && l == 0) {
+      const int n = max(0, min(16, bytes - W * lanes * 16));
+      copy16(dst + W * lanes * 16, n ? from + W * lanes * 16 : other, n);
+    }
+  }
+  __device__ __forceinline__ void take(f2 (&f)[4], int slot, int array, int v, uint32_t m) const {
+    take8<T, VEC, true>(f, mine + slot + (array * V + v) * kRun, m);
+  }
+};
+
+// The rows of one matrix that a unit goes through: the run that its warp fetches
+// next, and how far a row's first byte is past a 16-byte boundary.
+template <typename T, bool VEC>
+struct Rows {
+  const uint8_t* next;
+  int64_t step;         // bytes from one row of the unit to its next
+  const void* inside;
+  uint32_t first, ld;   // modulo 16
+  __device__ __forceinline__ Rows(const void* base, int64_t ld_, int64_t row, int64_t rows_on, int64_t col) {
+    next = (const uint8_t*)base + (row * ld_ + col) * (int)sizeof(T);
+    step = rows_on * ld_ * (int)sizeof(T);
+    inside = base;
+    first = (uint32_t)(uintptr_t)base;
+    ld = (uint32_t)ld_ * (uint32_t)sizeof(T);
+  }
+  // Of any chunk of the row: chunks are 16 or 32 bytes.
+  __device__ __forceinline__ uint32_t past(int64_t row) const { return VEC ? 0u : (first + (uint32_t)row * ld) & 15u; }
+};
+
+__device__ __forceinline__ void unpack8(float (&o)[8], const f2 (&f)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 p = unpack2(f[i]);
+    o[2 * i] = p.x;
+    o[2 * i + 1] = p.y;
+  }
+}
+__device__ __forceinline__ void load_weights(f2 (&w)[4], const float* p, int n, bool vec) {
+  float f[8];
+  if (vec) load8<float, true>(f, p, n);
+  else load8<float, false>(f, p, n);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = pack2(f[2 * i], f[2 * i + 1]);
+}
+
+// kThreads: of a CTA at most; kCtas: of them on an SM.
+template <typename T, bool VEC, int V, int kThreads, int kCtas, bool MULTI>
+__global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const AddNormFwdArgs a, int tpr) {
+  constexpr int D = depth<T, V>();
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float red[2][16];
   const Unit u(tpr, MULTI);
+  const Ring<T, VEC, V, 2, D> ring(smem, u);
   uint32_t calls = 0;
   const int64_t step = (int64_t)gridDim.x * u.units;
-  int64_t row = (int64_t)blockIdx.x * u.units + u.unit;
+  int64_t row = (int64_t)blockIdx.x * u.units + u.unit, ahead = row;
   int n[V];
-  float w[V][8];
+  f2 w[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * tpr + u.t) * 8;
     n[v] = (int)a.cols - c;
-    load8<float, VEC>(w[v], a.w + c, n[v]);
+    load_weights(w[v], a.w + c, n[v], VEC);
   }
-  if (a.q) zero_rows_behind(a.q_scales, a.rows, a.cols);
-  Raw8<T, VEC> xr[V], fr[V];
-  auto at = [&](const void* base, int64_t r, int64_t ld, int v) { return (const T*)base + r * ld + (v * tpr + u.t) * 8; };
-  auto fetch = [&](int64_t r) {
+  const int run0 = (u.t - ring.l) * 8, next_run = tpr * 8;  // columns of the warp's first run, and from there to the next
+  Rows<T, VEC> x(a.x, a.ldx, row, step, run0), f(a.f, a.ldf, row, step, run0);
+  int fetch_slot = 0;
+  auto fetch = [&]() {
+    const int cols = ahead < a.rows ? (int)a.cols - run0 : 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int k = r < a.rows ? n[v] : 0;
-      load_raw8<T, VEC>(fr[v], at(a.f, r, a.ldf, v), k);
-      if (a.x) load_raw8<T, VEC>(xr[v], at(a.x, r, a.ldx, v), k);
+      const int64_t off = (int64_t)(v * next_run) * (int)sizeof(T);
+      ring.fetch(fetch_slot, 0, v, f.next + off, cols - v * next_run, f.inside);
+      if (a.x) ring.fetch(fetch_slot, 1, v, x.next + off, cols - v * next_run, x.inside);
     }
+    f.next += f.step;
+    x.next += x.step;
+    ahead += step;
+    if ((fetch_slot += ring.kSlot) == ring.kWarp) fetch_slot = 0;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(row);
+#pragma unroll
+  for (int s = 0; s < D; ++s) fetch();
+  if (a.q) zero_rows_behind(a.q_scales, a.rows, a.cols);
+  clear_sums(red);
   const float inv = 1.f / (float)a.cols;
+  T* y_out = (T*)a.y + row * a.ldy + u.t * 8;
+  T* h_out = (T*)a.h + row * a.ldh + u.t * 8;
+  const int64_t y_step = step * a.ldy, h_step = step * a.ldh;
+  int slot = 0;
   for (int64_t base = (int64_t)blockIdx.x * u.units; base < a.rows; base += step, row += step) {  // as often for every unit
     const bool live = MULTI || row < a.rows;
-    float y[V][8];
-    float s = 0.f;
+    f2 y[V][4], s = 0;
+    uint32_t bits[V][4];
+    if (a.drop.cut) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) philox(bits[v], a.drop, (uint32_t)(v * tpr + u.t), (uint32_t)row);
+    }
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    __syncwarp();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      values8<T, VEC>(y[v], fr[v], at(a.f, row, a.ldf, v), n[v]);
-      if (a.drop.cut) {
-        uint32_t bits[4];
-        philox(bits, a.drop, (uint32_t)(v * tpr + u.t), (uint32_t)row);
-        drop8(y[v], a.drop, bits);
-      }
+      ring.take(y[v], slot, 0, v, f.past(row));
+      if (a.drop.cut) drop8(y[v], a.drop, bits[v]);
       if (a.x) {
-        float x[8];
-        values8<T, VEC>(x, xr[v], at(a.x, row, a.ldx, v), n[v]);
+        f2 more[4];
+        ring.take(more, slot, 1, v, x.past(row));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[v][e] += x[e];
+        for (int i = 0; i < 4; ++i) y[v][i] = add2(y[v][i], more[i]);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(y[v][e], y[v][e], s);
+      for (int i = 0; i < 4; ++i) s = fma2(y[v][i], y[v][i], s);
     }
-    fetch(row + step);
-#pragma unroll
-    for (int v = 0; v < V; ++v) store8_warp<T, VEC>((T*)a.y + row * a.ldy + (v * tpr + u.t) * 8, y[v], n[v], u.first, u.last, live);
-    s = unit_sum<MULTI>(s, u, red, calls);
-    const float r = rsqrtf(fmaf(s, inv, a.eps));
-    if (live && u.t == 0) a.rstd[row] = r;
+    __syncwarp();
+    fetch();
+    if ((slot += ring.kSlot) == ring.kWarp) slot = 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[v][e] = y[v][e] * r * w[v][e];
-      if (a.h) store8_warp<T, VEC>((T*)a.h + row * a.ldh + (v * tpr + u.t) * 8, y[v], n[v], u.first, u.last, live);
-      if (a.q) quantise8(a, y[v], row, (v * tpr + u.t) * 8, live);
+      float o[8];
+      unpack8(o, y[v]);
+      store8_warp<T, VEC>(y_out + v * next_run, o, n[v], u.first, u.last, live);
     }
+    y_out += y_step;
+    const float r = rsqrtf(fmaf(unit_sum<MULTI>(add_up(s), u, red, calls), inv, a.eps));
+    if (live && u.t == 0) a.rstd[row] = r;
+    const f2 rr = both(r);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[v][i] = mul2(mul2(y[v][i], rr), w[v][i]);
+      unpack8(o, y[v]);
+      if (a.h) store8_warp<T, VEC>(h_out + v * next_run, o, n[v], u.first, u.last, live);
+      if (a.q) quantise8(a, o, row, (v * tpr + u.t) * 8, live);
+    }
+    h_out += h_step;
     if (a.q) zero_blocks_behind(a, row, u.t, live);
   }
 }
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const AddNormFwdArgs a) {
-  __shared__ float red[2][16];
+  __shared__ __align__(16) float red[2][16];
   const Unit u(kLongThreads, true);
+  clear_sums(red);
   uint32_t calls = 0;
   if (a.q) zero_rows_behind(a.q_scales, a.rows, a.cols);
   const int64_t panels = (a.cols + kLongThreads * 8 - 1) / (kLongThreads * 8);
@@ -189,7 +317,7 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const A
       }
     };
     float s = 0.f, y[8];
-#pragma unroll 2
+#pragma unroll 4
     for (int64_t p = 0; p < panels; ++p) {
       const int64_t c = (p * kLongThreads + threadIdx.x) * 8;
       sum_at(y, c);
@@ -209,7 +337,7 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const A
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
       if (a.h) store8_warp<T, VEC>((T*)a.h + row * a.ldh + c, y, a.cols - c, u.first, u.last, true);
-      if (a.q) quantise8(a, y, row, c, true);
+      if (a.q) quantise8(a, y, row, (int)c, true);
     }
     if (a.q) zero_blocks_behind(a, row, u.t, true);
   }
@@ -226,86 +354,122 @@ __device__ __forceinline__ void into_t(float (&t)[8], float (&sums)[8], const fl
   }
 }
 
-template <typename T, bool VEC, int V, bool MULTI>
-__global__ void __launch_bounds__(MULTI ? 512 : 256) add_norm_bwd_kernel(const AddNormBwdArgs a, int tpr) {
-  __shared__ float red[2][16];
+template <typename T, bool VEC, int V, int kThreads, int kCtas, bool MULTI>
+__global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const AddNormBwdArgs a, int tpr) {
+  constexpr int D = depth<T, V>();
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(16) float red[2][16];
   __shared__ float lines[MULTI ? 1 : 32 * V * 8];
   const Unit u(tpr, MULTI);
+  const Ring<T, VEC, V, 3, D> ring(smem, u);
   uint32_t calls = 0;
   const int64_t step = (int64_t)gridDim.x * u.units;
-  int64_t row = (int64_t)blockIdx.x * u.units + u.unit;
+  int64_t row = (int64_t)blockIdx.x * u.units + u.unit, ahead = row;
   int n[V];
-  float w[V][8], sums[V][8];
+  f2 w[V][4], sums[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = (v * tpr + u.t) * 8;
     n[v] = (int)a.cols - c;
-    load8<float, VEC>(w[v], a.w + c, n[v]);
+    load_weights(w[v], a.w + c, n[v], VEC);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[v][e] = 0.f;
+    for (int i = 0; i < 4; ++i) sums[v][i] = 0;
   }
-  Raw8<T, VEC> dyr[V], dhr[V], yr[V];
-  auto at = [&](const void* base, int64_t r, int64_t ld, int v) { return (const T*)base + r * ld + (v * tpr + u.t) * 8; };
-  float next_r = 0.f;
-  auto fetch = [&](int64_t r) {
-    const bool live = r < a.rows;
+  const int run0 = (u.t - ring.l) * 8, next_run = tpr * 8;  // columns of the warp's first run, and from there to the next
+  Rows<T, VEC> dy(a.dy, a.lddy, row, step, run0), dh(a.dh, a.lddh, row, step, run0), y(a.y, a.ldy, row, step, run0);
+  int fetch_slot = 0;
+  auto fetch = [&]() {
+    const int cols = ahead < a.rows ? (int)a.cols - run0 : 0;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      const int k = live ? n[v] : 0;
-      load_raw8<T, VEC>(dhr[v], at(a.dh, r, a.lddh, v), k);
-      load_raw8<T, VEC>(yr[v], at(a.y, r, a.ldy, v), k);
-      if (a.dy) load_raw8<T, VEC>(dyr[v], at(a.dy, r, a.lddy, v), k);
+      const int64_t off = (int64_t)(v * next_run) * (int)sizeof(T);
+      ring.fetch(fetch_slot, 0, v, dh.next + off, cols - v * next_run, dh.inside);
+      ring.fetch(fetch_slot, 1, v, y.next + off, cols - v * next_run, y.inside);
+      if (a.dy) ring.fetch(fetch_slot, 2, v, dy.next + off, cols - v * next_run, dy.inside);
     }
-    next_r = live ? a.rstd[r] : 0.f;
+    dh.next += dh.step;
+    y.next += y.step;
+    dy.next += dy.step;
+    ahead += step;
+    if ((fetch_slot += ring.kSlot) == ring.kWarp) fetch_slot = 0;
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  fetch(row);
+#pragma unroll
+  for (int s = 0; s < D; ++s) fetch();
+  clear_sums(red);
   const float inv = 1.f / (float)a.cols;
+  float next_r = row < a.rows ? a.rstd[row] : 0.f;
+  T* dx_out = (T*)a.dx + row * a.lddx + u.t * 8;
+  T* df_out = (T*)a.df + row * a.lddf + u.t * 8;
+  const int64_t dx_step = step * a.lddx, df_step = step * a.lddf;
+  int slot = 0;
   for (int64_t base = (int64_t)blockIdx.x * u.units; base < a.rows; base += step, row += step) {
     const bool live = MULTI || row < a.rows;
     const float r = next_r;
-    float dy[V][8], dh[V][8], y[V][8];
-    float s = 0.f;
+    next_r = row + step < a.rows ? a.rstd[row + step] : 0.f;
+    f2 gv[V][4], yv[V][4], dv[V][4], s = 0;
+    asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
+    __syncwarp();
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      values8<T, VEC>(dh[v], dhr[v], at(a.dh, row, a.lddh, v), n[v]);
-      values8<T, VEC>(y[v], yr[v], at(a.y, row, a.ldy, v), n[v]);
-      if (a.dy) values8<T, VEC>(dy[v], dyr[v], at(a.dy, row, a.lddy, v), n[v]);
+      ring.take(gv[v], slot, 0, v, dh.past(row));
+      ring.take(yv[v], slot, 1, v, y.past(row));
+      if (a.dy) ring.take(dv[v], slot, 2, v, dy.past(row));
       else
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dy[v][e] = 0.f;
+        for (int i = 0; i < 4; ++i) dv[v][i] = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(dh[v][e] * w[v][e], y[v][e], s);
+      for (int i = 0; i < 4; ++i) s = fma2(mul2(gv[v][i], w[v][i]), yv[v][i], s);
     }
-    fetch(row + step);
-    s = unit_sum<MULTI>(s, u, red, calls);
-    const float back = r * r * r * (s * inv);
+    __syncwarp();
+    fetch();
+    if ((slot += ring.kSlot) == ring.kWarp) slot = 0;
+    const float total = unit_sum<MULTI>(add_up(s), u, red, calls);
+    const f2 rr = both(r), back = both(-(r * r * r * (total * inv)));  // - r^3 mean(dh w y)
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float t[8];
-      into_t(t, sums[v], dy[v], dh[v], y[v], w[v], r, back);
-      const int64_t c = (v * tpr + u.t) * 8;
-      if (a.dx) store8_warp<T, VEC>((T*)a.dx + row * a.lddx + c, t, n[v], u.first, u.last, live);
+      f2 t[4];
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const f2 g = mul2(gv[v][i], rr);
+        sums[v][i] = fma2(g, yv[v][i], sums[v][i]);
+        t[i] = fma2(back, yv[v][i], fma2(g, w[v][i], dv[v][i]));
+      }
+      if (a.dx) {
+        unpack8(o, t);
+        store8_warp<T, VEC>(dx_out + v * next_run, o, n[v], u.first, u.last, live);
+      }
       if (a.drop.cut) {
         uint32_t bits[4];
         philox(bits, a.drop, (uint32_t)(v * tpr + u.t), (uint32_t)row);
         drop8(t, a.drop, bits);
       }
-      store8_warp<T, VEC>((T*)a.df + row * a.lddf + c, t, n[v], u.first, u.last, live);
+      unpack8(o, t);
+      store8_warp<T, VEC>(df_out + v * next_run, o, n[v], u.first, u.last, live);
     }
+    dx_out += dx_step;
+    df_out += df_step;
   }
   float* out = a.parts + (int64_t)blockIdx.x * a.part_ld;
   if constexpr (MULTI) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+    for (int v = 0; v < V; ++v) {
+      float o[8];
+      unpack8(o, sums[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < n[v]) out[(v * tpr + u.t) * 8 + e] = sums[v][e];
+        if (e < n[v]) out[(v * tpr + u.t) * 8 + e] = o[e];
+    }
   } else {  // the units of a warp, then the warps, one after the other
-    for (int o = tpr; o < 32; o *= 2)
+    float o[V][8];
+#pragma unroll
+    for (int v = 0; v < V; ++v) unpack8(o[v], sums[v]);
+    for (int k = tpr; k < 32; k *= 2)
 #pragma unroll
       for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sums[v][e] += __shfl_xor_sync(0xffffffffu, sums[v][e], o);
+        for (int e = 0; e < 8; ++e) o[v][e] += __shfl_xor_sync(0xffffffffu, o[v][e], k);
     for (int k = 0; k < (int)blockDim.x >> 5; ++k) {
       if (u.warp == k && u.lane < tpr)
 #pragma unroll
@@ -313,7 +477,7 @@ __global__ void __launch_bounds__(MULTI ? 512 : 256) add_norm_bwd_kernel(const A
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const int c = (v * tpr + u.t) * 8 + e;
-            lines[c] = k ? lines[c] + sums[v][e] : sums[v][e];
+            lines[c] = k ? lines[c] + o[v][e] : o[v][e];
           }
       __syncthreads();
     }
@@ -324,8 +488,9 @@ __global__ void __launch_bounds__(MULTI ? 512 : 256) add_norm_bwd_kernel(const A
 // The column sums of long rows are kept in the CTA's row of parts.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const AddNormBwdArgs a) {
-  __shared__ float red[2][16];
+  __shared__ __align__(16) float red[2][16];
   const Unit u(kLongThreads, true);
+  clear_sums(red);
   uint32_t calls = 0;
   const int64_t panels = (a.cols + kLongThreads * 8 - 1) / (kLongThreads * 8);
   float* out = a.parts + (int64_t)blockIdx.x * a.part_ld;
@@ -336,6 +501,7 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const A
       load8<T, VEC>(y, (const T*)a.y + row * a.ldy + c, n);
       load8<float, VEC>(w, a.w + c, n);
     };
+#pragma unroll 4
     for (int64_t p = 0; p < panels; ++p) {
       const int64_t c = (p * kLongThreads + threadIdx.x) * 8;
       load(c, (int)max((int64_t)0, min((int64_t)8, a.cols - c)));
@@ -344,6 +510,7 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const A
     }
     s = unit_sum<true>(s, u, red, calls);
     const float r = a.rstd[row], back = r * r * r * (s * (1.f / (float)a.cols));
+#pragma unroll 2
     for (int64_t p = 0; p < panels; ++p) {
       const int64_t c = (p * kLongThreads + threadIdx.x) * 8, left = a.cols - c;
       const int n = (int)max((int64_t)0, min((int64_t)8, left));
@@ -367,52 +534,103 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const A
   }
 }
 
-// Threads of a unit, and of a CTA, and chunks a thread.
+// Threads of a unit and of a CTA, chunks a thread.
 struct Shape {
   int tpr, threads, v;
   int units() const { return threads / tpr; }
 };
+// 32 columns a thread in the forward take a sixth of the instructions away, and with
+// the registers they take as many warps: 16384 x 4096 bf16 to MXFP8 with dropout
+// 104 us either way, one row 13.5 us against 11.7.
 Shape shape_of(int64_t cols) {
   if (cols > 8192) return {512, 512, 4};
   int tpr = 4;
   while (tpr * 16 < cols) tpr *= 2;
-  return {tpr, std::max(tpr, tpr <= 32 ? 256 : 64), 2};
+  return {tpr, tpr <= 32 ? 256 : tpr, 2};
 }
-// CTAs that are resident together, of `threads` threads of at most 128 registers.
-int64_t resident(int threads, int sms) { return (int64_t)sms * std::max(1, 512 / threads) * 2; }
+constexpr int kFwdCtas = 3, kBwdCtas = 2;  // of 256 threads on an SM
+// CTAs for `rows`: what an SM holds together, and four rows a unit where that many
+// units have them (each CTA of the backward writes a row of partial sums).
+int64_t ctas_of(const Shape& sh, int64_t rows, int sms, int ctas256) {
+  const int64_t most = (int64_t)sms * std::max(1, ctas256 * 256 / sh.threads);
+  const int64_t few = (rows + 4 * sh.units() - 1) / (4 * sh.units());
+  return std::min(most, std::max<int64_t>(few, std::min<int64_t>((rows + sh.units() - 1) / sh.units(), sms)));
+}
+
+template <typename K, typename A>
+cudaError_t start(K kernel, const A& a, int64_t ctas, int threads, int smem, int tpr, cudaStream_t s) {
+  kernel<<<(unsigned)ctas, threads, smem, s>>>(a, tpr);
+  return cudaGetLastError();
+}
+
+// f(kernel, shared memory of a warp) for a shape.
+template <typename T, bool VEC, typename F>
+cudaError_t with_fwd(const Shape& sh, F f) {
+  constexpr int two = Ring<T, VEC, 2, 2, depth<T, 2>()>::kWarp, four = Ring<T, VEC, 4, 2, depth<T, 4>()>::kWarp;
+  if (sh.v == 4) return f(add_norm_fwd_kernel<T, VEC, 4, 512, 1, true>, four);
+  if (sh.tpr > 256) return f(add_norm_fwd_kernel<T, VEC, 2, 512, 1, true>, two);
+  if (sh.tpr > 32) return f(add_norm_fwd_kernel<T, VEC, 2, 256, kFwdCtas, true>, two);
+  return f(add_norm_fwd_kernel<T, VEC, 2, 256, kFwdCtas, false>, two);
+}
+template <typename T, bool VEC, typename F>
+cudaError_t with_bwd(const Shape& sh, F f) {
+  constexpr int D = depth<T, 2>();
+  if (sh.tpr > 256) return f(add_norm_bwd_kernel<T, VEC, 2, 512, 1, true>, Ring<T, VEC, 2, 3, D>::kWarp);
+  if (sh.tpr > 32) return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, true>, Ring<T, VEC, 2, 3, D>::kWarp);
+  return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, false>, Ring<T, VEC, 2, 3, D>::kWarp);
+}
 
 template <typename T, bool VEC>
 cudaError_t launch_fwd(const AddNormFwdArgs& a, int sms, cudaStream_t s) {
   if (a.cols > kMostFwd) {
-    add_norm_long_fwd_kernel<T, VEC><<<(unsigned)std::min<int64_t>(a.rows, resident(kLongThreads, sms)), kLongThreads, 0, s>>>(a);
+    add_norm_long_fwd_kernel<T, VEC><<<(unsigned)std::min<int64_t>(a.rows, 2 * sms), kLongThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
   const Shape sh = shape_of(a.cols);
-  const unsigned ctas = (unsigned)std::min<int64_t>((a.rows + sh.units() - 1) / sh.units(), resident(sh.threads, sms));
-  if (sh.v == 4) add_norm_fwd_kernel<T, VEC, 4, true><<<ctas, sh.threads, 0, s>>>(a, sh.tpr);
-  else if (sh.tpr > 32) add_norm_fwd_kernel<T, VEC, 2, true><<<ctas, sh.threads, 0, s>>>(a, sh.tpr);
-  else add_norm_fwd_kernel<T, VEC, 2, false><<<ctas, sh.threads, 0, s>>>(a, sh.tpr);
-  return cudaGetLastError();
+  const int64_t ctas = ctas_of(sh, a.rows, sms, kFwdCtas);
+  return with_fwd<T, VEC>(sh, [&](auto kernel, int warp) { return start(kernel, a, ctas, sh.threads, sh.threads / 32 * warp, sh.tpr, s); });
 }
 
 template <typename T, bool VEC>
-cudaError_t launch_bwd(const AddNormBwdArgs& a, unsigned ctas, cudaStream_t s) {
+cudaError_t launch_bwd(const AddNormBwdArgs& a, int64_t ctas, cudaStream_t s) {
   if (a.cols > kMostBwd) {
-    add_norm_long_bwd_kernel<T, VEC><<<ctas, kLongThreads, 0, s>>>(a);
+    add_norm_long_bwd_kernel<T, VEC><<<(unsigned)ctas, kLongThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
   const Shape sh = shape_of(a.cols);
-  if (sh.tpr > 32) add_norm_bwd_kernel<T, VEC, 2, true><<<ctas, sh.threads, 0, s>>>(a, sh.tpr);
-  else add_norm_bwd_kernel<T, VEC, 2, false><<<ctas, sh.threads, 0, s>>>(a, sh.tpr);
-  return cudaGetLastError();
+  return with_bwd<T, VEC>(sh, [&](auto kernel, int warp) { return start(kernel, a, ctas, sh.threads, sh.threads / 32 * warp, sh.tpr, s); });
+}
+
+template <typename T, bool VEC>
+cudaError_t configure() {
+  for (const int64_t cols : {512, 4096, 8192, 16384}) {  // every kernel, with its most threads
+    for (const bool fwd : {true, false}) {
+      if (!fwd && cols > kMostBwd) continue;
+      const Shape sh = shape_of(cols);
+      auto set = [&](auto kernel, int warp) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sh.threads / 32 * warp);
+      };
+      const cudaError_t e = fwd ? with_fwd<T, VEC>(sh, set) : with_bwd<T, VEC>(sh, set);
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return cudaSuccess;
 }
 
 }  // namespace
 
+cudaError_t add_norm_configure() {
+  for (auto one : {configure<float, true>, configure<float, false>, configure<__nv_bfloat16, true>, configure<__nv_bfloat16, false>,
+                   configure<__half, true>, configure<__half, false>}) {
+    const cudaError_t e = one();
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
 int64_t add_norm_bwd_ctas(int64_t rows, int64_t cols, int sms) {
-  if (cols > kMostBwd) return std::min<int64_t>(rows, resident(kLongThreads, sms));
-  const Shape sh = shape_of(cols);
-  return std::min<int64_t>((rows + sh.units() - 1) / sh.units(), resident(sh.threads, sms));
+  if (cols > kMostBwd) return std::min<int64_t>(rows, 2 * sms);
+  return ctas_of(shape_of(cols), rows, sms, kBwdCtas);
 }
 
 cudaError_t launch_add_norm_fwd(const AddNormFwdArgs& a, int dtype, int sms, cudaStream_t s) {
@@ -421,8 +639,7 @@ cudaError_t launch_add_norm_fwd(const AddNormFwdArgs& a, int dtype, int sms, cud
   return a.vec ? launch_fwd<float, true>(a, sms, s) : launch_fwd<float, false>(a, sms, s);
 }
 
-cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, int dtype, int64_t ctas_, cudaStream_t s) {
-  const unsigned ctas = (unsigned)ctas_;
+cudaError_t launch_add_norm_bwd(const AddNormBwdArgs& a, int dtype, int64_t ctas, cudaStream_t s) {
   if (dtype == DMUON_BF16) return a.vec ? launch_bwd<__nv_bfloat16, true>(a, ctas, s) : launch_bwd<__nv_bfloat16, false>(a, ctas, s);
   if (dtype == DMUON_F16) return a.vec ? launch_bwd<__half, true>(a, ctas, s) : launch_bwd<__half, false>(a, ctas, s);
   return a.vec ? launch_bwd<float, true>(a, ctas, s) : launch_bwd<float, false>(a, ctas, s);

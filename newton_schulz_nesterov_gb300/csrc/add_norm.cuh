@@ -40,6 +40,8 @@ struct AddNormBwdArgs {
   int vec;
 };
 
+// Before the launches.
+cudaError_t add_norm_configure();
 cudaError_t launch_add_norm_fwd(const AddNormFwdArgs& a, int dtype, int sms, cudaStream_t s);
 // CTAs of the backward: each writes one row of parts.
 int64_t add_norm_bwd_ctas(int64_t rows, int64_t cols, int sms);

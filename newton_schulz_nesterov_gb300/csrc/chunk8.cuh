@@ -14,6 +14,7 @@
 
 #include <type_traits>
 
+#include "f32x2.cuh"
 #include "pieces.cuh"
 
 namespace dmuon {
@@ -78,6 +79,53 @@ __device__ __forceinline__ void load8(float (&f)[8], const T* p, int n) {
   Raw8<T, VEC> r;
   load_raw8<T, VEC>(r, p, n);
   values8<T, VEC>(f, r, p, n);
+}
+
+// A 16-byte piece to shared memory, the first `bytes` of it (zeros behind them).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Eight values from shared memory, where the aligned pieces around them are; m: bytes
+// that the first of them is past a 16-byte boundary.  UNIFORM: it is mostly the same
+// for a whole warp, so a branch is cheaper than selects.
+template <typename T, bool VEC, bool UNIFORM = false>
+__device__ __forceinline__ void take8(f2 (&f)[4], const uint8_t* at, uint32_t m) {
+  constexpr int W = words8<T>(), N = W + (VEC ? 0 : 4);
+  uint32_t w[N];
+#pragma unroll
+  for (int i = 0; i < N; i += 4) {
+    const uint4 v = *reinterpret_cast<const uint4*>(at + i * 4);
+    w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+  }
+  if constexpr (!VEC && UNIFORM) {
+    uint32_t o[W];
+    shift_out<W>(o, w, m);
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = o[i];
+  } else if constexpr (!VEC) {
+#pragma unroll
+    for (int i = 0; i < W + 2; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+    if constexpr (sizeof(T) == 2)
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (m & 2) * 8);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if constexpr (sizeof(T) == 4) {
+      f[k] = pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      f[k] = pack2(v.x, v.y);
+    } else {
+      f[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+    }
+  }
 }
 
 // Eight values rounded to T, as words.

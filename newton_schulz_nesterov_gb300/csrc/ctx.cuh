@@ -132,7 +132,7 @@ struct dmuon_ctx {
   size_t op_ws_cap = 0;
   int norm_places[8] = {};
   bool quant_ready = false, norm_ready = false;  // the kernels' limits of shared memory are set
-  bool quant8_ready = false, act_ready = false, linear_ready[2] = {};  // (projections of 4 and 8 bits)
+  bool quant8_ready = false, act_ready = false, add_norm_ready = false, linear_ready[2] = {};  // (projections of 4 and 8 bits)
   bool op_ws_captured = false;         // a graph holds op_ws: it stays until the handle goes
   std::vector<void*> op_ws_kept;
 };

@@ -12,12 +12,14 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "f32x2.cuh"
+
 namespace dmuon {
 
 struct Drop {
   uint32_t cut;         // in the high half of a word; 0: everything stays
   float factor;
-  uint32_t key[2], offset[2];
+  uint32_t key[20], offset[2];  // key: of the ten rounds
 };
 
 // cut = round(65536 p); false for p that leaves nothing, or is no probability.
@@ -25,27 +27,40 @@ inline bool drop_of(float p, uint64_t seed, uint64_t offset, Drop* d) {
   if (!(p >= 0.f && p < 1.f)) return false;
   const uint32_t cut = (uint32_t)((double)p * 65536.0 + 0.5);
   if (cut >= 65536u) return false;
-  *d = Drop{cut << 16, 65536.f / (float)(65536u - cut), {(uint32_t)seed, (uint32_t)(seed >> 32)}, {(uint32_t)offset, (uint32_t)(offset >> 32)}};
+  d->cut = cut << 16;
+  d->factor = 65536.f / (float)(65536u - cut);
+  for (uint32_t i = 0; i < 10; ++i) {
+    d->key[2 * i] = (uint32_t)seed + i * 0x9E3779B9u;
+    d->key[2 * i + 1] = (uint32_t)(seed >> 32) + i * 0xBB67AE85u;
+  }
+  d->offset[0] = (uint32_t)offset;
+  d->offset[1] = (uint32_t)(offset >> 32);
   return true;
 }
 
 // The four words of columns 8 group .. 8 group + 7 of a row.
 __device__ __forceinline__ void philox(uint32_t (&w)[4], const Drop& d, uint32_t group, uint32_t row) {
-  uint32_t c0 = group, c1 = row, c2 = d.offset[0], c3 = d.offset[1], k0 = d.key[0], k1 = d.key[1];
+  uint32_t c0 = group, c1 = row, c2 = d.offset[0], c3 = d.offset[1];
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t a = (uint64_t)c0 * 0xD2511F53u, b = (uint64_t)c2 * 0xCD9E8D57u;
-    c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
-    c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+    c0 = (uint32_t)(b >> 32) ^ c1 ^ d.key[2 * i];
+    c2 = (uint32_t)(a >> 32) ^ c3 ^ d.key[2 * i + 1];
     c1 = (uint32_t)b;
     c3 = (uint32_t)a;
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
   }
   w[0] = c0; w[1] = c1; w[2] = c2; w[3] = c3;
 }
 
 // f[i] through the mask of the group; what goes is 0, also where it was Inf or NaN.
+__device__ __forceinline__ void drop8(f2 (&f)[4], const Drop& d, const uint32_t (&w)[4]) {
+  const f2 factor = both(d.factor);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 p = unpack2(mul2(f[j], factor));
+    f[j] = pack2((w[j] << 16) >= d.cut ? p.x : 0.f, w[j] >= d.cut ? p.y : 0.f);
+  }
+}
 __device__ __forceinline__ void drop8(float (&f)[8], const Drop& d, const uint32_t (&w)[4]) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {

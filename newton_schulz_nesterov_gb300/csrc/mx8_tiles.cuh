@@ -48,13 +48,6 @@ struct Geometry {
   static_assert(VEC || kWarpBytes >= 32 * 33 * (int)sizeof(T), "dz passes through a slot");
 };
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-
 // 32 x 32 elements (rows, cols of them in the matrix) to a warp's slot, zeros
 // outside the matrix; `row` is this lane's first row (a quad a row, whole lines an
 // access), `down` the bytes from it to its next one, eight rows on, `inside` an
@@ -84,38 +77,6 @@ __device__ __forceinline__ void fetch_tile(uint32_t slot, const uint8_t* row, in
     for (int k = 0; k < W + (VEC ? 0 : 1); ++k) {
       const int at = k * 64 + q * 16, n = max(0, min(16, bytes - at));
       if (k < W || q == 0) copy16(slot + i * 8 * G::kRowBytes + k * 64, n ? from + at : inside, n);
-    }
-  }
-}
-
-// Eight values from a slot's row; m: bytes of the matrix's row past a 16-byte boundary.
-template <typename T, bool VEC>
-__device__ __forceinline__ void take8(f2 (&f)[4], const uint8_t* at, uint32_t m) {
-  constexpr int W = words8<T>(), N = W + (VEC ? 0 : 4);
-  uint32_t w[N];
-#pragma unroll
-  for (int i = 0; i < N; i += 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(at + i * 4);
-    w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
-  }
-  if constexpr (!VEC) {
-#pragma unroll
-    for (int i = 0; i < W + 2; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
-#pragma unroll
-    for (int i = 0; i < W + 1; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
-    if constexpr (sizeof(T) == 2)
-#pragma unroll
-      for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], (m & 2) * 8);
-  }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    if constexpr (sizeof(T) == 4) {
-      f[k] = pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
-    } else if constexpr (std::is_same<T, __half>::value) {
-      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
-      f[k] = pack2(v.x, v.y);
-    } else {
-      f[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
     }
   }
 }

@@ -245,6 +245,7 @@ int dmuon_add_norm_forward(dmuon_handle_t h, const dmuon_add_norm_t* p, void* st
   if (!apart({p->y, p->h, p->q_data, p->q_scales, p->rstd}, {p->x, p->f, p->w}))
     return fail(h, DMUON_ERR_ARG, "add_norm_forward: an output is another or an input");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
+  if ((rc = ready(h, h->add_norm_ready, add_norm_configure, "add_norm_forward: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   a.x = p->x;
   a.f = p->f;
@@ -292,6 +293,7 @@ int dmuon_add_norm_backward(dmuon_handle_t h, const dmuon_add_norm_t* p, const d
   }
   if ((rc = check_matrix(h, g_->d_w, DMUON_F32, 0, 0, "add_norm_backward: d_w"))) return rc;
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
+  if ((rc = ready(h, h->add_norm_ready, add_norm_configure, "add_norm_backward: configure"))) return rc;
   cudaStream_t stream = (cudaStream_t)stream_;
   a.dy = g_->dy;
   a.dh = g_->dh;
