@@ -69,13 +69,23 @@ __device__ __forceinline__ float unit_sum(float v, const Unit& u, float (*red)[1
   return ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
 }
 
-// Scale bytes past the matrix are zero: rows from `rows` to the tile's end, by
-// all threads of the grid; blocks past a row's last, with the row.
+// Scale bytes past the matrix are zero: rows from `rows` to the last tile's end, a
+// warp of the grid a tile (a lane has the 16 bytes of rows lane, lane + 32, ..);
+// blocks past a row's last, with the row.
 __device__ __forceinline__ void zero_rows_behind(uint8_t* scales, int64_t rows, int64_t cols) {
-  const int64_t kt = mx_scale_cols(cols), all = (128 - (rows & 127)) % 128 * kt;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < all; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t r = rows + i / kt;
-    *reinterpret_cast<uint32_t*>(scales + ((r >> 7) * kt + i % kt) * kMxScaleTile + (r & 31) * 16 + ((r >> 5) & 3) * 4) = 0u;
+  const int left = (int)(rows & 127), lane = threadIdx.x & 31;  // rows of the last tile
+  if (left == 0) return;
+  const int64_t kt = mx_scale_cols(cols), warps = (int64_t)gridDim.x * (blockDim.x >> 5);
+  uint8_t* last = scales + (rows >> 7) * kt * kMxScaleTile + lane * 16;
+  for (int64_t i = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5); i < kt; i += warps) {
+    uint8_t* p = last + i * kMxScaleTile;
+    if (lane >= left) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(0, 0, 0, 0);
+      continue;
+    }
+#pragma unroll
+    for (int q = 1; q < 4; ++q)
+      if (lane + 32 * q >= left) *reinterpret_cast<uint32_t*>(p + 4 * q) = 0u;
   }
 }
 __device__ __forceinline__ uint8_t* scale_at(uint8_t* scales, int64_t row, int64_t blk, int64_t cols) {
@@ -549,11 +559,11 @@ Shape shape_of(int64_t cols) {
   return {tpr, tpr <= 32 ? 256 : tpr, 2};
 }
 constexpr int kFwdCtas = 3, kBwdCtas = 2;  // of 256 threads on an SM
-// CTAs for `rows`: what an SM holds together, and four rows a unit where that many
+// CTAs for `rows`: what an SM holds together, and two rows a unit where that many
 // units have them (each CTA of the backward writes a row of partial sums).
 int64_t ctas_of(const Shape& sh, int64_t rows, int sms, int ctas256) {
   const int64_t most = (int64_t)sms * std::max(1, ctas256 * 256 / sh.threads);
-  const int64_t few = (rows + 4 * sh.units() - 1) / (4 * sh.units());
+  const int64_t few = (rows + 2 * sh.units() - 1) / (2 * sh.units());
   return std::min(most, std::max<int64_t>(few, std::min<int64_t>((rows + sh.units() - 1) / sh.units(), sms)));
 }
 

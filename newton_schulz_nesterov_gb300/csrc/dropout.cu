@@ -1,7 +1,8 @@
 // out = dropout(x) + residual over a matrix (generator in dropout.cuh).
 //
-// A lane has one group of eight columns, whose bits one round of the generator
-// gives, in four rows, all loaded before one is used.  Short rows share a warp.
+// A lane has one group of eight columns, whose bits one call of the generator
+// gives, in four rows, all loaded before one is used; in one row where four would
+// leave SMs without work (777 x 2061 fp32).  Short rows share a warp.
 #include "../../include/dmuon.h"
 #include "chunk8.cuh"
 #include "dropout.cuh"
@@ -10,9 +11,9 @@ namespace dmuon {
 
 namespace {
 
-constexpr int kThreads = 256, kRows = 4;  // rows a lane has
+constexpr int kThreads = 256;
 
-template <typename T, bool VEC>
+template <typename T, bool VEC, int kRows>  // rows a lane has
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a, int lanes) {  // lanes of a row: a power of two
   const int64_t ct = (a.cols + 255) / 256;
   const int at_once = kThreads / lanes, lane = threadIdx.x & (lanes - 1);
@@ -48,23 +49,30 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a, 
   }
 }
 
-template <typename T>
-cudaError_t launch(const DropoutArgs& a, cudaStream_t s) {
-  int lanes = 1;
-  while (lanes < 32 && lanes * 8 < a.cols) lanes *= 2;
+template <typename T, int kRows>
+cudaError_t launch_rows(const DropoutArgs& a, int lanes, cudaStream_t s) {
   const int64_t per = kRows * (kThreads / lanes);
   const int64_t ctas = (a.rows + per - 1) / per * ((a.cols + 255) / 256);
-  if (a.vec) dropout_kernel<T, true><<<(unsigned)ctas, kThreads, 0, s>>>(a, lanes);
-  else dropout_kernel<T, false><<<(unsigned)ctas, kThreads, 0, s>>>(a, lanes);
+  if (a.vec) dropout_kernel<T, true, kRows><<<(unsigned)ctas, kThreads, 0, s>>>(a, lanes);
+  else dropout_kernel<T, false, kRows><<<(unsigned)ctas, kThreads, 0, s>>>(a, lanes);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch(const DropoutArgs& a, int sms, cudaStream_t s) {
+  int lanes = 1;
+  while (lanes < 32 && lanes * 8 < a.cols) lanes *= 2;
+  const int64_t per = 4 * (kThreads / lanes);
+  const bool few = (a.rows + per - 1) / per * ((a.cols + 255) / 256) < 4 * sms;
+  return few ? launch_rows<T, 1>(a, lanes, s) : launch_rows<T, 4>(a, lanes, s);
 }
 
 }  // namespace
 
-cudaError_t launch_dropout(const DropoutArgs& a, int dtype, cudaStream_t s) {
-  if (dtype == DMUON_BF16) return launch<__nv_bfloat16>(a, s);
-  if (dtype == DMUON_F16) return launch<__half>(a, s);
-  return launch<float>(a, s);
+cudaError_t launch_dropout(const DropoutArgs& a, int dtype, int sms, cudaStream_t s) {
+  if (dtype == DMUON_BF16) return launch<__nv_bfloat16>(a, sms, s);
+  if (dtype == DMUON_F16) return launch<__half>(a, sms, s);
+  return launch<float>(a, sms, s);
 }
 
 }  // namespace dmuon

@@ -77,6 +77,6 @@ struct DropoutArgs {
   Drop drop;
   int vec;
 };
-cudaError_t launch_dropout(const DropoutArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_dropout(const DropoutArgs& a, int dtype, int sms, cudaStream_t s);
 
 }  // namespace dmuon

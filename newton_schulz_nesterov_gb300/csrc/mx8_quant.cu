@@ -97,12 +97,14 @@ cudaError_t launch_dequant(const MxDequantArgs& a, cudaStream_t s) {
 // ------------------------------------------------------------ column sums
 
 // 32 columns a CTA, a row of 32 lanes every 32nd of the partial rows; then the
-// 32 sums of a column, in order.
+// 32 sums of a column, in order.  Launched ahead of the end of the kernel before
+// it, which it waits for (griddepcontrol.wait: its stores are then visible).
 __global__ void __launch_bounds__(1024) column_sums_kernel(const float* parts, int64_t n, int64_t ld, int64_t cols, float* out) {
   __shared__ float part[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t c = (int64_t)blockIdx.x * 32 + lane;
   float s = 0.f;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (c < cols) {
 #pragma unroll 8
     for (int64_t r = warp; r < n; r += 32) s += parts[r * ld + c];
@@ -129,8 +131,16 @@ cudaError_t launch_mx8_dequant(const MxDequantArgs& a, int dtype, cudaStream_t s
 }
 
 cudaError_t launch_column_sums(const float* parts, int64_t n, int64_t ld, int64_t cols, float* out, cudaStream_t s) {
-  column_sums_kernel<<<(unsigned)((cols + 31) / 32), 1024, 0, s>>>(parts, n, ld, cols, out);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3((unsigned)((cols + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(1024, 1, 1);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, column_sums_kernel, parts, n, ld, cols, out);
 }
 
 }  // namespace dmuon

@@ -359,7 +359,7 @@ int dmuon_dropout(dmuon_handle_t h, const void* x, int dtype, int64_t rows, int6
   a.ldout = ldout;
   a.vec = rows_aligned(x, ldx, dtype) && rows_aligned(out, ldout, dtype) && (!residual || rows_aligned(residual, ldres, dtype));
   LaunchGuard g(h, stream, DMUON_KIND_DROPOUT);
-  const cudaError_t e = launch_dropout(a, dtype, stream);
+  const cudaError_t e = launch_dropout(a, dtype, h->num_sms, stream);
   if (e != cudaSuccess) return fail(h, cuda_err(e), "dropout launch", e);
   h->last_stream = stream;
   return DMUON_OK;
