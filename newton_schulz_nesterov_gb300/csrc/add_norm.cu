@@ -43,30 +43,48 @@ struct Unit {
   }
 };
 
-// Sum over a unit, in a fixed order, to all of it.  Consecutive calls of a CTA
-// alternate between the halves of `red`: one is written again only after the
-// next call's barrier, when every thread has read it.  What no warp writes is zero
-// (clear_sums, ahead of a barrier or of the first call's).
-__device__ __forceinline__ void clear_sums(float (*red)[16]) {
-  if (threadIdx.x < 32 && threadIdx.x % 16 >= blockDim.x / 32) red[threadIdx.x / 16][threadIdx.x % 16] = 0.f;
+// Sums over a unit, to all of it.  A chunk's eight products are added up by its lane,
+// then chunks pairwise by the bits of their number, from the lowest: the order
+// does not depend on which lane has which chunk, nor on the type.  N sums a lane
+// are those of chunks that lie a unit's threads apart, so they meet last.
+// Consecutive calls of a CTA alternate between the halves of `red`: one is written
+// again only after the next call's barrier, when every thread has read it.  What no
+// warp writes is zero (clear_sums, ahead of the first call's barrier).
+constexpr int kSums = 4 * 16;  // of a half: N sums of 16 warps
+__device__ __forceinline__ void clear_sums(float* red) {
+  for (int i = threadIdx.x; i < 2 * kSums; i += blockDim.x)
+    if (i % 16 >= (int)blockDim.x / 32) red[i] = 0.f;
 }
-template <bool MULTI>
-__device__ __forceinline__ float unit_sum(float v, const Unit& u, float (*red)[16], uint32_t& calls) {
+template <int N>
+__device__ __forceinline__ float pairwise(const float (&v)[N]) {
+  if constexpr (N == 1) return v[0];
+  else if constexpr (N == 2) return v[0] + v[1];
+  else return (v[0] + v[1]) + (v[2] + v[3]);
+}
+template <bool MULTI, int N>
+__device__ __forceinline__ float unit_sum(float (&v)[N], const Unit& u, float* red, uint32_t& calls) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-    if (MULTI || o < u.tpr) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if constexpr (!MULTI) return v;
-  float* mine = red[calls++ & 1];
-  if (u.lane == 0) mine[u.warp] = v;
+  for (int o = 1; o < 32; o *= 2)
+    if (MULTI || o < u.tpr)
+#pragma unroll
+      for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
+  if constexpr (!MULTI) return pairwise(v);
+  float* mine = red + (calls++ & 1) * kSums;
+  if (u.lane == 0)
+#pragma unroll
+    for (int k = 0; k < N; ++k) mine[k * 16 + u.warp] = v[k];
   __syncthreads();
-  const float4* four = reinterpret_cast<const float4*>(mine);
-  float4 p = four[0], q = four[1];
-  if (blockDim.x > 256) {
-    const float4 r = four[2], t = four[3];
-    p.x += r.x; p.y += r.y; p.z += r.z; p.w += r.w;
-    q.x += t.x; q.y += t.y; q.z += t.z; q.w += t.w;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float4* four = reinterpret_cast<const float4*>(mine + k * 16);
+    const float4 p = four[0], q = four[1];
+    v[k] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+    if (blockDim.x > 256) {
+      const float4 r = four[2], t = four[3];
+      v[k] += ((r.x + r.y) + (r.z + r.w)) + ((t.x + t.y) + (t.z + t.w));
+    }
   }
-  return ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
+  return pairwise(v);
 }
 
 // Scale bytes past the matrix are zero: rows from `rows` to the last tile's end, a
@@ -92,26 +110,43 @@ __device__ __forceinline__ uint8_t* scale_at(uint8_t* scales, int64_t row, int64
   return scales + ((row >> 7) * mx_scale_cols(cols) + (blk >> 2)) * kMxScaleTile + (row & 31) * 16 + ((row >> 5) & 3) * 4 + (blk & 3);
 }
 
-// Eight values of columns col .. of a row to codes; a warp's lanes together, four
-// consecutive ones a block.
-__device__ __forceinline__ void quantise8(const AddNormFwdArgs& a, const float (&h)[8], int64_t row, int col, bool live) {
-  const float m = mx8::max_abs(h);
+// 8 C consecutive values of a row, from column col on, to codes; a warp's lanes
+// together, 4 / C consecutive ones a block.
+template <int C>
+__device__ __forceinline__ void quantise(const AddNormFwdArgs& a, const float (&h)[C][8], int64_t row, int col, bool live) {
+  float m = 0.f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) m = mx8::max_abs(m, mx8::max_abs(h[c]), 0.f);
   uint32_t key = mx8::keys2(m, m, a.up);
-  key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, 1));
-  key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, 2));
+#pragma unroll
+  for (int o = 1; o < 4 / C; o *= 2) key = mx8::max_halves(key, __shfl_xor_sync(0xffffffffu, key, o));
   uint32_t bad = 0;  // the block holds Inf or NaN
   if (__any_sync(0xffffffffu, mx8::may_not_be_finite(key))) {
     bad = mx8::not_finite(m);
-    bad |= __shfl_xor_sync(0xffffffffu, bad, 1);
-    bad |= __shfl_xor_sync(0xffffffffu, bad, 2);
+#pragma unroll
+    for (int o = 1; o < 4 / C; o *= 2) bad |= __shfl_xor_sync(0xffffffffu, bad, o);
   }
   if (!live || col >= (int)mx_blocks(a.cols) * kMxBlock) return;
   const uint32_t ex = mx8::exponents2(key);
   const float inv = mx8::factors2(ex).y;
-  uint2 w = make_uint2(mx8::codes4(h[0] * inv, h[1] * inv, h[2] * inv, h[3] * inv), mx8::codes4(h[4] * inv, h[5] * inv, h[6] * inv, h[7] * inv));
-  if (bad) w = make_uint2(0, 0);
-  *reinterpret_cast<uint2*>(a.q + row * mx_pitch(a.cols, 8) + col) = w;
+  uint32_t w[2 * C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    w[2 * c] = mx8::codes4(h[c][0] * inv, h[c][1] * inv, h[c][2] * inv, h[c][3] * inv);
+    w[2 * c + 1] = mx8::codes4(h[c][4] * inv, h[c][5] * inv, h[c][6] * inv, h[c][7] * inv);
+  }
+  if (bad)
+#pragma unroll
+    for (int i = 0; i < 2 * C; ++i) w[i] = 0;
+  uint8_t* q = a.q + row * mx_pitch(a.cols, 8) + col;
+  if constexpr (C == 1) *reinterpret_cast<uint2*>(q) = make_uint2(w[0], w[1]);
+  else
+#pragma unroll
+    for (int i = 0; i < 2 * C; i += 4) reinterpret_cast<uint4*>(q)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
   if ((col & 31) == 0) *scale_at(a.q_scales, row, col >> 5, a.cols) = bad ? 255 : (uint8_t)mx8::byte_of(ex, 1);
+}
+__device__ __forceinline__ void quantise8(const AddNormFwdArgs& a, const float (&h)[8], int64_t row, int col, bool live) {
+  quantise<1>(a, reinterpret_cast<const float (&)[1][8]>(h), row, col, live);
 }
 __device__ __forceinline__ void zero_blocks_behind(const AddNormFwdArgs& a, int64_t row, int t, bool live) {
   const int64_t nb = mx_blocks(a.cols);
@@ -122,14 +157,14 @@ __device__ __forceinline__ void zero_blocks_behind(const AddNormFwdArgs& a, int6
 template <typename T, int V>
 constexpr int depth() { return (sizeof(T) == 4 ? 2 : 3) - (V == 4 ? 1 : 0); }
 
-// The ring of a warp: DEPTH slots of ARRAYS x V runs.  A run is the 16-byte pieces
-// that the chunks of a unit's lanes of this warp lie in, one after the other (rows
-// on any element: one piece more), copied by those lanes piece by piece.
-template <typename T, bool VEC, int V, int ARRAYS, int DEPTH>
+// The ring of a warp: DEPTH slots of ARRAYS x RUNS runs.  A run is the 16-byte pieces
+// that C chunks of each of a unit's lanes of this warp lie in, one after the other
+// (rows on any element: one piece more), copied by those lanes piece by piece.
+template <typename T, bool VEC, int RUNS, int C, int ARRAYS, int DEPTH>
 struct Ring {
-  static constexpr int W = words8<T>() / 4;                      // pieces of a lane
+  static constexpr int W = C * words8<T>() / 4;                  // pieces of a lane
   static constexpr int kRun = (32 * W + (VEC ? 0 : 8)) * 16;     // bytes; up to eight units a warp
-  static constexpr int kSlot = ARRAYS * V * kRun;
+  static constexpr int kSlot = ARRAYS * RUNS * kRun;
   static constexpr int kWarp = DEPTH * kSlot;
   const uint8_t* mine;     // this lane's first piece in slot 0
   uint32_t copies;         // where it copies its first piece to
@@ -142,20 +177,20 @@ struct Ring {
     mine = warp + run + l * W * 16;
     copies = ptx::smem_addr(warp + run + l * 16);
   }
-  // Run (array, v) of the slot at `slot` bytes: p its first element (of the unit's
+  // Run (array, r) of the slot at `slot` bytes: p its first element (of the unit's
   // first lane in this warp), left the elements of the row from there on (none:
   // below 1), inside an address of the matrix.
-  __device__ __forceinline__ void fetch(int slot, int array, int v, const uint8_t* p, int left, const void* inside) const {
-    const uint32_t dst = copies + slot + (array * V + v) * kRun;
+  __device__ __forceinline__ void fetch(int slot, int array, int r, const uint8_t* p, int left, const void* inside) const {
+    const uint32_t dst = copies + slot + (array * RUNS + r) * kRun;
     const uint32_t m = VEC ? 0u : past16(p);
     const uint8_t* from = p - m + l * 16;
-    if (left >= lanes * 8) {
+    if (left >= lanes * 8 * C) {
 #pragma unroll
       for (int k = 0; k < W; ++k) copy16(dst + k * lanes * 16, from + k * lanes * 16);
       if (!VEC && l == 0) copy16(dst + W * lanes * 16, m ? from + W * lanes * 16 : from, (int)m);
       return;
     }
-    const int bytes = left > 0 ? min(left, lanes * 8) * (int)sizeof(T) + (int)m : 0;
+    const int bytes = left > 0 ? min(left, lanes * 8 * C) * (int)sizeof(T) + (int)m : 0;
     const uint8_t* other = reinterpret_cast<const uint8_t*>(inside) - past16(reinterpret_cast<const uint8_t*>(inside));
 #pragma unroll
     for (int k = 0; k < W; ++k) {
@@ -167,10 +202,20 @@ struct Ring {
       copy16(dst + W * lanes * 16, n ? from + W * lanes * 16 : other, n);
     }
   }
+  // Chunk v of the lane: of run v, or the vth of the one run.
   __device__ __forceinline__ void take(f2 (&f)[4], int slot, int array, int v, uint32_t m) const {
-    take8<T, VEC, true>(f, mine + slot + (array * V + v) * kRun, m);
+    take8<T, VEC, true>(f, mine + slot + (array * RUNS + v / C) * kRun + v % C * (W / C * 16), m);
   }
 };
+// How a thread's V chunks lie: one after the other where a row has warps of its own
+// and 16-bit elements (one run; 32 bytes a lane, and on any element half the shifting
+// and half the ends: 16384 x 4095 bf16 forward 164 -> 140 us, backward 212 -> 176), a
+// unit's threads apart otherwise (V runs; fp32 on any element 1371 x 6082 backward
+// 48 us so, 57 one after the other).
+template <typename T, bool MULTI>
+constexpr bool wide() { return MULTI && sizeof(T) == 2; }
+template <typename T, bool VEC, bool MULTI, int V, int ARRAYS, int DEPTH>
+using RingOf = Ring<T, VEC, wide<T, MULTI>() ? 1 : V, wide<T, MULTI>() ? V : 1, ARRAYS, DEPTH>;
 
 // The rows of one matrix that a unit goes through: the run that its warp fetches
 // next, and how far a row's first byte is past a 16-byte boundary.
@@ -199,6 +244,20 @@ __device__ __forceinline__ void unpack8(float (&o)[8], const f2 (&f)[4]) {
     o[2 * i + 1] = p.y;
   }
 }
+// A row's chunks of a thread; next_run as in the kernels, n: columns from each chunk on.
+template <typename T, bool VEC, bool MULTI, int V>
+__device__ __forceinline__ void store_chunks(T* p, int next_run, const f2 (&f)[V][4], const int (&n)[V], const Unit& u, bool live) {
+  if constexpr (wide<T, MULTI>()) {
+    store_wide<T, VEC, V>(p, f, n[0]);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      float o[8];
+      unpack8(o, f[v]);
+      store8_warp<T, VEC, MULTI>(p + v * next_run, o, n[v], u.first, u.last, live);
+    }
+  }
+}
 __device__ __forceinline__ void load_weights(f2 (&w)[4], const float* p, int n, bool vec) {
   float f[8];
   if (vec) load8<float, true>(f, p, n);
@@ -212,9 +271,12 @@ template <typename T, bool VEC, int V, int kThreads, int kCtas, bool MULTI>
 __global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const AddNormFwdArgs a, int tpr) {
   constexpr int D = depth<T, V>();
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float red[2][16];
+  __shared__ __align__(16) float red[2 * kSums];
   const Unit u(tpr, MULTI);
-  const Ring<T, VEC, V, 2, D> ring(smem, u);
+  constexpr bool kWide = wide<T, MULTI>();
+  constexpr int kRuns = kWide ? 1 : V, kApart = kWide || !MULTI ? 1 : V;
+  const RingOf<T, VEC, MULTI, V, 2, D> ring(smem, u);
+  auto col = [&](int v) { return kWide ? (u.t * V + v) * 8 : (v * tpr + u.t) * 8; };
   uint32_t calls = 0;
   const int64_t step = (int64_t)gridDim.x * u.units;
   int64_t row = (int64_t)blockIdx.x * u.units + u.unit, ahead = row;
@@ -222,17 +284,17 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const Add
   f2 w[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = (v * tpr + u.t) * 8;
+    const int c = col(v);
     n[v] = (int)a.cols - c;
     load_weights(w[v], a.w + c, n[v], VEC);
   }
-  const int run0 = (u.t - ring.l) * 8, next_run = tpr * 8;  // columns of the warp's first run, and from there to the next
+  const int run0 = col(0) - ring.l * (kWide ? 8 * V : 8), next_run = tpr * 8;  // columns of the warp's first run, and from there to the next
   Rows<T, VEC> x(a.x, a.ldx, row, step, run0), f(a.f, a.ldf, row, step, run0);
   int fetch_slot = 0;
   auto fetch = [&]() {
     const int cols = ahead < a.rows ? (int)a.cols - run0 : 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < kRuns; ++v) {
       const int64_t off = (int64_t)(v * next_run) * (int)sizeof(T);
       ring.fetch(fetch_slot, 0, v, f.next + off, cols - v * next_run, f.inside);
       if (a.x) ring.fetch(fetch_slot, 1, v, x.next + off, cols - v * next_run, x.inside);
@@ -248,17 +310,18 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const Add
   if (a.q) zero_rows_behind(a.q_scales, a.rows, a.cols);
   clear_sums(red);
   const float inv = 1.f / (float)a.cols;
-  T* y_out = (T*)a.y + row * a.ldy + u.t * 8;
-  T* h_out = (T*)a.h + row * a.ldh + u.t * 8;
+  T* y_out = (T*)a.y + row * a.ldy + col(0);
+  T* h_out = (T*)a.h + row * a.ldh + col(0);
   const int64_t y_step = step * a.ldy, h_step = step * a.ldh;
   int slot = 0;
   for (int64_t base = (int64_t)blockIdx.x * u.units; base < a.rows; base += step, row += step) {  // as often for every unit
     const bool live = MULTI || row < a.rows;
-    f2 y[V][4], s = 0;
+    f2 y[V][4];
+    float s[V];
     uint32_t bits[V][4];
     if (a.drop.cut) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) philox(bits[v], a.drop, (uint32_t)(v * tpr + u.t), (uint32_t)row);
+      for (int v = 0; v < V; ++v) philox(bits[v], a.drop, (uint32_t)(col(v) >> 3), (uint32_t)row);
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     __syncwarp();
@@ -272,30 +335,39 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const Add
 #pragma unroll
         for (int i = 0; i < 4; ++i) y[v][i] = add2(y[v][i], more[i]);
       }
+      f2 square = mul2(y[v][0], y[v][0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s = fma2(y[v][i], y[v][i], s);
+      for (int i = 1; i < 4; ++i) square = fma2(y[v][i], y[v][i], square);
+      s[v] = add_up(square);
     }
     __syncwarp();
     fetch();
     if ((slot += ring.kSlot) == ring.kWarp) slot = 0;
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float o[8];
-      unpack8(o, y[v]);
-      store8_warp<T, VEC>(y_out + v * next_run, o, n[v], u.first, u.last, live);
-    }
+    store_chunks<T, VEC, MULTI>(y_out, next_run, y, n, u, live);
     y_out += y_step;
-    const float r = rsqrtf(fmaf(unit_sum<MULTI>(add_up(s), u, red, calls), inv, a.eps));
+    float total[kApart];
+    if constexpr (kApart == 1) total[0] = pairwise(s);
+    else
+#pragma unroll
+      for (int v = 0; v < V; ++v) total[v] = s[v];
+    const float r = rsqrtf(fmaf(unit_sum<MULTI>(total, u, red, calls), inv, a.eps));
     if (live && u.t == 0) a.rstd[row] = r;
     const f2 rr = both(r);
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      float o[8];
+    for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int i = 0; i < 4; ++i) y[v][i] = mul2(mul2(y[v][i], rr), w[v][i]);
-      unpack8(o, y[v]);
-      if (a.h) store8_warp<T, VEC>(h_out + v * next_run, o, n[v], u.first, u.last, live);
-      if (a.q) quantise8(a, o, row, (v * tpr + u.t) * 8, live);
+    if (a.h) store_chunks<T, VEC, MULTI>(h_out, next_run, y, n, u, live);
+    if (a.q) {
+      float o[V][8];
+#pragma unroll
+      for (int v = 0; v < V; ++v) unpack8(o[v], y[v]);
+      if constexpr (kWide) {
+        quantise<V>(a, o, row, col(0), live);
+      } else {
+#pragma unroll
+        for (int v = 0; v < V; ++v) quantise8(a, o[v], row, col(v), live);
+      }
     }
     h_out += h_step;
     if (a.q) zero_blocks_behind(a, row, u.t, live);
@@ -304,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const Add
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const AddNormFwdArgs a) {
-  __shared__ __align__(16) float red[2][16];
+  __shared__ __align__(16) float red[2 * kSums];
   const Unit u(kLongThreads, true);
   clear_sums(red);
   uint32_t calls = 0;
@@ -333,9 +405,10 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const A
       sum_at(y, c);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s = fmaf(y[e], y[e], s);
-      store8_warp<T, VEC>((T*)a.y + row * a.ldy + c, y, a.cols - c, u.first, u.last, true);
+      store8_warp<T, VEC, true>((T*)a.y + row * a.ldy + c, y, a.cols - c, u.first, u.last, true);
     }
-    s = unit_sum<true>(s, u, red, calls);
+    float one[1] = {s};
+    s = unit_sum<true>(one, u, red, calls);
     const float r = rsqrtf(fmaf(s, 1.f / (float)a.cols, a.eps));
     if (threadIdx.x == 0) a.rstd[row] = r;
 #pragma unroll 2
@@ -346,7 +419,7 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const A
       load8<float, VEC>(w, a.w + c, (int)max((int64_t)0, min((int64_t)8, a.cols - c)));
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = y[e] * r * w[e];
-      if (a.h) store8_warp<T, VEC>((T*)a.h + row * a.ldh + c, y, a.cols - c, u.first, u.last, true);
+      if (a.h) store8_warp<T, VEC, true>((T*)a.h + row * a.ldh + c, y, a.cols - c, u.first, u.last, true);
       if (a.q) quantise8(a, y, row, (int)c, true);
     }
     if (a.q) zero_blocks_behind(a, row, u.t, true);
@@ -368,10 +441,13 @@ template <typename T, bool VEC, int V, int kThreads, int kCtas, bool MULTI>
 __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const AddNormBwdArgs a, int tpr) {
   constexpr int D = depth<T, V>();
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ __align__(16) float red[2][16];
+  __shared__ __align__(16) float red[2 * kSums];
   __shared__ float lines[MULTI ? 1 : 32 * V * 8];
   const Unit u(tpr, MULTI);
-  const Ring<T, VEC, V, 3, D> ring(smem, u);
+  constexpr bool kWide = wide<T, MULTI>();
+  constexpr int kRuns = kWide ? 1 : V, kApart = kWide || !MULTI ? 1 : V;
+  const RingOf<T, VEC, MULTI, V, 3, D> ring(smem, u);
+  auto col = [&](int v) { return kWide ? (u.t * V + v) * 8 : (v * tpr + u.t) * 8; };
   uint32_t calls = 0;
   const int64_t step = (int64_t)gridDim.x * u.units;
   int64_t row = (int64_t)blockIdx.x * u.units + u.unit, ahead = row;
@@ -379,19 +455,19 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
   f2 w[V][4], sums[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    const int c = (v * tpr + u.t) * 8;
+    const int c = col(v);
     n[v] = (int)a.cols - c;
     load_weights(w[v], a.w + c, n[v], VEC);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[v][i] = 0;
   }
-  const int run0 = (u.t - ring.l) * 8, next_run = tpr * 8;  // columns of the warp's first run, and from there to the next
+  const int run0 = col(0) - ring.l * (kWide ? 8 * V : 8), next_run = tpr * 8;  // columns of the warp's first run, and from there to the next
   Rows<T, VEC> dy(a.dy, a.lddy, row, step, run0), dh(a.dh, a.lddh, row, step, run0), y(a.y, a.ldy, row, step, run0);
   int fetch_slot = 0;
   auto fetch = [&]() {
     const int cols = ahead < a.rows ? (int)a.cols - run0 : 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+    for (int v = 0; v < kRuns; ++v) {
       const int64_t off = (int64_t)(v * next_run) * (int)sizeof(T);
       ring.fetch(fetch_slot, 0, v, dh.next + off, cols - v * next_run, dh.inside);
       ring.fetch(fetch_slot, 1, v, y.next + off, cols - v * next_run, y.inside);
@@ -409,15 +485,16 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
   clear_sums(red);
   const float inv = 1.f / (float)a.cols;
   float next_r = row < a.rows ? a.rstd[row] : 0.f;
-  T* dx_out = (T*)a.dx + row * a.lddx + u.t * 8;
-  T* df_out = (T*)a.df + row * a.lddf + u.t * 8;
+  T* dx_out = (T*)a.dx + row * a.lddx + col(0);
+  T* df_out = (T*)a.df + row * a.lddf + col(0);
   const int64_t dx_step = step * a.lddx, df_step = step * a.lddf;
   int slot = 0;
   for (int64_t base = (int64_t)blockIdx.x * u.units; base < a.rows; base += step, row += step) {
     const bool live = MULTI || row < a.rows;
     const float r = next_r;
     next_r = row + step < a.rows ? a.rstd[row + step] : 0.f;
-    f2 gv[V][4], yv[V][4], dv[V][4], s = 0;
+    f2 gv[V][4], yv[V][4], dv[V][4];
+    float s[V];
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     __syncwarp();
 #pragma unroll
@@ -428,36 +505,39 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
       else
 #pragma unroll
         for (int i = 0; i < 4; ++i) dv[v][i] = 0;
+      f2 product = mul2(mul2(gv[v][0], w[v][0]), yv[v][0]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) s = fma2(mul2(gv[v][i], w[v][i]), yv[v][i], s);
+      for (int i = 1; i < 4; ++i) product = fma2(mul2(gv[v][i], w[v][i]), yv[v][i], product);
+      s[v] = add_up(product);
     }
     __syncwarp();
     fetch();
     if ((slot += ring.kSlot) == ring.kWarp) slot = 0;
-    const float total = unit_sum<MULTI>(add_up(s), u, red, calls);
-    const f2 rr = both(r), back = both(-(r * r * r * (total * inv)));  // - r^3 mean(dh w y)
+    float total[kApart];
+    if constexpr (kApart == 1) total[0] = pairwise(s);
+    else
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      f2 t[4];
-      float o[8];
+      for (int v = 0; v < V; ++v) total[v] = s[v];
+    const f2 rr = both(r), back = both(-(r * r * r * (unit_sum<MULTI>(total, u, red, calls) * inv)));  // - r^3 mean(dh w y)
+    f2 (&t)[V][4] = dv;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const f2 g = mul2(gv[v][i], rr);
         sums[v][i] = fma2(g, yv[v][i], sums[v][i]);
-        t[i] = fma2(back, yv[v][i], fma2(g, w[v][i], dv[v][i]));
+        t[v][i] = fma2(back, yv[v][i], fma2(g, w[v][i], dv[v][i]));
       }
-      if (a.dx) {
-        unpack8(o, t);
-        store8_warp<T, VEC>(dx_out + v * next_run, o, n[v], u.first, u.last, live);
-      }
-      if (a.drop.cut) {
+    if (a.dx) store_chunks<T, VEC, MULTI>(dx_out, next_run, t, n, u, live);
+    if (a.drop.cut) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
         uint32_t bits[4];
-        philox(bits, a.drop, (uint32_t)(v * tpr + u.t), (uint32_t)row);
-        drop8(t, a.drop, bits);
+        philox(bits, a.drop, (uint32_t)(col(v) >> 3), (uint32_t)row);
+        drop8(t[v], a.drop, bits);
       }
-      unpack8(o, t);
-      store8_warp<T, VEC>(df_out + v * next_run, o, n[v], u.first, u.last, live);
     }
+    store_chunks<T, VEC, MULTI>(df_out, next_run, t, n, u, live);
     dx_out += dx_step;
     df_out += df_step;
   }
@@ -469,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
       unpack8(o, sums[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < n[v]) out[(v * tpr + u.t) * 8 + e] = o[e];
+        if (e < n[v]) out[col(v) + e] = o[e];
     }
   } else {  // the units of a warp, then the warps, one after the other
     float o[V][8];
@@ -486,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
         for (int v = 0; v < V; ++v)
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            const int c = (v * tpr + u.t) * 8 + e;
+            const int c = col(v) + e;
             lines[c] = k ? lines[c] + o[v][e] : o[v][e];
           }
       __syncthreads();
@@ -498,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
 // The column sums of long rows are kept in the CTA's row of parts.
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const AddNormBwdArgs a) {
-  __shared__ __align__(16) float red[2][16];
+  __shared__ __align__(16) float red[2 * kSums];
   const Unit u(kLongThreads, true);
   clear_sums(red);
   uint32_t calls = 0;
@@ -518,7 +598,8 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const A
 #pragma unroll
       for (int e = 0; e < 8; ++e) s = fmaf(dh[e] * w[e], y[e], s);
     }
-    s = unit_sum<true>(s, u, red, calls);
+    float one[1] = {s};
+    s = unit_sum<true>(one, u, red, calls);
     const float r = a.rstd[row], back = r * r * r * (s * (1.f / (float)a.cols));
 #pragma unroll 2
     for (int64_t p = 0; p < panels; ++p) {
@@ -533,13 +614,13 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const A
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (e < n) out[c + e] = sums[e];
-      if (a.dx) store8_warp<T, VEC>((T*)a.dx + row * a.lddx + c, t, left, u.first, u.last, true);
+      if (a.dx) store8_warp<T, VEC, true>((T*)a.dx + row * a.lddx + c, t, left, u.first, u.last, true);
       if (a.drop.cut) {
         uint32_t bits[4];
         philox(bits, a.drop, (uint32_t)(c >> 3), (uint32_t)row);
         drop8(t, a.drop, bits);
       }
-      store8_warp<T, VEC>((T*)a.df + row * a.lddf + c, t, left, u.first, u.last, true);
+      store8_warp<T, VEC, true>((T*)a.df + row * a.lddf + c, t, left, u.first, u.last, true);
     }
   }
 }
@@ -576,7 +657,7 @@ cudaError_t start(K kernel, const A& a, int64_t ctas, int threads, int smem, int
 // f(kernel, shared memory of a warp) for a shape.
 template <typename T, bool VEC, typename F>
 cudaError_t with_fwd(const Shape& sh, F f) {
-  constexpr int two = Ring<T, VEC, 2, 2, depth<T, 2>()>::kWarp, four = Ring<T, VEC, 4, 2, depth<T, 4>()>::kWarp;
+  constexpr int two = Ring<T, VEC, 2, 1, 2, depth<T, 2>()>::kWarp, four = Ring<T, VEC, 4, 1, 2, depth<T, 4>()>::kWarp;
   if (sh.v == 4) return f(add_norm_fwd_kernel<T, VEC, 4, 512, 1, true>, four);
   if (sh.tpr > 256) return f(add_norm_fwd_kernel<T, VEC, 2, 512, 1, true>, two);
   if (sh.tpr > 32) return f(add_norm_fwd_kernel<T, VEC, 2, 256, kFwdCtas, true>, two);
@@ -585,9 +666,9 @@ cudaError_t with_fwd(const Shape& sh, F f) {
 template <typename T, bool VEC, typename F>
 cudaError_t with_bwd(const Shape& sh, F f) {
   constexpr int D = depth<T, 2>();
-  if (sh.tpr > 256) return f(add_norm_bwd_kernel<T, VEC, 2, 512, 1, true>, Ring<T, VEC, 2, 3, D>::kWarp);
-  if (sh.tpr > 32) return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, true>, Ring<T, VEC, 2, 3, D>::kWarp);
-  return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, false>, Ring<T, VEC, 2, 3, D>::kWarp);
+  if (sh.tpr > 256) return f(add_norm_bwd_kernel<T, VEC, 2, 512, 1, true>, Ring<T, VEC, 2, 1, 3, D>::kWarp);
+  if (sh.tpr > 32) return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, true>, Ring<T, VEC, 2, 1, 3, D>::kWarp);
+  return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, false>, Ring<T, VEC, 2, 1, 3, D>::kWarp);
 }
 
 template <typename T, bool VEC>

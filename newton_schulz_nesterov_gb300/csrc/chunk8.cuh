@@ -16,6 +16,7 @@
 
 #include "f32x2.cuh"
 #include "pieces.cuh"
+#include "ptx.cuh"
 
 namespace dmuon {
 
@@ -148,14 +149,25 @@ __device__ __forceinline__ void pack8(uint32_t* w, const float (&f)[8]) {
   }
 }
 
+// N words to p, 16-byte aligned; 32 bytes at a time where it is aligned to them.
+template <int N>
+__device__ __forceinline__ void store_words(uint8_t* p, const uint32_t (&w)[N]) {
+  if (N % 8 == 0 && ((uintptr_t)p & 31) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; i += 8) ptx::st_global_v8(p + 4 * i, w + i);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < N; i += 4) *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+}
+
 // The first n of eight values to p, 16-byte aligned.
 template <typename T>
 __device__ __forceinline__ void store8(T* p, const float (&f)[8], int n) {
   uint32_t w[words8<T>()];
   pack8<T>(w, f);
   if (n >= 8) {
-#pragma unroll
-    for (int i = 0; i < words8<T>(); i += 4) *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(p) + i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    store_words(reinterpret_cast<uint8_t*>(p), w);
     return;
   }
 #pragma unroll
@@ -166,13 +178,105 @@ __device__ __forceinline__ void store8(T* p, const float (&f)[8], int n) {
     }
 }
 
-// The same for a warp, whose lanes hold consecutive runs of eight; rows on any
-// element.  `first`, `last`, `live` as in store_pieces; n: of the row from p on.
-template <typename T, bool VEC>
+// A warp's words, N consecutive ones a lane, to a row on any element of SIZE bytes, p
+// this lane's place in it.  Lane k > 0 stores the 16 bytes that its first element
+// lies in, the first words of which lane k - 1 has, and those behind them; the
+// elements before lane 1's and behind lane 31's pieces, fewer than eight either
+// side, are stored one a lane.
+template <int K, int N>
+__device__ __forceinline__ void shift_up(uint32_t (&o)[N], const uint32_t (&w)[N], uint32_t sh) {  // o[i] = stream word K + i, shifted
+  uint32_t s[N + 1];
+#pragma unroll
+  for (int i = 0; i <= N; ++i) {
+    const int at = K + i;  // of the four last words of the lane before and then this lane's
+    s[i] = at < 4 ? __shfl_up_sync(0xffffffffu, w[at < 4 ? N - 4 + at : 0], 1) : w[at < 4 ? 0 : at - 4];
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) o[i] = __funnelshift_r(s[i], s[i + 1], sh);
+}
+template <int SIZE, int N>
+__device__ __forceinline__ void store_row(uint8_t* p, const uint32_t (&w)[N]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t m = __shfl_sync(0xffffffffu, past16(p), 0);
+  if (m == 0) {
+    store_words(p, w);
+    return;
+  }
+  uint32_t o[N];
+  const uint32_t sh = (m & 2) * 8;
+  switch ((16 - m) >> 2) {
+    case 0: shift_up<0>(o, w, sh); break;
+    case 1: shift_up<1>(o, w, sh); break;
+    case 2: shift_up<2>(o, w, sh); break;
+    default: shift_up<3>(o, w, sh); break;
+  }
+  if (lane > 0) *reinterpret_cast<uint4*>(p - m) = make_uint4(o[0], o[1], o[2], o[3]);
+#pragma unroll
+  for (int i = 4; i < N; i += 4) *reinterpret_cast<uint4*>(p - m + 4 * i) = make_uint4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+  // Element e of lane 0's first 16 bytes, or of lane 31's last.
+  constexpr int kPer = 16 / SIZE;
+  const int e = lane & (kPer - 1);
+  const bool end = lane & kPer;
+  uint32_t g[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) g[i] = __shfl_sync(0xffffffffu, lane == 31 ? w[N - 4 + i] : w[i], end ? 31 : 0);
+  const int at = e * SIZE / 4;
+  const uint32_t low = at & 1 ? g[1] : g[0], high = at & 1 ? g[3] : g[2], word = at & 2 ? high : low;
+  if (lane < 2 * kPer && (end ? e * SIZE >= 16 - (int)m : e * SIZE < 16 - (int)m)) {
+    uint8_t* to = p - lane * 4 * N + (end ? 32 * 4 * N - 16 : 0) + e * SIZE;
+    if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(to) = word;
+    else *reinterpret_cast<uint16_t*>(to) = (uint16_t)(e & 1 ? word >> 16 : word);
+  }
+}
+
+// 8 V consecutive values a lane, a warp's after one another, to a row on any
+// element (VEC: 16-byte aligned); n: of the row from p on.
+template <typename T, bool VEC, int V>
+__device__ __forceinline__ void store_wide(T* p, const f2 (&f)[V][4], int n) {
+  constexpr int N = words8<T>();
+  uint32_t w[V * N];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 q = unpack2(f[v][i]);
+      o[2 * i] = q.x;
+      o[2 * i + 1] = q.y;
+    }
+    pack8<T>(w + v * N, o);
+  }
+  if (VEC) {
+    if (n >= 8 * V) {
+      store_words(reinterpret_cast<uint8_t*>(p), w);
+      return;
+    }
+  } else if (__all_sync(0xffffffffu, n >= 8 * V)) {
+    store_row<(int)sizeof(T)>(reinterpret_cast<uint8_t*>(p), w);
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8 * V; ++e)
+    if (e < n) {
+      if constexpr (sizeof(T) == 4) reinterpret_cast<uint32_t*>(p)[e] = w[e];
+      else reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+    }
+}
+
+// The same for a warp whose lanes hold consecutive runs of eight of one row (ROW) or
+// of several; n: elements of the row from p on.  `first`, `last`, `live` as in
+// store_pieces.
+template <typename T, bool VEC, bool ROW = false>
 __device__ __forceinline__ void store8_warp(T* p, const float (&f)[8], int64_t n, bool first, bool last, bool live) {
   if constexpr (VEC) {
     if (live) store8<T>(p, f, (int)min((int64_t)8, n));
   } else {
+    if (ROW && __all_sync(0xffffffffu, live && n >= 8)) {
+      uint32_t w[words8<T>()];
+      pack8<T>(w, f);
+      store_row<(int)sizeof(T)>(reinterpret_cast<uint8_t*>(p), w);
+      return;
+    }
     constexpr int W = words8<T>();
     uint32_t w[W + 8];
     pack8<T>(w + 4, f);

@@ -45,7 +45,9 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a, 
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] += g[e];
     }
-    store8_warp<T, VEC>((T*)a.out + r * a.ldout + col, f, left, lane == 0, lane == lanes - 1, r < a.rows);
+    T* out = (T*)a.out + r * a.ldout + col;
+    if (lanes == 32) store8_warp<T, VEC, true>(out, f, left, lane == 0, lane == lanes - 1, r < a.rows);
+    else store8_warp<T, VEC>(out, f, left, lane == 0, lane == lanes - 1, r < a.rows);
   }
 }
 
