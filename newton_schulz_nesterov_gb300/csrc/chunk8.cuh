@@ -129,6 +129,47 @@ __device__ __forceinline__ void take8(f2 (&f)[4], const uint8_t* at, uint32_t m)
   }
 }
 
+// 32 bytes of a row a lane, as loaded: the aligned pieces that hold one of them.
+template <bool VEC>
+struct Raw32 {
+  uint32_t w[VEC ? 8 : 12];
+};
+// bytes: of the row from p on (none wanted: below 1).
+template <bool VEC>
+__device__ __forceinline__ void load_raw32(Raw32<VEC>& r, const uint8_t* p, int bytes) {
+  const uint32_t m = VEC ? 0u : past16(p);
+  const uint4* piece = reinterpret_cast<const uint4*>(p - m);
+  const int end = bytes > 0 ? (int)m + min(bytes, 32) : 0;
+#pragma unroll
+  for (int i = 0; i < (VEC ? 2 : 3); ++i) {
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (16 * i < end) v = piece[i];
+    r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
+  }
+}
+// The values, those of the first `bytes` the row's.
+template <typename T, bool VEC>
+__device__ __forceinline__ void values32(f2 (&f)[16 / sizeof(T)], const Raw32<VEC>& r, const uint8_t* p) {
+  uint32_t w[8];
+  if constexpr (VEC) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = r.w[i];
+  } else {
+    shift_out<8>(w, r.w, past16(p));
+  }
+#pragma unroll
+  for (int k = 0; k < 16 / (int)sizeof(T); ++k) {
+    if constexpr (sizeof(T) == 4) {
+      f[k] = pack2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+    } else if constexpr (std::is_same<T, __half>::value) {
+      const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[k]));
+      f[k] = pack2(v.x, v.y);
+    } else {
+      f[k] = pack2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xFFFF0000u));
+    }
+  }
+}
+
 // Eight values rounded to T, as words.
 template <typename T>
 __device__ __forceinline__ void pack8(uint32_t* w, const float (&f)[8]) {
@@ -226,6 +267,28 @@ __device__ __forceinline__ void store_row(uint8_t* p, const uint32_t (&w)[N]) {
     uint8_t* to = p - lane * 4 * N + (end ? 32 * 4 * N - 16 : 0) + e * SIZE;
     if constexpr (SIZE == 4) *reinterpret_cast<uint32_t*>(to) = word;
     else *reinterpret_cast<uint16_t*>(to) = (uint16_t)(e & 1 ? word >> 16 : word);
+  }
+}
+
+// 32 bytes a lane, consecutive lanes' after one another in rows of `lanes` lanes;
+// bytes: of the row from p on.  w: words 4 to 11, the rest is scratch.
+template <int SIZE, bool VEC>
+__device__ __forceinline__ void store32(uint8_t* p, uint32_t (&w)[16], int64_t bytes, int lane, int lanes, bool live) {
+  if constexpr (VEC) {
+    if (!live || bytes <= 0) return;
+    if (bytes >= 32) {
+      store_words(p, *reinterpret_cast<const uint32_t(*)[8]>(w + 4));
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 32 / SIZE - 1; ++e)
+      if (e * SIZE < bytes) {
+        if constexpr (SIZE == 4) reinterpret_cast<uint32_t*>(p)[e] = w[4 + e];
+        else reinterpret_cast<uint16_t*>(p)[e] = (uint16_t)(w[4 + e / 2] >> (16 * (e & 1)));
+      }
+  } else {
+    if (lanes == 32 && __all_sync(0xffffffffu, live && bytes >= 32)) store_row<SIZE>(p, *reinterpret_cast<const uint32_t(*)[8]>(w + 4));
+    else store_pieces<SIZE>(p, w, bytes, lane == 0, lane == lanes - 1 || bytes < 64, live);
   }
 }
 

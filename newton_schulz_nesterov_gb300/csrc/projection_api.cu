@@ -346,7 +346,7 @@ int dmuon_dropout(dmuon_handle_t h, const void* x, int dtype, int64_t rows, int6
     return rc;
   if (rows > 1 && ((out == x && ldout != ldx) || (out == residual && ldout != ldres)))
     return fail(h, DMUON_ERR_ARG, "dropout: out is an input with another leading dimension");
-  if (((rows + 31) / 32) * ((cols + 255) / 256) > INT32_MAX) return fail(h, DMUON_ERR_ARG, "dropout: too many tiles");
+  if (((rows + 7) / 8) * ((cols + 255) / 256) > INT32_MAX) return fail(h, DMUON_ERR_ARG, "dropout: too many tiles");
   if (cudaSetDevice(h->device) != cudaSuccess) return fail(h, DMUON_ERR_CUDA, "cudaSetDevice");
   cudaStream_t stream = (cudaStream_t)stream_;
   a.x = x;
