@@ -3,13 +3,14 @@
 // activations' type, and h and its MXFP8 codes come from y before it is rounded.
 //
 // A row is held by a unit of threads, V chunks of eight columns a thread, so that
-// it is read once: part of a warp up to 256 columns, a warp up to 512, a CTA up
-// to 16384 (backward: 8192).  A unit goes from row to row with its columns' weights
-// (and, backward, their sums) in registers; the coming rows are on their way to a
-// ring in shared memory (cp.async: no registers), each warp's part its own, so that
-// only the row's sums meet at a barrier.  Longer rows are read in two passes by one
-// CTA (add_norm_long_*).
-// A block of 32 columns is four lanes, so its scale byte takes two exchanges.
+// it is read once: part of a warp up to 256 columns, a warp up to 512, a CTA of as
+// many warps as it takes up to 16384 (backward: 8192).  A unit goes from row to row
+// with its columns' weights (and, backward, their sums) in registers; the coming
+// rows are on their way to a ring in shared memory (cp.async: no registers), each
+// warp's part its own, so that only the row's sums meet at a barrier.  Longer rows
+// are read in two passes by one CTA (add_norm_long_*).
+// A block of 32 columns is four lanes (two of 16 columns), so its scale byte takes
+// two exchanges or one.
 #include <algorithm>
 
 #include "../../include/dmuon.h"
@@ -46,20 +47,30 @@ struct Unit {
 // Sums over a unit, to all of it.  A chunk's eight products are added up by its lane,
 // then chunks pairwise by the bits of their number, from the lowest: the order
 // does not depend on which lane has which chunk, nor on the type.  N sums a lane
-// are those of chunks that lie a unit's threads apart, so they meet last.
+// are those of chunks that lie a unit's threads apart, so each is a sum of 32
+// chunks when it leaves its warp.
 // Consecutive calls of a CTA alternate between the halves of `red`: one is written
 // again only after the next call's barrier, when every thread has read it.  What no
 // warp writes is zero (clear_sums, ahead of the first call's barrier).
-constexpr int kSums = 4 * 16;  // of a half: N sums of 16 warps
-__device__ __forceinline__ void clear_sums(float* red) {
+constexpr int kSums = 64;  // of a half: 16 warps, up to four each
+__device__ __forceinline__ void clear_sums(float* red, int sums) {
   for (int i = threadIdx.x; i < 2 * kSums; i += blockDim.x)
-    if (i % 16 >= (int)blockDim.x / 32) red[i] = 0.f;
+    if (i % kSums >= sums * ((int)blockDim.x / 32)) red[i] = 0.f;
 }
 template <int N>
 __device__ __forceinline__ float pairwise(const float (&v)[N]) {
   if constexpr (N == 1) return v[0];
   else if constexpr (N == 2) return v[0] + v[1];
   else return (v[0] + v[1]) + (v[2] + v[3]);
+}
+__device__ __forceinline__ float sum16(const float* p) {
+  float s[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float4 q = reinterpret_cast<const float4*>(p)[i];
+    s[i] = (q.x + q.y) + (q.z + q.w);
+  }
+  return pairwise(s);
 }
 template <bool MULTI, int N>
 __device__ __forceinline__ float unit_sum(float (&v)[N], const Unit& u, float* red, uint32_t& calls) {
@@ -70,21 +81,17 @@ __device__ __forceinline__ float unit_sum(float (&v)[N], const Unit& u, float* r
       for (int k = 0; k < N; ++k) v[k] += __shfl_xor_sync(0xffffffffu, v[k], o);
   if constexpr (!MULTI) return pairwise(v);
   float* mine = red + (calls++ & 1) * kSums;
+  const int warps = blockDim.x >> 5;
   if (u.lane == 0)
 #pragma unroll
-    for (int k = 0; k < N; ++k) mine[k * 16 + u.warp] = v[k];
+    for (int k = 0; k < N; ++k) mine[k * warps + u.warp] = v[k];
   __syncthreads();
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const float4* four = reinterpret_cast<const float4*>(mine + k * 16);
-    const float4 p = four[0], q = four[1];
-    v[k] = ((p.x + p.y) + (p.z + p.w)) + ((q.x + q.y) + (q.z + q.w));
-    if (blockDim.x > 256) {
-      const float4 r = four[2], t = four[3];
-      v[k] += ((r.x + r.y) + (r.z + r.w)) + ((t.x + t.y) + (t.z + t.w));
-    }
+  float s = sum16(mine);
+  if (N * warps > 16) {
+    s += sum16(mine + 16);
+    if (N * warps > 32) s += sum16(mine + 32) + sum16(mine + 48);
   }
-  return pairwise(v);
+  return s;
 }
 
 // Scale bytes past the matrix are zero: rows from `rows` to the last tile's end, a
@@ -308,7 +315,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const Add
 #pragma unroll
   for (int s = 0; s < D; ++s) fetch();
   if (a.q) zero_rows_behind(a.q_scales, a.rows, a.cols);
-  clear_sums(red);
+  clear_sums(red, kApart);
   const float inv = 1.f / (float)a.cols;
   T* y_out = (T*)a.y + row * a.ldy + col(0);
   T* h_out = (T*)a.h + row * a.ldh + col(0);
@@ -378,7 +385,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const AddNormFwdArgs a) {
   __shared__ __align__(16) float red[2 * kSums];
   const Unit u(kLongThreads, true);
-  clear_sums(red);
+  clear_sums(red, 1);
   uint32_t calls = 0;
   if (a.q) zero_rows_behind(a.q_scales, a.rows, a.cols);
   const int64_t panels = (a.cols + kLongThreads * 8 - 1) / (kLongThreads * 8);
@@ -482,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
   };
 #pragma unroll
   for (int s = 0; s < D; ++s) fetch();
-  clear_sums(red);
+  clear_sums(red, kApart);
   const float inv = 1.f / (float)a.cols;
   float next_r = row < a.rows ? a.rstd[row] : 0.f;
   T* dx_out = (T*)a.dx + row * a.lddx + col(0);
@@ -547,9 +554,11 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
     for (int v = 0; v < V; ++v) {
       float o[8];
       unpack8(o, sums[v]);
+      if (((uintptr_t)out & 15) == 0) store8<float>(out + col(v), o, n[v]);
+      else
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n[v]) out[col(v) + e] = o[e];
+        for (int e = 0; e < 8; ++e)
+          if (e < n[v]) out[col(v) + e] = o[e];
     }
   } else {  // the units of a warp, then the warps, one after the other
     float o[V][8];
@@ -580,7 +589,7 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const AddNormBwdArgs a) {
   __shared__ __align__(16) float red[2 * kSums];
   const Unit u(kLongThreads, true);
-  clear_sums(red);
+  clear_sums(red, 1);
   uint32_t calls = 0;
   const int64_t panels = (a.cols + kLongThreads * 8 - 1) / (kLongThreads * 8);
   float* out = a.parts + (int64_t)blockIdx.x * a.part_ld;
@@ -634,10 +643,13 @@ struct Shape {
 // the registers they take as many warps: 16384 x 4096 bf16 to MXFP8 with dropout
 // 104 us either way, one row 13.5 us against 11.7.
 Shape shape_of(int64_t cols) {
-  if (cols > 8192) return {512, 512, 4};
+  if (cols > 512) {
+    const int v = cols > 8192 ? 4 : 2, threads = (int)((cols + v * 256 - 1) / (v * 256)) * 32;
+    return {threads, threads, v};
+  }
   int tpr = 4;
   while (tpr * 16 < cols) tpr *= 2;
-  return {tpr, tpr <= 32 ? 256 : tpr, 2};
+  return {tpr, 256, 2};
 }
 constexpr int kFwdCtas = 3, kBwdCtas = 2;  // of 256 threads on an SM
 // CTAs for `rows`: what an SM holds together, and two rows a unit where that many
