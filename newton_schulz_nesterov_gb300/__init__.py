@@ -845,8 +845,14 @@ def dmuon_act_backward(h, dout, pre, act, dz=None, d_bias=None, by_rows=None, by
         _check(rc, "dmuon_act_backward", h)
 
 
+def _check_uint64(seed, offset):
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        raise ValueError("seed and offset must be from 0 to 2^64 - 1")
+
+
 def _add_norm(h, x, f, y, w, rstd, out, q, mode, p, seed, offset, eps, like):
     """The fields that forward and backward share; ``like`` is f, or df."""
+    _check_uint64(seed, offset)
     index = _device(h, like, "f")
     fp, ldf, code, size = _matrix(like, "f", index)
     rows, cols = size
@@ -892,6 +898,7 @@ def dmuon_dropout(h, x, out, p, seed, offset=0, residual=None, stream=None):
     probability 1 - p, as (p, seed, offset, row, column) tell, and is then scaled
     by 1 / (1 - p).  The same call on a gradient is the backward pass; out may be
     x or residual."""
+    _check_uint64(seed, offset)
     index = _device(h, x, "x")
     ptr, ld, code, size = _matrix(x, "x", index)
     first = index, x.dtype, code, size

@@ -88,28 +88,28 @@ __device__ __forceinline__ f2 normal_below2(f2 z, f2& bell) {
 }
 
 // f[i] = act(f[i])
-template <int N>
-__device__ __forceinline__ void act_values(f2 (&f)[N], const Act& act) {
-  if (act.kind == kActClamp) {
+template <int KIND, int N>
+__device__ __forceinline__ void act_values_of(f2 (&f)[N], const Act& act) {
+  const f2 a = both(act.a), b = both(act.b);
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+  for (int i = 0; i < N; ++i) {
+    if constexpr (KIND == kActClamp) {
       const float2 p = unpack2(f[i]);
       f[i] = pack2(p.x < act.a ? 0.f : p.x, p.y < act.a ? 0.f : p.y);
-    }
-  } else if (act.kind == kActGate) {
-    const f2 a = both(act.a), b = both(act.b);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
+    } else if constexpr (KIND == kActGate) {
       const f2 z = act_inside2(f[i]);
       f[i] = mul2(f[i], rcp_fast2(add2(exp2_fast2(mul2(z, fma2(b, mul2(z, z), a))), both(1.f))));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
+    } else {
       f2 bell;
       f[i] = mul2(f[i], normal_below2(act_inside2(f[i]), bell));
     }
   }
+}
+template <int N>
+__device__ __forceinline__ void act_values(f2 (&f)[N], const Act& act) {
+  if (act.kind == kActClamp) act_values_of<kActClamp>(f, act);
+  else if (act.kind == kActGate) act_values_of<kActGate>(f, act);
+  else act_values_of<kActErf>(f, act);
 }
 
 // g[i] *= act'(z[i]); relu has slope 0 at 0, and where z is below it the

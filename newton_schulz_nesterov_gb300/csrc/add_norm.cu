@@ -732,7 +732,8 @@ cudaError_t add_norm_configure() {
 }
 
 int64_t add_norm_bwd_ctas(int64_t rows, int64_t cols, int sms) {
-  if (cols > kMostBwd) return std::min<int64_t>(rows, 2 * sms);
+  // Long rows: at most a gigabyte of partial sums.
+  if (cols > kMostBwd) return std::min<int64_t>(rows, std::min<int64_t>(2 * sms, std::max<int64_t>(1, (1 << 28) / cols)));
   return ctas_of(shape_of(cols), rows, sms, kBwdCtas);
 }
 

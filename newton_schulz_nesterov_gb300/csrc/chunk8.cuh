@@ -1,11 +1,12 @@
 // Eight consecutive elements of a row, loaded and stored by one thread, in rows
 // that are 16-byte aligned (VEC) or on any element.
 //
-// Loads take the aligned 16-byte pieces that hold one of the wanted elements
-// (such a piece lies in one allocation, whatever else is in it) and shift them
-// together: 8191 columns of bf16 cost two loads and fifteen selects for eight
-// elements, where single elements would cost eight loads that touch a line a
-// lane.  Stores of a warp whose lanes hold consecutive runs go by pieces.cuh.
+// Loads take the aligned 16-byte pieces that hold one of the wanted elements and
+// shift them together: 8191 columns of bf16 cost two loads and fifteen selects for
+// eight elements, where single elements would cost eight loads that touch a line a
+// lane.  A row's first piece begins at most 15 bytes before it (where it does, the
+// matrix does not begin an allocation); its last is cut off at the row's end, or at
+// the matrix's.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,6 +31,20 @@ struct Raw8 {
   uint32_t w[kWords];
 };
 
+// The first `bytes` (a multiple of SIZE) of a 16-byte piece, zeros behind them.
+template <int SIZE>
+__device__ __forceinline__ uint4 load_piece(const uint4* piece, int bytes) {
+  if (bytes >= 16) return *piece;
+  uint32_t w[4] = {0, 0, 0, 0};
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(piece);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    if (4 * k + 4 <= bytes) w[k] = p[k];
+    else if (SIZE == 2 && 4 * k + 2 <= bytes) w[k] = reinterpret_cast<const uint16_t*>(piece)[2 * k];
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // n: elements of the row from p on; those past the eighth are not wanted.
 template <typename T, bool VEC>
 __device__ __forceinline__ void load_raw8(Raw8<T, VEC>& r, const T* p, int n) {
@@ -38,8 +53,7 @@ __device__ __forceinline__ void load_raw8(Raw8<T, VEC>& r, const T* p, int n) {
   const int bytes = (int)m + min(n, 8) * (int)sizeof(T);
 #pragma unroll
   for (int i = 0; i < Raw8<T, VEC>::kWords / 4; ++i) {
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (n > 0 && 16 * i < bytes) v = piece[i];
+    const uint4 v = load_piece<(int)sizeof(T)>(piece + i, n > 0 ? (n >= 8 + 16 / (int)sizeof(T) ? 16 : bytes - 16 * i) : 0);
     r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
   }
 }
@@ -134,8 +148,9 @@ template <bool VEC>
 struct Raw32 {
   uint32_t w[VEC ? 8 : 12];
 };
-// bytes: of the row from p on (none wanted: below 1).
-template <bool VEC>
+// bytes: of the row from p on (none wanted: below 1).  END: the matrix may end with
+// it, so its last piece is cut off; else 16 bytes of the matrix follow the row.
+template <int SIZE, bool VEC, bool END>
 __device__ __forceinline__ void load_raw32(Raw32<VEC>& r, const uint8_t* p, int bytes) {
   const uint32_t m = VEC ? 0u : past16(p);
   const uint4* piece = reinterpret_cast<const uint4*>(p - m);
@@ -143,7 +158,7 @@ __device__ __forceinline__ void load_raw32(Raw32<VEC>& r, const uint8_t* p, int 
 #pragma unroll
   for (int i = 0; i < (VEC ? 2 : 3); ++i) {
     uint4 v = make_uint4(0, 0, 0, 0);
-    if (16 * i < end) v = piece[i];
+    if (16 * i < end) v = END ? load_piece<SIZE>(piece + i, end - 16 * i) : piece[i];
     r.w[4 * i] = v.x; r.w[4 * i + 1] = v.y; r.w[4 * i + 2] = v.z; r.w[4 * i + 3] = v.w;
   }
 }

@@ -28,12 +28,18 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const DropoutArgs a, 
   const uint8_t* x = (const uint8_t*)a.x + (row0 * a.ldx + col) * S;
   const uint8_t* res = (const uint8_t*)a.res + (row0 * a.ldres + col) * S;
   Raw32<VEC> xr[ROWS], rr[ROWS];
+  auto load = [&](auto end) {
+    constexpr bool kEnd = decltype(end)::value;
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) {
-    const int here = row0 + at_once * i < a.rows ? left : 0;
-    load_raw32<VEC>(xr[i], x + i * at_once * a.ldx * S, here);
-    if (a.res) load_raw32<VEC>(rr[i], res + i * at_once * a.ldres * S, here);
-  }
+    for (int i = 0; i < ROWS; ++i) {
+      const int here = row0 + at_once * i < a.rows ? left : 0;
+      load_raw32<S, VEC, kEnd>(xr[i], x + i * at_once * a.ldx * S, here);
+      if (a.res) load_raw32<S, VEC, kEnd>(rr[i], res + i * at_once * a.ldres * S, here);
+    }
+  };
+  // Sixteen rows of the matrix, 16 bytes at least, follow all of a CTA's but in the last CTAs.
+  if ((int64_t)(blockIdx.x / ct + 1) * ROWS * at_once + 16 <= a.rows) load(std::false_type());
+  else load(std::true_type());
 #pragma unroll
   for (int i = 0; i < ROWS; ++i) {
     const int64_t r = row0 + at_once * i;

@@ -359,6 +359,10 @@ __device__ __forceinline__ void store_block(const A& a, int64_t row0, int64_t co
     T* dst = d + (row0 + lr) * a.ldd + col0 + lc * 4 * kPer;
     const int64_t step = (int64_t)kRows * a.ldd;
     if constexpr (std::is_same<A, MxLinearArgs>::value) {
+      // A copy an activation, so that the instructions that run lie together: with the
+      // branch inside the unrolled loop the epilogue waited for its instructions
+      // (10822 x 8548 x 318 of MXFP8 to fp32 without an activation 125 us, so 88), and
+      // in two passes over the scratch, with a loop up to the activation, it took 109.
       const int64_t at_row = row0 + lr, at_col = col0 + lc * 4 * kPer;
 #pragma unroll
       for (int q = 0; q < 8; ++q)
@@ -370,51 +374,63 @@ __device__ __forceinline__ void store_block(const A& a, int64_t row0, int64_t co
         for (int q = 0; q < kLanes; ++q)
           old[q] = at_row + q * kRows < rows ? *reinterpret_cast<const uint4*>(c + (int64_t)(q * kRows) * a.ldc) : make_uint4(0, 0, 0, 0);
       }
-      float bias[4 * kPer];
+      f2 bias[2 * kPer];
 #pragma unroll
-      for (int e = 0; e < 4 * kPer; e += 4) {
-        const float4 b = a.bias ? *reinterpret_cast<const float4*>(a.bias + at_col + e) : make_float4(0.f, 0.f, 0.f, 0.f);
-        bias[e] = b.x; bias[e + 1] = b.y; bias[e + 2] = b.z; bias[e + 3] = b.w;
+      for (int e = 0; e < 2 * kPer; e += 2) {
+        const float4 b = a.bias ? *reinterpret_cast<const float4*>(a.bias + at_col + 2 * e) : make_float4(0.f, 0.f, 0.f, 0.f);
+        bias[e] = pack2(b.x, b.y);
+        bias[e + 1] = pack2(b.z, b.w);
       }
       __syncwarp();
-#pragma unroll
-      for (int q = 0; q < kLanes; ++q) {
-        const uint32_t* acc = scratch + (q * kRows + lr) * 36 + lc * 4 * kPer;
-        float f[4 * kPer];
-#pragma unroll
-        for (int e = 0; e < 4 * kPer; ++e) f[e] = fmaf(a.alpha, __uint_as_float(acc[e]), bias[e]);
-        const bool live = at_row + q * kRows < rows;
+      const uint32_t* mine = scratch + lr * 36 + lc * 4 * kPer;
+      auto to_words = [&](const f2 (&g)[2 * kPer]) {
         uint32_t w[4];
-        if (a.pre) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) w[k] = Pack<T>::pack(f + k * kPer);
-          if (live)
-            *reinterpret_cast<uint4*>((T*)a.pre + (at_row + q * kRows) * a.ldpre + at_col) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        f2 g[2 * kPer];
-#pragma unroll
-        for (int e = 0; e < 2 * kPer; ++e) g[e] = pack2(f[2 * e], f[2 * e + 1]);
-        act_values(g, a.act);
-#pragma unroll
-        for (int e = 0; e < 2 * kPer; ++e) {
-          const float2 p = unpack2(g[e]);
-          f[2 * e] = p.x;
-          f[2 * e + 1] = p.y;
-        }
-        if (a.c) {
-          const uint32_t o4[4] = {old[q].x, old[q].y, old[q].z, old[q].w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float o[2];
-            Pack<T>::unpack(o4[k], o);
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) f[k * kPer + e] = fmaf(a.beta, o[e], f[k * kPer + e]);
+        for (int k = 0; k < 4; ++k) {
+          float f[2];
+          if constexpr (kPer == 2) {
+            const float2 p = unpack2(g[k]);
+            f[0] = p.x;
+            f[1] = p.y;
+          } else {
+            const float2 p = unpack2(g[k / 2]);
+            f[0] = k & 1 ? p.y : p.x;
           }
+          w[k] = Pack<T>::pack(f);
         }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+      };
+      const f2 beta = both(a.beta), alpha = both(a.alpha);
+      auto values = [&](auto kind) {
+        constexpr int kKind = decltype(kind)::value;
+        T* pre = (T*)a.pre + at_row * a.ldpre + at_col;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = Pack<T>::pack(f + k * kPer);
-        if (live) *reinterpret_cast<uint4*>(dst + q * step) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
+        for (int q = 0; q < kLanes; ++q) {
+          const uint32_t* p = mine + q * kRows * 36;
+          f2 g[2 * kPer];
+#pragma unroll
+          for (int e = 0; e < 2 * kPer; e += 2) {
+            const float4 x = *reinterpret_cast<const float4*>(p + 2 * e);
+            g[e] = fma2(alpha, pack2(x.x, x.y), bias[e]);
+            g[e + 1] = fma2(alpha, pack2(x.z, x.w), bias[e + 1]);
+          }
+          const bool live = at_row + q * kRows < rows;
+          if (a.pre && live) *reinterpret_cast<uint4*>(pre + (int64_t)(q * kRows) * a.ldpre) = to_words(g);
+          act_values_of<kKind>(g, a.act);
+          if (a.c) {
+            const uint32_t o4[4] = {old[q].x, old[q].y, old[q].z, old[q].w};
+            float o[4 * kPer];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) Pack<T>::unpack(o4[k], o + k * kPer);
+#pragma unroll
+            for (int e = 0; e < 2 * kPer; ++e) g[e] = fma2(beta, pack2(o[2 * e], o[2 * e + 1]), g[e]);
+          }
+          if (live) *reinterpret_cast<uint4*>(dst + q * step) = to_words(g);
+        }
+      };
+      if (a.act.kind == kActClamp) values(std::integral_constant<int, kActClamp>());
+      else if (a.act.kind == kActGate) values(std::integral_constant<int, kActGate>());
+      else values(std::integral_constant<int, kActErf>());
     } else if (a.beta == 0.f) {
 #pragma unroll
       for (int q = 0; q < kLanes; ++q) {
@@ -973,28 +989,35 @@ __global__ void __launch_bounds__(Pair<BITS, EPI>::kThreads, 1) mx_gemm_pair_ker
   } else {
     const int quad = warp & 3;
     uint32_t* mine = scratch + (warp - 2) * kScratch;
+    const T* added = (const T*)a.d;  // the matrix whose tile is added
+    int64_t ld_added = a.ldd;
+    bool adds = a.beta != 0.f;
+    if constexpr (EPI) {
+      added = (const T*)a.c;
+      ld_added = a.ldc;
+      adds = a.c != nullptr && warp < 6;  // one of the two warps of a quarter
+    }
+    // A tile of it comes to L2 while its products run: whole 16-byte pieces, the
+    // first of them the row's first element's.  (A tile ahead, while the one before
+    // is stored, 10822 x 8548 x 318 plus C to fp32 took 206 us, so 176, without 216.)
+    auto prefetch = [&](int t) {
+      if (!adds || t >= tiles) return;
+      int mt, nt;
+      tile_of(t, tm, tn, mt, nt);
+      const int64_t row = (int64_t)mt * 256 + rank * 128 + quad * 32 + lane, col0 = (int64_t)nt * 256;
+      if (row >= a.p_rows) return;
+      const T* old = added + row * ld_added + col0;
+      const uintptr_t from = (uintptr_t)old & ~(uintptr_t)15, to = (uintptr_t)(old + min((int64_t)256, a.q_rows - col0)) & ~(uintptr_t)15;
+      if (from < to)
+        asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
+    };
     uint32_t tc = 0;
     for (int t = pair; t < tiles; t += npairs, ++tc) {
       const uint32_t acc = tc & 1u;
       int mt, nt;
       tile_of(t, tm, tn, mt, nt);
       const int64_t row0 = (int64_t)mt * 256 + rank * 128 + quad * 32, col0 = (int64_t)nt * 256;
-      const T* added = (const T*)a.d;  // the matrix whose tile is added
-      int64_t ld_added = a.ldd;
-      bool adds = a.beta != 0.f;
-      if constexpr (EPI) {
-        added = (const T*)a.c;
-        ld_added = a.ldc;
-        adds = a.c != nullptr;
-      }
-      if (adds && row0 + lane < a.p_rows) {
-        // It comes to L2 while the products run: whole 16-byte pieces, the
-        // first of them the row's first element's.
-        const T* old = added + (row0 + lane) * ld_added + col0;
-        const uintptr_t from = (uintptr_t)old & ~(uintptr_t)15, to = (uintptr_t)(old + min((int64_t)256, a.q_rows - col0)) & ~(uintptr_t)15;
-        if (from < to)
-          asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
-      }
+      prefetch(t);
       if (!bounded_wait_warp(ptx::smem_addr(tfull + acc), (tc >> 1) & 1u, abort_flag, a.err, tmo)) break;
       ptx::tc_fence_after();
       const uint32_t tq = tmem + acc * P::kAccStride + ((uint32_t)(quad * 32) << 16);
@@ -1004,29 +1027,19 @@ __global__ void __launch_bounds__(Pair<BITS, EPI>::kThreads, 1) mx_gemm_pair_ker
       if constexpr (EPI) {
         // Of the two warps of a quarter one has the shared blocks 0, 2 and the
         // others 1, 3, .., one the shared block 1 and the others 0, 2, ..: four each.
-        const int h = (warp - 2) >> 2;
-        constexpr int kMine = (kShared + 1) / 2;
-        uint32_t v[kMine][32];
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-          if (h + 2 * q < kShared) ptx::tmem_ld32(tq + shared0 + (h + 2 * q) * 32, v[q]);
-        ptx::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tshared), 0));
-#pragma unroll
-        for (int q = 0; q < kMine; ++q)
-          if (h + 2 * q < kShared && col0 + shared0 + (h + 2 * q) * 32 < a.q_rows)
-            store_block<T>(a, row0, col0 + shared0 + (h + 2 * q) * 32, a.p_rows, a.q_rows, v[q], mine, lane);
+        const int h = (warp - 2) >> 2, first = (kShared + 1 - h) / 2;
+        auto block = [&](int i) { return i < first ? shared0 + (h + 2 * i) * 32 : rest0 + (1 - h + 2 * (i - first)) * 32; };
 #pragma unroll 1
-        for (int i = 1 - h; i < kRest; i += 2) {
-          const int c = rest0 + i * 32;
-          ptx::tmem_ld32(tq + c, v[0]);
-          if (i + 2 >= kRest) {
+        for (int i = 0; i < 4; ++i) {
+          const int c = block(i);
+          uint32_t v[32];
+          ptx::tmem_ld32(tq + c, v);
+          if (i + 1 == first || i == 3) {
             ptx::tc_fence_before();
             __syncwarp();
-            if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tempty + acc), 0));
+            if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(i == 3 ? tempty + acc : tshared), 0));
           }
-          if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, v[0], mine, lane);
+          if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, v, mine, lane);
         }
       } else {
         uint32_t v[P::kSharedCols];

@@ -143,13 +143,13 @@ int dmuon_mx_linear(dmuon_handle_t h, const dmuon_mx_linear_t* p, void* stream_)
   a.alpha = p->alpha;
   a.beta = p->beta;
   a.dtype = p->dtype;
-  a.c = p->c;
+  a.c = p->beta != 0.f ? p->c : nullptr;
   a.ldc = p->ldc;
   a.bias = p->bias;
   a.pre = p->pre;
   a.ldpre = p->ldpre;
   a.act = act_of(p->act);
-  a.vec = rows_aligned(p->d, p->ldd, p->dtype) && (!p->c || rows_aligned(p->c, p->ldc, p->dtype)) &&
+  a.vec = rows_aligned(p->d, p->ldd, p->dtype) && (!a.c || rows_aligned(a.c, a.ldc, p->dtype)) &&
           (!p->pre || rows_aligned(p->pre, p->ldpre, p->dtype)) && aligned(p->bias, 16);
   const Product<MxLinearArgs> product = eight ? Product<MxLinearArgs>{8, launch_mx_linear8, launch_mx_linear8_pair}
                                               : Product<MxLinearArgs>{4, launch_mx_linear4, launch_mx_linear4_pair};

@@ -159,6 +159,16 @@ def test_no_rows_of_k_and_empty(handle):
         handle.mx_linear(dm.dmuon_mxfp8_empty(m, 64), dm.dmuon_mxfp8_empty(n, 64), torch.empty((m, n), device="cuda"), 64)
 
 
+def test_a_residual_of_no_weight_is_not_read(handle):
+    a, b = dm.dmuon_mxfp8_empty(3, 64), dm.dmuon_mxfp8_empty(200, 64)
+    handle.mxfp8_quantize(torch.randn(3, 64, device="cuda"), a)
+    handle.mxfp8_quantize(torch.randn(200, 64, device="cuda"), b)
+    out, want = buffer(3, 200, "f32", False, float("nan")), buffer(3, 200, "f32", False)
+    handle.mx_linear(a, b, want, 64)
+    handle.mx_linear(a, b, out, 64, residual=out, beta=0.0)
+    assert torch.equal(out, want)
+
+
 def test_refusals(handle):
     a, b, a4 = dm.dmuon_mxfp8_empty(8, 64), dm.dmuon_mxfp8_empty(16, 64), dm.dmuon_mxfp4_empty(8, 64)
     out = torch.zeros((8, 16), device="cuda")

@@ -139,6 +139,14 @@ def test_one_on_another_device(no_library, name, arg, index):
         call(HandleOn(0), **dict(args(0), **{arg: args(index)[arg]}))
 
 
+@pytest.mark.parametrize("name", ["add_norm_forward", "add_norm_backward", "dropout"])
+@pytest.mark.parametrize("bad", [dict(seed=-1), dict(seed=1 << 64), dict(offset=-1), dict(offset=1 << 64)])
+def test_seeds_and_offsets_have_64_bits(no_library, name, bad):
+    call, args = CALLS[name]
+    with pytest.raises(ValueError):
+        call(HandleOn(0), **dict(args(0), **bad))
+
+
 def test_structures_match_the_header(tmp_path):
     """The sizes and last fields' offsets that the compiler sees."""
     import subprocess
