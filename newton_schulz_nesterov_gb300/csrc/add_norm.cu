@@ -4,7 +4,7 @@
 //
 // A row is held by a unit of threads, V chunks of eight columns a thread, so that
 // it is read once: part of a warp up to 256 columns, a warp up to 512, a CTA of as
-// many warps as it takes up to 16384 (backward: 8192).  A unit goes from row to row
+// many warps as it takes up to 16384.  A unit goes from row to row
 // with its columns' weights (and, backward, their sums) in registers; the coming
 // rows are on their way to a ring in shared memory (cp.async: no registers), each
 // warp's part its own, so that only the row's sums meet at a barrier.  Longer rows
@@ -25,7 +25,7 @@ namespace dmuon {
 namespace {
 
 constexpr int kLongThreads = 512;
-constexpr int kMostFwd = 16384, kMostBwd = 8192;  // columns that a unit holds
+constexpr int kMost = 16384;  // columns that a unit holds
 
 // Where a unit's threads stand.  MULTI: the CTA is one unit; else units of tpr <=
 // 32 lanes share warps.
@@ -167,10 +167,10 @@ constexpr int depth() { return (sizeof(T) == 4 ? 2 : 3) - (V == 4 ? 1 : 0); }
 // The ring of a warp: DEPTH slots of ARRAYS x RUNS runs.  A run is the 16-byte pieces
 // that C chunks of each of a unit's lanes of this warp lie in, one after the other
 // (rows on any element: one piece more), copied by those lanes piece by piece.
-template <typename T, bool VEC, int RUNS, int C, int ARRAYS, int DEPTH>
+template <typename T, bool VEC, int UNITS, int RUNS, int C, int ARRAYS, int DEPTH>  // UNITS of a warp at most
 struct Ring {
   static constexpr int W = C * words8<T>() / 4;                  // pieces of a lane
-  static constexpr int kRun = (32 * W + (VEC ? 0 : 8)) * 16;     // bytes; up to eight units a warp
+  static constexpr int kRun = (32 * W + (VEC ? 0 : UNITS)) * 16; // bytes
   static constexpr int kSlot = ARRAYS * RUNS * kRun;
   static constexpr int kWarp = DEPTH * kSlot;
   const uint8_t* mine;     // this lane's first piece in slot 0
@@ -218,11 +218,12 @@ struct Ring {
 // and 16-bit elements (one run; 32 bytes a lane, and on any element half the shifting
 // and half the ends: 16384 x 4095 bf16 forward 164 -> 140 us, backward 212 -> 176), a
 // unit's threads apart otherwise (V runs; fp32 on any element 1371 x 6082 backward
-// 48 us so, 57 one after the other).
-template <typename T, bool MULTI>
-constexpr bool wide() { return MULTI && sizeof(T) == 2; }
+// 48 us so, 57 one after the other; four chunks one after the other meet in the
+// banks of shared memory, 2048 x 16384 bf16 forward 57 us against 47).
+template <typename T, bool MULTI, int V>
+constexpr bool wide() { return MULTI && sizeof(T) == 2 && V == 2; }
 template <typename T, bool VEC, bool MULTI, int V, int ARRAYS, int DEPTH>
-using RingOf = Ring<T, VEC, wide<T, MULTI>() ? 1 : V, wide<T, MULTI>() ? V : 1, ARRAYS, DEPTH>;
+using RingOf = Ring<T, VEC, MULTI ? 1 : 8, wide<T, MULTI, V>() ? 1 : V, wide<T, MULTI, V>() ? V : 1, ARRAYS, DEPTH>;
 
 // The rows of one matrix that a unit goes through: the run that its warp fetches
 // next, and how far a row's first byte is past a 16-byte boundary.
@@ -254,7 +255,7 @@ __device__ __forceinline__ void unpack8(float (&o)[8], const f2 (&f)[4]) {
 // A row's chunks of a thread; next_run as in the kernels, n: columns from each chunk on.
 template <typename T, bool VEC, bool MULTI, int V>
 __device__ __forceinline__ void store_chunks(T* p, int next_run, const f2 (&f)[V][4], const int (&n)[V], const Unit& u, bool live) {
-  if constexpr (wide<T, MULTI>()) {
+  if constexpr (wide<T, MULTI, V>()) {
     store_wide<T, VEC, V>(p, f, n[0]);
   } else {
 #pragma unroll
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_fwd_kernel(const Add
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float red[2 * kSums];
   const Unit u(tpr, MULTI);
-  constexpr bool kWide = wide<T, MULTI>();
+  constexpr bool kWide = wide<T, MULTI, V>();
   constexpr int kRuns = kWide ? 1 : V, kApart = kWide || !MULTI ? 1 : V;
   const RingOf<T, VEC, MULTI, V, 2, D> ring(smem, u);
   auto col = [&](int v) { return kWide ? (u.t * V + v) * 8 : (v * tpr + u.t) * 8; };
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
   __shared__ __align__(16) float red[2 * kSums];
   __shared__ float lines[MULTI ? 1 : 32 * V * 8];
   const Unit u(tpr, MULTI);
-  constexpr bool kWide = wide<T, MULTI>();
+  constexpr bool kWide = wide<T, MULTI, V>();
   constexpr int kRuns = kWide ? 1 : V, kApart = kWide || !MULTI ? 1 : V;
   const RingOf<T, VEC, MULTI, V, 3, D> ring(smem, u);
   auto col = [&](int v) { return kWide ? (u.t * V + v) * 8 : (v * tpr + u.t) * 8; };
@@ -459,12 +460,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
   const int64_t step = (int64_t)gridDim.x * u.units;
   int64_t row = (int64_t)blockIdx.x * u.units + u.unit, ahead = row;
   int n[V];
-  f2 w[V][4], sums[V][4];
+  // 32 columns a thread leave no registers for the weights and for the row's values
+  // beside their sums: they are read where they are used, the values twice.
+  constexpr bool kReread = V == 4;
+  f2 w[kReread ? 1 : V][4], sums[V][4];
 #pragma unroll
   for (int v = 0; v < V; ++v) {
     const int c = col(v);
     n[v] = (int)a.cols - c;
-    load_weights(w[v], a.w + c, n[v], VEC);
+    if constexpr (!kReread) load_weights(w[v], a.w + c, n[v], VEC);
 #pragma unroll
     for (int i = 0; i < 4; ++i) sums[v][i] = 0;
   }
@@ -500,41 +504,75 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
     const bool live = MULTI || row < a.rows;
     const float r = next_r;
     next_r = row + step < a.rows ? a.rstd[row + step] : 0.f;
-    f2 gv[V][4], yv[V][4], dv[V][4];
-    float s[V];
+    float s[V], total[kApart];
     asm volatile("cp.async.wait_group %0;" ::"n"(D - 1) : "memory");
     __syncwarp();
+    f2 dv[V][4];
+    f2 (&t)[V][4] = dv;
+    auto sum = [&]() {  // of dh w y over the row, times - r^3 / cols
+      if constexpr (kApart == 1) total[0] = pairwise(s);
+      else
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      ring.take(gv[v], slot, 0, v, dh.past(row));
-      ring.take(yv[v], slot, 1, v, y.past(row));
+        for (int v = 0; v < V; ++v) total[v] = s[v];
+      return both(-(r * r * r * (unit_sum<MULTI>(total, u, red, calls) * inv)));
+    };
+    auto product = [](const f2 (&g)[4], const f2 (&y)[4], const f2 (&weight)[4]) {
+      f2 p = mul2(mul2(g[0], weight[0]), y[0]);
+#pragma unroll
+      for (int i = 1; i < 4; ++i) p = fma2(mul2(g[i], weight[i]), y[i], p);
+      return add_up(p);
+    };
+    auto take_dy = [&](int v) {
       if (a.dy) ring.take(dv[v], slot, 2, v, dy.past(row));
       else
 #pragma unroll
         for (int i = 0; i < 4; ++i) dv[v][i] = 0;
-      f2 product = mul2(mul2(gv[v][0], w[v][0]), yv[v][0]);
-#pragma unroll
-      for (int i = 1; i < 4; ++i) product = fma2(mul2(gv[v][i], w[v][i]), yv[v][i], product);
-      s[v] = add_up(product);
-    }
-    __syncwarp();
-    fetch();
-    if ((slot += ring.kSlot) == ring.kWarp) slot = 0;
-    float total[kApart];
-    if constexpr (kApart == 1) total[0] = pairwise(s);
-    else
-#pragma unroll
-      for (int v = 0; v < V; ++v) total[v] = s[v];
-    const f2 rr = both(r), back = both(-(r * r * r * (unit_sum<MULTI>(total, u, red, calls) * inv)));  // - r^3 mean(dh w y)
-    f2 (&t)[V][4] = dv;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
+    };
+    const f2 rr = both(r);
+    auto into_t = [&](int v, const f2 (&g)[4], const f2 (&yv)[4], const f2 (&weight)[4], f2 back) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const f2 g = mul2(gv[v][i], rr);
-        sums[v][i] = fma2(g, yv[v][i], sums[v][i]);
-        t[v][i] = fma2(back, yv[v][i], fma2(g, w[v][i], dv[v][i]));
+        const f2 gr = mul2(g[i], rr);
+        sums[v][i] = fma2(gr, yv[i], sums[v][i]);
+        t[v][i] = fma2(back, yv[i], fma2(gr, weight[i], dv[v][i]));
       }
+    };
+    if constexpr (!kReread) {
+      f2 gv[V][4], yv[V][4];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        ring.take(gv[v], slot, 0, v, dh.past(row));
+        ring.take(yv[v], slot, 1, v, y.past(row));
+        take_dy(v);
+        s[v] = product(gv[v], yv[v], w[v]);
+      }
+      __syncwarp();
+      fetch();
+      const f2 back = sum();
+#pragma unroll
+      for (int v = 0; v < V; ++v) into_t(v, gv[v], yv[v], w[v], back);
+    } else {
+      f2 g[4], yv[4], weight[4];
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        ring.take(g, slot, 0, v, dh.past(row));
+        ring.take(yv, slot, 1, v, y.past(row));
+        load_weights(weight, a.w + col(v), n[v], VEC);
+        s[v] = product(g, yv, weight);
+      }
+      const f2 back = sum();
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        ring.take(g, slot, 0, v, dh.past(row));
+        ring.take(yv, slot, 1, v, y.past(row));
+        take_dy(v);
+        load_weights(weight, a.w + col(v), n[v], VEC);
+        into_t(v, g, yv, weight, back);
+      }
+      __syncwarp();
+      fetch();
+    }
+    if ((slot += ring.kSlot) == ring.kWarp) slot = 0;
     if (a.dx) store_chunks<T, VEC, MULTI>(dx_out, next_run, t, n, u, live);
     if (a.drop.cut) {
 #pragma unroll
@@ -669,23 +707,24 @@ cudaError_t start(K kernel, const A& a, int64_t ctas, int threads, int smem, int
 // f(kernel, shared memory of a warp) for a shape.
 template <typename T, bool VEC, typename F>
 cudaError_t with_fwd(const Shape& sh, F f) {
-  constexpr int two = Ring<T, VEC, 2, 1, 2, depth<T, 2>()>::kWarp, four = Ring<T, VEC, 4, 1, 2, depth<T, 4>()>::kWarp;
-  if (sh.v == 4) return f(add_norm_fwd_kernel<T, VEC, 4, 512, 1, true>, four);
+  constexpr int two = RingOf<T, VEC, true, 2, 2, depth<T, 2>()>::kWarp;
+  if (sh.v == 4) return f(add_norm_fwd_kernel<T, VEC, 4, 512, 1, true>, RingOf<T, VEC, true, 4, 2, depth<T, 4>()>::kWarp);
   if (sh.tpr > 256) return f(add_norm_fwd_kernel<T, VEC, 2, 512, 1, true>, two);
   if (sh.tpr > 32) return f(add_norm_fwd_kernel<T, VEC, 2, 256, kFwdCtas, true>, two);
-  return f(add_norm_fwd_kernel<T, VEC, 2, 256, kFwdCtas, false>, two);
+  return f(add_norm_fwd_kernel<T, VEC, 2, 256, kFwdCtas, false>, RingOf<T, VEC, false, 2, 2, depth<T, 2>()>::kWarp);
 }
 template <typename T, bool VEC, typename F>
 cudaError_t with_bwd(const Shape& sh, F f) {
-  constexpr int D = depth<T, 2>();
-  if (sh.tpr > 256) return f(add_norm_bwd_kernel<T, VEC, 2, 512, 1, true>, Ring<T, VEC, 2, 1, 3, D>::kWarp);
-  if (sh.tpr > 32) return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, true>, Ring<T, VEC, 2, 1, 3, D>::kWarp);
-  return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, false>, Ring<T, VEC, 2, 1, 3, D>::kWarp);
+  constexpr int two = RingOf<T, VEC, true, 2, 3, depth<T, 2>()>::kWarp;
+  if (sh.v == 4) return f(add_norm_bwd_kernel<T, VEC, 4, 512, 1, true>, RingOf<T, VEC, true, 4, 3, depth<T, 4>()>::kWarp);
+  if (sh.tpr > 256) return f(add_norm_bwd_kernel<T, VEC, 2, 512, 1, true>, two);
+  if (sh.tpr > 32) return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, true>, two);
+  return f(add_norm_bwd_kernel<T, VEC, 2, 256, kBwdCtas, false>, RingOf<T, VEC, false, 2, 3, depth<T, 2>()>::kWarp);
 }
 
 template <typename T, bool VEC>
 cudaError_t launch_fwd(const AddNormFwdArgs& a, int sms, cudaStream_t s) {
-  if (a.cols > kMostFwd) {
+  if (a.cols > kMost) {
     add_norm_long_fwd_kernel<T, VEC><<<(unsigned)std::min<int64_t>(a.rows, 2 * sms), kLongThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
@@ -696,7 +735,7 @@ cudaError_t launch_fwd(const AddNormFwdArgs& a, int sms, cudaStream_t s) {
 
 template <typename T, bool VEC>
 cudaError_t launch_bwd(const AddNormBwdArgs& a, int64_t ctas, cudaStream_t s) {
-  if (a.cols > kMostBwd) {
+  if (a.cols > kMost) {
     add_norm_long_bwd_kernel<T, VEC><<<(unsigned)ctas, kLongThreads, 0, s>>>(a);
     return cudaGetLastError();
   }
@@ -708,7 +747,6 @@ template <typename T, bool VEC>
 cudaError_t configure() {
   for (const int64_t cols : {512, 4096, 8192, 16384}) {  // every kernel, with its most threads
     for (const bool fwd : {true, false}) {
-      if (!fwd && cols > kMostBwd) continue;
       const Shape sh = shape_of(cols);
       auto set = [&](auto kernel, int warp) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, sh.threads / 32 * warp);
@@ -733,7 +771,7 @@ cudaError_t add_norm_configure() {
 
 int64_t add_norm_bwd_ctas(int64_t rows, int64_t cols, int sms) {
   // Long rows: at most a gigabyte of partial sums.
-  if (cols > kMostBwd) return std::min<int64_t>(rows, std::min<int64_t>(2 * sms, std::max<int64_t>(1, (1 << 28) / cols)));
+  if (cols > kMost) return std::min<int64_t>(rows, std::min<int64_t>(2 * sms, std::max<int64_t>(1, (1 << 28) / cols)));
   return ctas_of(shape_of(cols), rows, sms, kBwdCtas);
 }
 

@@ -761,9 +761,9 @@ __global__ void __launch_bounds__(kThreads, 1) mx_gemm_kernel(const __grid_const
 // ---------------------------------------------------------------------------
 constexpr int kPairN = 5;
 constexpr int kPairSets = 4;
-// A tile's products take 18000 clocks at K = 4096; its epilogue by four warps takes
+// A tile's products take 18000 clocks at K = 4096; an epilogue by four warps takes
 // about as many without, and 26000 with bias, GELU and two outputs (8192 x 14336 x
-// 4096 460 and 612 thousand clocks), so that one has eight warps.
+// 4096 of MXFP8 460 and 612 thousand clocks), so that one has eight warps (472).
 template <int BITS, bool EPI>
 struct Pair {
   static constexpr int kEpiWarps = EPI ? 8 : 4;
