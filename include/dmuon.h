@@ -462,8 +462,8 @@ int dmuon_mxfp8_dequantize(dmuon_handle_t h, const void* data,
  *   z = alpha * A B^T + bias,   D = act(z) + beta * C,   pre = z
  * A m x k and B n x k in MXFP4 or MXFP8 (bits: of both), D, C and pre m x n of
  * `dtype`.  Everything is fp32 up to one rounding at each store; D comes from z
- * before it is rounded; beta == 0 does not read C.  Sizes, leading dimensions, determinism and waits as in
- * dmuon_mxfp4_gemm.
+ * before it is rounded; beta == 0 does not read C.  Sizes, leading dimensions,
+ * determinism and waits as in dmuon_mxfp4_gemm.
  */
 typedef struct {
     int64_t m, n, k;
