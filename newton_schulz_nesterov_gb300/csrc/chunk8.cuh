@@ -24,7 +24,7 @@ namespace dmuon {
 template <typename T>
 constexpr int words8() { return (int)sizeof(T) * 2; }  // 32-bit words of eight elements
 
-// Pieces of a run of eight as they are loaded; `shift` puts them together.
+// Pieces of a run of eight as they are loaded; values8 puts them together.
 template <typename T, bool VEC>
 struct Raw8 {
   static constexpr int kWords = words8<T>() + (VEC ? 0 : 4);

@@ -2,7 +2,7 @@
 // E8M0 scale per 32 elements of either operand:
 //   BITS = 4  MXFP4 (tcgen05.mma kind::mxf4, K = 64 an instruction)
 //   BITS = 8  MXFP8 (kind::mxf8f6f4 of E4M3, K = 32 an instruction)
-//   EPI = 0   D = alpha A B^T + beta D
+//   EPI = 0   D = alpha A B^T + beta D (MXFP4 only)
 //   EPI = 1   z = alpha A B^T + bias; D = act(z) + beta C, z itself to `pre`
 // The kernels are the same for both formats: an instruction takes 32 bytes of K
 // and a stage 128 bytes of every row, which is 256 or 128 elements.
@@ -171,27 +171,6 @@ __device__ __forceinline__ void tmem_ld96(uint32_t taddr, uint32_t (&v)[96]) {
         "=r"(v[80]), "=r"(v[81]), "=r"(v[82]), "=r"(v[83]), "=r"(v[84]), "=r"(v[85]), "=r"(v[86]), "=r"(v[87]),
         "=r"(v[88]), "=r"(v[89]), "=r"(v[90]), "=r"(v[91]), "=r"(v[92]), "=r"(v[93]), "=r"(v[94]), "=r"(v[95])
       : "r"(taddr), "r"(taddr + 64)
-      : "memory");
-}
-
-// 32 lanes x 64 columns, waited for.
-__device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&v)[64]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {"
-      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, "
-      "%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47, "
-      "%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [%64];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
-        "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-        "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
-        "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
-        "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
-        "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
-        "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63])
-      : "r"(taddr)
       : "memory");
 }
 
@@ -1042,9 +1021,9 @@ __global__ void __launch_bounds__(Pair<BITS, EPI>::kThreads, 1) mx_gemm_pair_ker
           if (col0 + c < a.q_rows) store_block<T>(a, row0, col0 + c, a.p_rows, a.q_rows, v, mine, lane);
         }
       } else {
+        static_assert(BITS == 4, "the product without an epilogue is MXFP4's");
         uint32_t v[P::kSharedCols];
-        if constexpr (BITS == 4) tmem_ld96(tq + shared0, v);
-        else tmem_ld64(tq + shared0, v);
+        tmem_ld96(tq + shared0, v);
         ptx::tc_fence_before();
         __syncwarp();
         if (lane == 0) arrive_remote(ptx::mapa_shared(ptx::smem_addr(tshared), 0));
