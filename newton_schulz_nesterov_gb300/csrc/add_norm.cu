@@ -434,16 +434,9 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_fwd_kernel(const A
   }
 }
 
-// t and a row's share of the column sums, from the row's sum of dh w y.
-__device__ __forceinline__ void into_t(float (&t)[8], float (&sums)[8], const float (&dy)[8], const float (&dh)[8], const float (&y)[8],
-                                       const float (&w)[8], float r, float back) {  // back: r^3 mean(dh w y)
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float dhr = dh[e] * r;
-    sums[e] = fmaf(dhr, y[e], sums[e]);
-    t[e] = fmaf(dhr, w[e], dy[e]) - back * y[e];
-  }
-}
+// The backward knows a row by yn = y r alone, which is of size one whatever y's size:
+// r^2 or r^3 by itself leaves fp32's range for rows that y, r and the gradients are
+// well inside of (r^3 below 2^-126 from a row of size 5e12 on, above 2^127 below 1e-13).
 
 template <typename T, bool VEC, int V, int kThreads, int kCtas, bool MULTI>
 __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const AddNormBwdArgs a, int tpr) {
@@ -509,17 +502,33 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
     __syncwarp();
     f2 dv[V][4];
     f2 (&t)[V][4] = dv;
-    auto sum = [&]() {  // of dh w y over the row, times - r^3 / cols
+    auto sum = [&]() {  // minus the mean of dh w yn over the row
       if constexpr (kApart == 1) total[0] = pairwise(s);
       else
 #pragma unroll
         for (int v = 0; v < V; ++v) total[v] = s[v];
-      return both(-(r * r * r * (unit_sum<MULTI>(total, u, red, calls) * inv)));
+      return both(-(unit_sum<MULTI>(total, u, red, calls) * inv));
     };
-    auto product = [](const f2 (&g)[4], const f2 (&y)[4], const f2 (&weight)[4]) {
-      f2 p = mul2(mul2(g[0], weight[0]), y[0]);
+    const f2 rr = both(r);
+    // y to yn and dh to dh w.
+    auto normalise = [&](f2 (&g)[4], f2 (&yn)[4], const f2 (&weight)[4]) {
 #pragma unroll
-      for (int i = 1; i < 4; ++i) p = fma2(mul2(g[i], weight[i]), y[i], p);
+      for (int i = 0; i < 4; ++i) {
+        yn[i] = mul2(yn[i], rr);
+        g[i] = mul2(g[i], weight[i]);
+      }
+    };
+    // The same, with the row's share of the column sums; the sum of dh w yn.
+    auto product = [&](int v, f2 (&g)[4], f2 (&yn)[4], const f2 (&weight)[4]) {
+      f2 d[4], p;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = g[i];
+      normalise(g, yn, weight);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        sums[v][i] = fma2(d[i], yn[i], sums[v][i]);
+        p = i ? fma2(g[i], yn[i], p) : mul2(g[i], yn[i]);
+      }
       return add_up(p);
     };
     auto take_dy = [&](int v) {
@@ -528,14 +537,9 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
 #pragma unroll
         for (int i = 0; i < 4; ++i) dv[v][i] = 0;
     };
-    const f2 rr = both(r);
-    auto into_t = [&](int v, const f2 (&g)[4], const f2 (&yv)[4], const f2 (&weight)[4], f2 back) {
+    auto into_t = [&](int v, const f2 (&g)[4], const f2 (&yn)[4], f2 back) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const f2 gr = mul2(g[i], rr);
-        sums[v][i] = fma2(gr, yv[i], sums[v][i]);
-        t[v][i] = fma2(back, yv[i], fma2(gr, weight[i], dv[v][i]));
-      }
+      for (int i = 0; i < 4; ++i) t[v][i] = fma2(rr, fma2(back, yn[i], g[i]), dv[v][i]);
     };
     if constexpr (!kReread) {
       f2 gv[V][4], yv[V][4];
@@ -543,14 +547,15 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
       for (int v = 0; v < V; ++v) {
         ring.take(gv[v], slot, 0, v, dh.past(row));
         ring.take(yv[v], slot, 1, v, y.past(row));
-        take_dy(v);
-        s[v] = product(gv[v], yv[v], w[v]);
+        s[v] = product(v, gv[v], yv[v], w[v]);
       }
+#pragma unroll
+      for (int v = 0; v < V; ++v) take_dy(v);  // last: before the products 16384 x 4096 bf16 takes 106 us, so 103
       __syncwarp();
       fetch();
       const f2 back = sum();
 #pragma unroll
-      for (int v = 0; v < V; ++v) into_t(v, gv[v], yv[v], w[v], back);
+      for (int v = 0; v < V; ++v) into_t(v, gv[v], yv[v], back);
     } else {
       f2 g[4], yv[4], weight[4];
 #pragma unroll
@@ -558,7 +563,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
         ring.take(g, slot, 0, v, dh.past(row));
         ring.take(yv, slot, 1, v, y.past(row));
         load_weights(weight, a.w + col(v), n[v], VEC);
-        s[v] = product(g, yv, weight);
+        s[v] = product(v, g, yv, weight);
       }
       const f2 back = sum();
 #pragma unroll
@@ -567,7 +572,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) add_norm_bwd_kernel(const Add
         ring.take(yv, slot, 1, v, y.past(row));
         take_dy(v);
         load_weights(weight, a.w + col(v), n[v], VEC);
-        into_t(v, g, yv, weight, back);
+        normalise(g, yv, weight);
+        into_t(v, g, yv, back);
       }
       __syncwarp();
       fetch();
@@ -632,22 +638,25 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const A
   const int64_t panels = (a.cols + kLongThreads * 8 - 1) / (kLongThreads * 8);
   float* out = a.parts + (int64_t)blockIdx.x * a.part_ld;
   for (int64_t row = blockIdx.x; row < a.rows; row += gridDim.x) {
-    float s = 0.f, dh[8], y[8], w[8];
+    const float r = a.rstd[row];
+    float s = 0.f, dh[8], yn[8], w[8];
     auto load = [&](int64_t c, int n) {
       load8<T, VEC>(dh, (const T*)a.dh + row * a.lddh + c, n);
-      load8<T, VEC>(y, (const T*)a.y + row * a.ldy + c, n);
+      load8<T, VEC>(yn, (const T*)a.y + row * a.ldy + c, n);
       load8<float, VEC>(w, a.w + c, n);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) yn[e] *= r;
     };
 #pragma unroll 4
     for (int64_t p = 0; p < panels; ++p) {
       const int64_t c = (p * kLongThreads + threadIdx.x) * 8;
       load(c, (int)max((int64_t)0, min((int64_t)8, a.cols - c)));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(dh[e] * w[e], y[e], s);
+      for (int e = 0; e < 8; ++e) s = fmaf(dh[e] * w[e], yn[e], s);
     }
     float one[1] = {s};
     s = unit_sum<true>(one, u, red, calls);
-    const float r = a.rstd[row], back = r * r * r * (s * (1.f / (float)a.cols));
+    const float back = s * (1.f / (float)a.cols);  // the mean of dh w yn
 #pragma unroll 2
     for (int64_t p = 0; p < panels; ++p) {
       const int64_t c = (p * kLongThreads + threadIdx.x) * 8, left = a.cols - c;
@@ -657,7 +666,11 @@ __global__ void __launch_bounds__(kLongThreads) add_norm_long_bwd_kernel(const A
       if (a.dy) load8<T, VEC>(dy, (const T*)a.dy + row * a.lddy + c, n);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sums[e] = row != blockIdx.x && e < n ? out[c + e] : 0.f;
-      into_t(t, sums, dy, dh, y, w, r, back);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        sums[e] = fmaf(dh[e], yn[e], sums[e]);
+        t[e] = fmaf(r, fmaf(-back, yn[e], dh[e] * w[e]), dy[e]);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         if (e < n) out[c + e] = sums[e];
