@@ -449,7 +449,8 @@ int dmuon_mxfp8_dequantize(dmuon_handle_t h, const void* data,
                            const void* scales, int64_t rows, int64_t k,
                            void* dst, int dtype, int64_t ld, void* stream);
 
-/* Activations of a projection's epilogue. */
+/* Activations of a projection's epilogue.  Values and slopes of magnitude below
+ * 2^-118 may come as 0. */
 #define DMUON_ACT_NONE      0
 #define DMUON_ACT_RELU      1  /* slope 0 at 0; where z <= 0 a gradient is 0
                                 * even if it was Inf or NaN                   */
@@ -462,7 +463,8 @@ int dmuon_mxfp8_dequantize(dmuon_handle_t h, const void* data,
  *   z = alpha * A B^T + bias,   D = act(z) + beta * C,   pre = z
  * A m x k and B n x k in MXFP4 or MXFP8 (bits: of both), D, C and pre m x n of
  * `dtype`.  Everything is fp32 up to one rounding at each store; D comes from z
- * before it is rounded; beta == 0 does not read C.  Sizes, leading dimensions,
+ * before it is rounded; beta == 0 does not read C.  D and pre share no memory with
+ * each other or an input, but for C, which may be D.  Sizes, leading dimensions,
  * determinism and waits as in dmuon_mxfp4_gemm.
  */
 typedef struct {
@@ -486,8 +488,9 @@ int dmuon_mx_linear(dmuon_handle_t h, const dmuon_mx_linear_t* p, void* stream);
  * `dtype` into dz and / or quantised (from fp32) to MXFP8 by rows and / or
  * columns for the two gradient products, and its column sums, the bias's
  * gradient.  NULL for what is not wanted.  Column sums run in a fixed order: the
- * same inputs give the same bits.  rows == 0 writes a zero d_bias.  Workspace for
- * d_bias as in dmuon_block_norm_backward.
+ * same inputs give the same bits.  rows == 0 writes a zero d_bias.  Outputs share no
+ * memory with each other or an input.  Workspace for d_bias as in
+ * dmuon_block_norm_backward.
  */
 typedef struct {
     int64_t rows, cols;
@@ -512,7 +515,8 @@ int dmuon_act_backward(dmuon_handle_t h, const dmuon_act_backward_t* p,
  * 2^-17 keeps everything.  The bits are those of Philox4x32-10 with key `seed` and
  * counter (column / 8, row, low and high word of offset): column 8 g + 2 j has the
  * low, 8 g + 2 j + 1 the high half of word j.  Callers give each use of one seed
- * an offset of its own.
+ * an offset of its own; a captured call keeps its own seed and offset, so every
+ * replay of a graph drops the same elements.
  *
  *   out = dropout(x) (+ residual)     rows x cols of `dtype`
  *
@@ -529,7 +533,10 @@ int dmuon_dropout(dmuon_handle_t h, const void* x, int dtype, int64_t rows,
  *   y = x + dropout(f),   h = rms(y) * w,   rms(v) = v / sqrt(mean(v^2) + eps)
  * y (the next residual stream) is rounded once to `dtype`; h comes from y before
  * its rounding and goes to `dtype` (h) and / or, from fp32, to MXFP8 by rows (q),
- * which the next projection takes.  Matrices as in dmuon_block_norm_forward.
+ * which the next projection takes.  Matrices as in dmuon_block_norm_forward; outputs
+ * share no memory with each other or an input.  The sum of y^2 is fp32's: past 3.4e38
+ * (rows of size 2.9e17 at 4096 columns) rstd and h are 0, and with eps = 0 rows of
+ * size 1e-19 and below lose bits.
  */
 typedef struct {
     int64_t rows, cols;
@@ -556,8 +563,9 @@ int dmuon_add_norm_forward(dmuon_handle_t h, const dmuon_add_norm_t* p,
  * where h went to MXFP8) and dy (gradient of y from its other uses, NULL = 0) the
  * gradients of x, of f and, in fp32, of w (written, not added; in a fixed order).
  * Takes p's y, w, rstd, p, seed and offset.  dx NULL: not wanted (without dropout
- * it is df).  rows == 0 writes a zero d_w.  Workspace as in
- * dmuon_block_norm_backward.
+ * it is df).  rows == 0 writes a zero d_w.  Takes rows of any size, with the rstd
+ * that belongs to them.  Outputs share no memory with each other or an input.
+ * Workspace as in dmuon_block_norm_backward.
  */
 typedef struct {
     const void* dy; int64_t lddy;

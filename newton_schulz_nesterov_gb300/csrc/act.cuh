@@ -9,7 +9,10 @@
 // Phi(-|z|) = exp(-z^2/2) erfcx(x) / 2 with x = |z| / sqrt 2 and erfcx(x) = exp(x^2)
 // erfc(x) as t P(t), t = 1 / (1 + 0.4 x): P of degree 8 fitted to erfcx over the
 // half line by least squares of the relative error, reweighted towards the
-// largest; off by 1.5e-7 at most, and by 5e-7 as fp32 evaluates it.  A NaN stays one.
+// largest; off by 1.5e-7 at most, and by 5e-7 as fp32 evaluates it.  exp2's argument is
+// rounded besides, so a value has 2^-21 (2 + |u|) of itself (u the exponent: z^2/2 for
+// gelu), and what exp2 or the reciprocal would make subnormal is 0: silu and gelu_tanh
+// below 2^-119, gelu below 2^-127, slopes below 2^-118.  A NaN stays one.
 #pragma once
 
 #include <cuda_runtime.h>

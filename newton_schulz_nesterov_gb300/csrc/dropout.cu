@@ -3,7 +3,7 @@
 // A lane has 32 bytes of a row, one or two groups of eight columns, and two rows, all
 // loaded before one is used; one row where two would leave SMs without work
 // (777 x 2061 fp32).  Short rows share a warp.  Bound by HBM: 16384 x 14336 bf16
-// with a residual 226 us (6.2 TB/s).
+// with a residual 213 us (6.6 TB/s).
 #include "../../include/dmuon.h"
 #include "chunk8.cuh"
 #include "dropout.cuh"

@@ -94,6 +94,10 @@ int launch_product(dmuon_ctx* h, Args& a, const Product<Args>& product, const vo
   // second wave (an SM takes about 70 bytes a clock from L2 either way, and a
   // pair's tile asks half as many of it for a product): 1024 x 4096 x 4096
   // (256 tiles) 10.5 us against 15.0, 512 x 4096 x 4096 (128) 10.2 against 8.2.
+  // The border is the same at 8 bits and with bias, GELU and two bf16 outputs (us,
+  // operands from HBM, one-CTA tiles against pairs): 512 x 4096 x 4096 16.3 against 18.5,
+  // K = 320 7.5 against 9.7; 608 x 4096 x 4096 (160 tiles) 26.8 against 18.9, K = 320
+  // 12.3 against 9.7; at 4 bits 11.9 against 14.1 and 19.7 against 14.2.
   const int64_t small_tiles = ((m + 127) / 128) * ((n + 127) / 128);
   const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
   const bool pairs = h->max_clusters > 0 && m > 128 && n > 128 && small_tiles > h->num_sms;
@@ -120,6 +124,11 @@ int launch_product(dmuon_ctx* h, Args& a, const Product<Args>& product, const vo
     // NT = 32 and about 2 us at 128, a stage 0.25 us: 1 x 4096 x 4096 6.7 us
     // whole, 4.6 in four; 512 x 512 x 512 4.4 whole, 6.2 in two.  Eight ranks of
     // 210 KB each do not all find an SM at once (128 x 4096 x 4096: 22 us).
+    // At 8 bits, with bias and a residual, operands from HBM: 1 x 4096 x 14336 25.3
+    // whole, 16.0 in two, 13.8 in four; 64 x 4096 x 4096 14.1, 15.2 and 11.4;
+    // 512 x 2048 x 14336 39.2, 31.7 and 37.9.  What the rule gets wrong is 129 to 256
+    // rows, whose tiles store a column a lane: 256 x 4096 x 4096 20.6 whole, 23.6 in
+    // two (as chosen), 18.3 on pairs.
     const int64_t stages = (k * product.bits + 1023) / 1024;
     const int most = nt == 128 ? 4 : 8;
     int split = 1;
