@@ -126,9 +126,9 @@ int launch_product(dmuon_ctx* h, Args& a, const Product<Args>& product, const vo
     // 210 KB each do not all find an SM at once (128 x 4096 x 4096: 22 us).
     // At 8 bits, with bias and a residual, operands from HBM: 1 x 4096 x 14336 25.3
     // whole, 16.0 in two, 13.8 in four; 64 x 4096 x 4096 14.1, 15.2 and 11.4;
-    // 512 x 2048 x 14336 39.2, 31.7 and 37.9.  What the rule gets wrong is 129 to 256
-    // rows, whose tiles store a column a lane: 256 x 4096 x 4096 20.6 whole, 23.6 in
-    // two (as chosen), 18.3 on pairs.
+    // 512 x 2048 x 14336 39.2, 31.7 and 37.9.  A residual at 129 to 256 rows, read a
+    // column a lane where shares meet, is what the rule does not see: 256 x 4096 x 4096
+    // 23.5 in two (as chosen), 20.5 whole, 18.1 on pairs; without one 14.3, 16.9, 16.4.
     const int64_t stages = (k * product.bits + 1023) / 1024;
     const int most = nt == 128 ? 4 : 8;
     int split = 1;
